@@ -48,6 +48,14 @@ size_t mx_stage_bytes(int64_t T, int32_t K) {
   return round_up((size_t)T * K) + round_up((size_t)T * (K / 32));
 }
 
+// Scratch of a projection from bf16 x besides kv: MXFP8 staging of x, or the
+// MXFP4 weight expanded to bf16 for the tiled GEMM.
+size_t wkv_scratch_bytes(int64_t T, int64_t K, int64_t N, int32_t w_format) {
+  if (w_format == ENGRAM_W_MXFP8) return mx_stage_bytes(T, (int32_t)K);
+  if (w_format == ENGRAM_W_MXFP4) return round_up((size_t)N * K * 2);
+  return 0;
+}
+
 int check_wkv(const void* x, int64_t T, int32_t K, const void* w,
               const uint8_t* w_scales, int32_t w_format, int32_t N, void* kv) {
   if (T < 0 || K <= 0 || N <= 0) return ENGRAM_EINVAL;
@@ -59,6 +67,9 @@ int check_wkv(const void* x, int64_t T, int32_t K, const void* w,
   } else if (w_format == ENGRAM_W_MXFP8) {
     if (T > 0 && (!w_scales || ((uintptr_t)w_scales & 3u))) return ENGRAM_EINVAL;
     if (K % 128 != 0 || N % 32 != 0) return ENGRAM_EUNSUPPORTED;
+  } else if (w_format == ENGRAM_W_MXFP4) {
+    if (T > 0 && (!w_scales || ((uintptr_t)w_scales & 3u))) return ENGRAM_EINVAL;
+    if (K % 128 != 0 || N % 4 != 0) return ENGRAM_EUNSUPPORTED;
   } else {
     return ENGRAM_EINVAL;
   }
@@ -86,6 +97,10 @@ int run_wkv(const void* x, int64_t T, int32_t K, const void* w,
   if (w_format == ENGRAM_W_BF16)
     return hip_status(!ep.hidden && gemv_bf16_supported(T, K, N) ? launch_gemv_bf16(x, T, K, w, N, kv, s)
                                                                  : launch_gemm_bf16(x, T, K, w, N, kv, s, ep));
+  if (w_format == ENGRAM_W_MXFP4) {
+    if (launch_mxfp4_to_bf16(w, w_scales, N, K, workspace, s) != hipSuccess) return ENGRAM_EHIP;
+    return hip_status(launch_gemm_bf16(x, T, K, workspace, N, kv, s, ep));
+  }
   uint8_t* xq = (uint8_t*)workspace;
   uint8_t* xs = xq + round_up((size_t)T * K);
   hipError_t e = launch_mx_quantize(x, T, K, xq, xs, s);
@@ -99,6 +114,10 @@ int run_wkv_tiled(const void* x, int64_t T, int32_t K, const void* w, const uint
                   int32_t w_format, int32_t N, void* kv, void* workspace, hipStream_t s, const GateEpi& ep) {
   if (T == 0) return ENGRAM_OK;
   if (w_format == ENGRAM_W_BF16) return hip_status(launch_gemm_bf16(x, T, K, w, N, kv, s, ep));
+  if (w_format == ENGRAM_W_MXFP4) {
+    if (launch_mxfp4_to_bf16(w, w_scales, N, K, workspace, s) != hipSuccess) return ENGRAM_EHIP;
+    return hip_status(launch_gemm_bf16(x, T, K, workspace, N, kv, s, ep));
+  }
   uint8_t* xq = (uint8_t*)workspace;
   uint8_t* xs = xq + round_up((size_t)T * K);
   if (launch_mx_quantize(x, T, K, xq, xs, s) != hipSuccess) return ENGRAM_EHIP;
@@ -231,9 +250,8 @@ int engram_mx_quantize(const void* x, int64_t T, int32_t K, uint8_t* xq,
 
 size_t engram_wkv_workspace_size(int64_t T, int32_t K, int32_t N,
                                  int32_t w_format) {
-  (void)N;
-  if (T <= 0 || K <= 0) return 0;
-  return w_format == ENGRAM_W_MXFP8 ? mx_stage_bytes(T, K) : 0;
+  if (T <= 0 || K <= 0 || (N <= 0 && w_format == ENGRAM_W_MXFP4)) return 0;
+  return wkv_scratch_bytes(T, K, N, w_format);
 }
 
 int engram_wkv_gate_partials(const void* x, int64_t T, int32_t K, const void* w,
@@ -269,6 +287,53 @@ int engram_wkv(const void* x, int64_t T, int32_t K, const void* w,
   if (workspace_bytes < need || (need && (!workspace || ((uintptr_t)workspace % kAlign))))
     return ENGRAM_EINVAL;
   return run_wkv(x, T, K, w, w_scales, w_format, N, kv, workspace, (hipStream_t)stream);
+}
+
+size_t engram_wkv_mx_workspace_size(int64_t T, int32_t K, int32_t N, int32_t w_format) {
+  if (T <= 0 || K <= 0 || N <= 0 || w_format != ENGRAM_W_MXFP4) return 0;
+  return round_up((size_t)N * K * 2) + round_up((size_t)T * K * 2);
+}
+
+int engram_wkv_mx(const uint8_t* xq, const uint8_t* xs, int64_t T, int32_t K, const void* w,
+                  const uint8_t* w_scales, int32_t w_format, int32_t N, void* kv, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+  int st = check_wkv(xq, T, K, w, w_scales, w_format, N, kv);
+  if (st != ENGRAM_OK) return st;
+  if (w_format == ENGRAM_W_BF16) return ENGRAM_EUNSUPPORTED;
+  if (T == 0) return ENGRAM_OK;
+  if (!xs || !aligned16(xs)) return ENGRAM_EINVAL;
+  const size_t need = engram_wkv_mx_workspace_size(T, K, N, w_format);
+  if (workspace_bytes < need || (need && (!workspace || ((uintptr_t)workspace % kAlign))))
+    return ENGRAM_EINVAL;
+  hipStream_t s = (hipStream_t)stream;
+  if (w_format == ENGRAM_W_MXFP8)
+    return hip_status(run_mx_projection(xq, xs, T, K, w, w_scales, N, kv, s, kPlainStore));
+  void* wb = workspace;
+  void* xb = (uint8_t*)workspace + round_up((size_t)N * K * 2);
+  if (launch_mxfp4_to_bf16(w, w_scales, N, K, wb, s) != hipSuccess) return ENGRAM_EHIP;
+  if (launch_mxfp8_to_bf16(xq, xs, T, K, xb, s) != hipSuccess) return ENGRAM_EHIP;
+  return hip_status(launch_gemm_bf16(xb, T, K, wb, N, kv, s, kPlainStore));
+}
+
+int engram_add_rms_norm(const void* x, int64_t x_stride_t, int64_t x_stride_h, const void* residual,
+                        int64_t residual_stride_t, int64_t residual_stride_h, const void* weight,
+                        int32_t weight_hc, int64_t T, int32_t hc, int32_t dim, float eps, void* residual_out,
+                        void* out, uint8_t* xq, uint8_t* xs, void* stream) {
+  if (T < 0 || hc <= 0 || dim <= 0 || !(eps >= 0.0f)) return ENGRAM_EINVAL;
+  if (x_stride_t < 0 || x_stride_h < 0 || residual_stride_t < 0 || residual_stride_h < 0) return ENGRAM_EINVAL;
+  if (weight && weight_hc != 1 && weight_hc != hc) return ENGRAM_EINVAL;
+  if ((xq == nullptr) != (xs == nullptr)) return ENGRAM_EINVAL;
+  if (dim % 8 != 0 || dim > 16384 || (xq && dim % 32 != 0)) return ENGRAM_EUNSUPPORTED;
+  if ((x_stride_t | x_stride_h | residual_stride_t | residual_stride_h) & 7) return ENGRAM_EUNSUPPORTED;
+  if (T > INT32_MAX / hc) return ENGRAM_EUNSUPPORTED;
+  if (T == 0) return ENGRAM_OK;
+  if (!x || (!out && !xq)) return ENGRAM_EINVAL;
+  for (const void* p : {x, residual, weight, (const void*)residual_out, (const void*)out, (const void*)xq})
+    if (!aligned16(p)) return ENGRAM_EINVAL;
+  const RmsNormArgs a{(const uint16_t*)x, x_stride_t, x_stride_h, (const uint16_t*)residual,
+                      residual_stride_t, residual_stride_h, (const uint16_t*)weight, weight_hc, T * hc, hc,
+                      dim, eps, (uint16_t*)residual_out, (uint16_t*)out, xq, xs};
+  return hip_status(launch_add_rms_norm(a, (hipStream_t)stream));
 }
 
 int engram_gate_finish(const void* hidden, const void* value, const float* partials,
@@ -309,7 +374,7 @@ size_t engram_forward_workspace_size(const engram_forward_args* a) {
   const int64_t K = (int64_t)a->n_cols * a->head_dim;
   const int64_t N = (int64_t)(a->hc + 1) * a->dim;
   size_t bytes = round_up((size_t)a->T * K * 2) + round_up((size_t)a->T * N * 2);
-  if (a->w_format == ENGRAM_W_MXFP8) bytes += mx_stage_bytes(a->T, (int32_t)K);
+  if (K <= INT32_MAX && N <= INT32_MAX) bytes += wkv_scratch_bytes(a->T, K, N, a->w_format);
   if (K <= INT32_MAX && N <= INT32_MAX && use_decode_path(a, (int32_t)K, (int32_t)N))
     bytes = std::max(bytes, decode_forward_scratch_bytes(a->T, (int)K, (int)N, a->dim));
   return kSyncBytes + bytes;
@@ -358,8 +423,9 @@ static int run_forward(const engram_forward_args* a, int32_t K, int32_t N, uint8
   // turns key tiles into the gate's partial sums and stores only the value:
   // kv's keys never reach HBM. The value and partials take kv's place in the
   // workspace.
-  const bool tiled = a->w_format == ENGRAM_W_BF16 ? !gemv_bf16_supported(a->T, K, N)
-                                                 : !gemv_mxfp8_supported(a->T, K);
+  const bool tiled = a->w_format == ENGRAM_W_BF16    ? !gemv_bf16_supported(a->T, K, N)
+                     : a->w_format == ENGRAM_W_MXFP8 ? !gemv_mxfp8_supported(a->T, K)
+                                                     : true;
   const bool epi = !(a->options & ENGRAM_FORWARD_STORE_KV) && tiled && a->dim % 256 == 0;
   uint16_t* value = (uint16_t*)kv;
   float2* part = (float2*)((uint8_t*)kv + round_up((size_t)a->T * a->dim * 2));

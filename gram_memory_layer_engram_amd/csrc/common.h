@@ -41,6 +41,13 @@ __device__ __forceinline__ uint32_t cvt_pk_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
 }
 
+// Byte B of a word of e2m1 codes (two codes, the lower k in the low nibble)
+// times a power of two -> a pair of bf16 (v_cvt_scalef32_pk_bf16_fp4; exact).
+template <int B>
+__device__ __forceinline__ uint32_t fp4_pair_to_bf16(uint32_t codes, float scale) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, B));
+}
+
 // Device properties the launchers need (cached per device by the ABI layer).
 struct DevInfo {
   int num_cus;
@@ -68,6 +75,25 @@ hipError_t launch_gate_parts(const void* hidden, const void* value, const float2
 
 hipError_t launch_mx_quantize(const void* x, int64_t T, int K, uint8_t* xq,
                               uint8_t* xs, hipStream_t s);
+
+// Residual addition + RMS norm (rms_norm.hip). residual, weight,
+// residual_out, out and (xq, xs) may be null; strides in elements.
+struct RmsNormArgs {
+  const uint16_t* x;
+  int64_t x_st, x_sh;
+  const uint16_t* residual;
+  int64_t r_st, r_sh;
+  const uint16_t* weight;   // [weight_hc, dim]
+  int weight_hc;
+  int64_t rows;             // T * hc
+  int hc, dim;
+  float eps;
+  uint16_t* residual_out;   // [T, hc, dim]
+  uint16_t* out;            // [T, hc, dim]
+  uint8_t* xq;              // [T, hc, dim]
+  uint8_t* xs;              // [T, hc, dim / 32]
+};
+hipError_t launch_add_rms_norm(const RmsNormArgs& a, hipStream_t s);
 
 // Row gather fused with the MXFP8 quantizer (head_dim % 32 == 0); an fp8
 // table when table_scales is not null.
@@ -103,6 +129,11 @@ hipError_t launch_gemm_mxfp8(const uint8_t* xq, const uint8_t* xs, int64_t T,
 hipError_t launch_gemv_mxfp8(const uint8_t* xq, const uint8_t* xs, int64_t T,
                              int K, const uint8_t* w, const uint8_t* ws, int N,
                              void* kv, hipStream_t s);
+
+// MXFP4 weights (e2m1 [N, K/2], E8M0 [N, K/32]) and MXFP8 rows expanded to
+// bf16 (exact); K % 32 == 0.
+hipError_t launch_mxfp4_to_bf16(const void* w, const uint8_t* scales, int64_t N, int K, void* out, hipStream_t s);
+hipError_t launch_mxfp8_to_bf16(const uint8_t* xq, const uint8_t* xs, int64_t T, int K, void* out, hipStream_t s);
 
 // Largest T the decode GEMV serves; above it the tiled GEMM runs.
 constexpr int kGemvMaxT = 64;

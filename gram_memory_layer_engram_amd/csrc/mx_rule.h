@@ -68,5 +68,29 @@ __device__ __forceinline__ int mx_block(const uint32_t* w, uint32_t* packed) {
   return byte;
 }
 
+// The same rule on fp32 values: the 8 elements of one lane out of a 32-element
+// block whose largest magnitude has the bits `amax` -> 2 code words; returns
+// the block's scale byte. floor(log2(amax)) + 127 is amax's exponent field
+// (a subnormal amax is far below the byte range and gets byte 0 as well).
+// The codes come from v_cvt_pk_fp8_f32 (OCP e4m3fn, nearest-even, sign
+// kept); it does not saturate, so values are clamped to +-448 first.
+__device__ __forceinline__ int mx_piece_f32(const float* v, uint32_t amax, uint32_t* packed) {
+  if (amax >= 0x7f800000u) {
+    packed[0] = packed[1] = 0x7f7f7f7fu;
+    return 255;
+  }
+  const int byte = max((int)(amax >> 23) - 8, 0);
+  const float inv_scale = __uint_as_float((uint32_t)(254 - byte) << 23);   // 2^(127 - byte)
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[j] = __builtin_amdgcn_fmed3f(v[4 * i + j] * inv_scale, -448.f, 448.f);
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], w, true);
+    packed[i] = (uint32_t)w;
+  }
+  return byte;
+}
 
 }  // namespace engram

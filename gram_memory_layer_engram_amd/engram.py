@@ -18,7 +18,7 @@ LIB_PATH = os.path.join(_HERE, "libengram.so")
 
 ENGRAM_OK, ENGRAM_EINVAL, ENGRAM_EUNSUPPORTED, ENGRAM_EHIP, ENGRAM_ENOSPACE = 0, 1, 2, 3, 4
 NOALLOC_SCRATCH_BYTES = 32 << 20
-W_BF16, W_MXFP8 = 0, 1
+W_BF16, W_MXFP8, W_MXFP4 = 0, 1, 2
 FORWARD_STORE_KV = 1
 
 _vp = ctypes.c_void_p
@@ -56,6 +56,10 @@ EXPORTS = {
     "engram_wkv": (_i32, [_vp, _i64, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _sz, _vp]),
     "engram_wkv_gate_partials": (_i32, [_vp, _i64, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp,
                                         _vp, _sz, _vp]),
+    "engram_wkv_mx_workspace_size": (_sz, [_i64, _i32, _i32, _i32]),
+    "engram_wkv_mx": (_i32, [_vp, _vp, _i64, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _sz, _vp]),
+    "engram_add_rms_norm": (_i32, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i32, _i64, _i32, _i32, _f32, _vp, _vp,
+                                   _vp, _vp, _vp]),
     "engram_gate": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _f32, _f32, _vp, _vp, _vp]),
     "engram_gate_finish": (_i32, [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _f32, _f32, _vp, _vp, _vp]),
     "engram_forward_workspace_size": (_sz, [ctypes.POINTER(ForwardArgs)]),
@@ -162,6 +166,45 @@ def _stream() -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+def _format(w: torch.Tensor, w_scales, K: int) -> int:
+    """The wkv weight format by its tensors: bf16 [N, K] without scales,
+    MXFP8 codes [N, K], or MXFP4 codes [N, K/2]."""
+    if w_scales is None:
+        return W_BF16
+    return W_MXFP4 if w.dim() == 2 and 2 * w.shape[1] == K else W_MXFP8
+
+
+def _check_mxfp4(w: torch.Tensor, w_scales: torch.Tensor, N: int, K: int) -> None:
+    _dense(w_scales, "w_scales")
+    if w.dtype != torch.uint8 or w_scales.dtype != torch.uint8 or tuple(w_scales.shape) != (N, K // 32):
+        raise ValueError("MXFP4 wkv needs uint8 codes [N, K/2] and uint8 scales [N, K/32]")
+
+
+def _device_of(*tensors) -> torch.device:
+    """The one device all given tensors (None left out) are on; the call is
+    made with it current, on its current stream."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("libengram takes device tensors only")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}: one device is needed")
+    return dev
+
+
+def _run_on(dev: torch.device, fn, *args) -> None:
+    """fn(*args, stream) with dev current, on dev's current stream."""
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream().cuda_stream))
+        return
+    with torch.cuda.device(dev):
+        _check(fn(*args, torch.cuda.current_stream().cuda_stream))
+
+
 def lookup(table, hash_ids: torch.Tensor, rows_out: torch.Tensor | None = None,
            err_flag: torch.Tensor | None = None, background: bool = False) -> torch.Tensor:
     """rows[t, c, :] = table[hash_ids[t, c], :] (hash_ids may be strided).
@@ -222,20 +265,26 @@ def mx_quantize(x: torch.Tensor, xq: torch.Tensor | None = None, xs: torch.Tenso
 
 def wkv(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor | None = None,
         kv: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
-    """kv = bf16(x . W^T); MXFP8 when ``w_scales`` is given (w = uint8 codes)."""
+    """kv = bf16(x . W^T). ``w_scales`` given: MXFP8 (w = uint8 codes [N, K],
+    scales [N/32, K/32]) or MXFP4 (w = uint8 packed codes [N, K/2], scales
+    [N, K/32]), told apart by w's shape."""
     L = load_library()
     _dense(x, "x")
     _dense(w, "w")
     T, K = x.shape
     N = w.shape[0]
-    fmt = W_BF16 if w_scales is None else W_MXFP8
-    if w.dim() != 2 or w.shape[1] != K:
+    fmt = _format(w, w_scales, K)
+    if fmt == W_MXFP4:
+        _check_mxfp4(w, w_scales, N, K)
+        if x.dtype != torch.bfloat16:
+            raise ValueError("MXFP4 wkv needs bf16 x (wkv_mx takes MXFP8 activations)")
+    elif w.dim() != 2 or w.shape[1] != K:
         raise ValueError(f"w must be [N, {K}], got {tuple(w.shape)}")
     if fmt == W_MXFP8:
         _dense(w_scales, "w_scales")
         if w.dtype != torch.uint8 or tuple(w_scales.shape) != (N // 32, K // 32):
             raise ValueError("MXFP8 wkv needs uint8 codes [N, K] and scales [N/32, K/32]")
-    elif w.dtype != torch.bfloat16 or x.dtype != torch.bfloat16:
+    elif fmt == W_BF16 and (w.dtype != torch.bfloat16 or x.dtype != torch.bfloat16):
         raise ValueError("bf16 wkv needs bf16 x and w")
     if kv is None:
         kv = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
@@ -246,6 +295,108 @@ def wkv(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor | None = None,
     _check(L.engram_wkv(_ptr(x), T, K, _ptr(w), _ptr(w_scales), fmt, N, _ptr(kv),
                         _ptr(workspace), ws_bytes, _stream()))
     return kv
+
+
+def wkv_mx(xq: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+           kv: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """kv = bf16(deq(xq, xs) . deq(W)^T): the projection from MXFP8 activations
+    (uint8 codes [T, K], E8M0 bytes [T, K/32], as mx_quantize or add_rms_norm
+    give them), W in MXFP8 or MXFP4 as in ``wkv``."""
+    L = load_library()
+    dev = _device_of(xq, xs, w, w_scales, kv, workspace)
+    for t, n in ((xq, "xq"), (xs, "xs"), (w, "w"), (w_scales, "w_scales")):
+        _dense(t, n)
+        if t.dtype != torch.uint8 or t.dim() != 2:
+            raise ValueError(f"{n} must be a uint8 matrix")
+    T, K = xq.shape
+    N = w.shape[0]
+    if tuple(xs.shape) != (T, K // 32):
+        raise ValueError(f"xs must be [{T}, {K // 32}], got {tuple(xs.shape)}")
+    fmt = _format(w, w_scales, K)
+    if fmt == W_MXFP4:
+        _check_mxfp4(w, w_scales, N, K)
+    elif tuple(w.shape) != (N, K) or tuple(w_scales.shape) != (N // 32, K // 32):
+        raise ValueError(f"w must be [N, {K}] with scales [N/32, K/32] (MXFP8) or [N, {K // 2}] with [N, K/32] (MXFP4)")
+    if kv is None:
+        kv = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+    elif tuple(kv.shape) != (T, N) or kv.dtype != torch.bfloat16:
+        raise ValueError(f"kv must be bf16 [{T}, {N}]")
+    _dense(kv, "kv")
+    need = L.engram_wkv_mx_workspace_size(T, K, N, fmt)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _run_on(dev, L.engram_wkv_mx, xq.data_ptr(), xs.data_ptr(), T, K, w.data_ptr(), w_scales.data_ptr(), fmt, N,
+            kv.data_ptr(), None if workspace is None else workspace.data_ptr(), ws_bytes)
+    return kv
+
+
+def add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None = None, weight: torch.Tensor | None = None,
+                 eps: float = 1e-6, out_format: str = "bf16", residual_out: torch.Tensor | None = None,
+                 out: torch.Tensor | None = None, xq: torch.Tensor | None = None,
+                 xs: torch.Tensor | None = None):
+    """s = x + residual; y = s / sqrt(mean(s^2) + eps) * weight. Returns
+    (residual_out = bf16(s), out = bf16(y), xq, xs = y in MXFP8), None for what
+    is not asked for: ``out_format`` is "bf16", "mxfp8" or "both", and
+    residual_out comes with a residual.
+
+    x and residual: bf16 [T, hc, dim] (or [T, dim]), last dimension contiguous,
+    other strides free (a slice of a wider tensor, or an expanded copy
+    dimension). weight: bf16 [dim], or [hc, dim] with one row per copy. The
+    outputs may be given (contiguous); residual_out may be residual itself and
+    out may be x itself."""
+    L = load_library()
+    if x.dim() not in (2, 3):
+        raise ValueError("x must be [T, hc, dim] or [T, dim]")
+    dev = _device_of(x, residual, weight, residual_out, out, xq, xs)
+    shape = tuple(x.shape)
+    T, hc, dim = shape if x.dim() == 3 else (shape[0], 1, shape[1])
+    if out_format not in ("bf16", "mxfp8", "both"):
+        raise ValueError('out_format must be "bf16", "mxfp8" or "both"')
+    for t, n in ((x, "x"), (residual, "residual")):
+        if t is None:
+            continue
+        if t.dtype != torch.bfloat16 or tuple(t.shape) != shape:
+            raise ValueError(f"{n} must be bf16 {shape}")
+        if dim > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{n} must be contiguous in its last dimension")
+    whc = 1
+    if weight is not None:
+        _dense(weight, "weight")
+        if weight.dtype != torch.bfloat16 or tuple(weight.shape) not in ((dim,), (hc, dim), (1, dim)):
+            raise ValueError(f"weight must be bf16 [{dim}] or [{hc}, {dim}]")
+        whc = weight.shape[0] if weight.dim() == 2 else 1
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    if out_format == "mxfp8":
+        if out is not None:
+            raise ValueError('out is not written with out_format "mxfp8"')
+    elif out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    if out_format == "bf16":
+        if xq is not None or xs is not None:
+            raise ValueError('xq and xs are not written with out_format "bf16"')
+    else:
+        if xq is None:
+            xq = torch.empty(shape, dtype=torch.uint8, device=dev)
+        if xs is None:
+            xs = torch.empty(shape[:-1] + (dim // 32,), dtype=torch.uint8, device=dev)
+    for t, n, dt, sh in ((residual_out, "residual_out", torch.bfloat16, shape), (out, "out", torch.bfloat16, shape),
+                         (xq, "xq", torch.uint8, shape), (xs, "xs", torch.uint8, shape[:-1] + (dim // 32,))):
+        if t is None:
+            continue
+        _dense(t, n)
+        if t.dtype != dt or tuple(t.shape) != sh:
+            raise ValueError(f"{n} must be {dt} {sh}")
+    three = x.dim() == 3
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    # the stride of a dimension of one element is never used, whatever torch says it is
+    st = lambda t: (0, 0) if t is None else (t.stride(0) if T > 1 else 0, t.stride(1) if three and hc > 1 else 0)  # noqa: E731
+    _run_on(dev, L.engram_add_rms_norm, p(x), *st(x), p(residual), *st(residual), p(weight), whc, T, hc, dim, eps,
+            p(residual_out), p(out), p(xq), p(xs))
+    return residual_out, out, xq, xs
 
 
 def wkv_gate_partials(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor | None,
@@ -261,9 +412,11 @@ def wkv_gate_partials(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor |
     T, K = x.shape
     _, hc, dim = hidden.shape
     N = (hc + 1) * dim
-    fmt = W_BF16 if w_scales is None else W_MXFP8
-    if tuple(w.shape) != (N, K):
-        raise ValueError(f"w must be [{N}, {K}], got {tuple(w.shape)}")
+    fmt = _format(w, w_scales, K)
+    if tuple(w.shape) != (N, K // 2 if fmt == W_MXFP4 else K):
+        raise ValueError(f"w must be [{N}, {K}] (MXFP4: [{N}, {K // 2}]), got {tuple(w.shape)}")
+    if fmt == W_MXFP4:
+        _check_mxfp4(w, w_scales, N, K)
     if fmt == W_MXFP8:
         _dense(w_scales, "w_scales")
     if value is None:
@@ -328,7 +481,10 @@ def forward_args(table, hash_ids, w, w_scales, hidden, q_weight, k_weight, token
     a.hash_ids = _ptr(hash_ids)
     a.ids_stride_t = hash_ids.stride(0); a.ids_stride_c = hash_ids.stride(1)
     a.w = _ptr(w); a.w_scales = _ptr(w_scales)
-    a.w_format = W_BF16 if w_scales is None else W_MXFP8
+    K = hash_ids.shape[1] * table.shape[1]
+    a.w_format = _format(w, w_scales, K)
+    if a.w_format == W_MXFP4:
+        _check_mxfp4(w, w_scales, (hc + 1) * dim, K)
     a.hidden = _ptr(hidden); a.q_weight = _ptr(q_weight); a.k_weight = _ptr(k_weight)
     a.token_mask = _ptr(token_mask)
     a.T = T; a.hc = hc; a.dim = dim

@@ -49,7 +49,11 @@ enum {
 /* wkv weight formats. */
 enum {
   ENGRAM_W_BF16 = 0,  /* W bf16 [N, K] row-major */
-  ENGRAM_W_MXFP8 = 1  /* W e4m3fn codes [N, K] row-major + E8M0 bytes [N/32, K/32] */
+  ENGRAM_W_MXFP8 = 1, /* W e4m3fn codes [N, K] row-major + E8M0 bytes [N/32, K/32] */
+  ENGRAM_W_MXFP4 = 2  /* W e2m1 codes [N, K/2] row-major, two per byte (the lower k in
+                         the low nibble) + E8M0 bytes [N, K/32], one per row and 32 k:
+                         OCP MX v1.0 MXFP4; W[n,k] = e2m1(code) * 2^(byte - 127),
+                         byte 255 is NaN */
 };
 
 /* Version of this ABI (ENGRAM_ABI_VERSION). */
@@ -169,15 +173,22 @@ int engram_mx_quantize(const void* x, int64_t T, int32_t K, uint8_t* xq,
  *   E8M0 scales per 32x32 block [N/32, K/32].
  *
  *   x          bf16 [T, K] (the staged rows [T, C, head_dim] viewed flat).
- *   w          bf16 [N, K] (ENGRAM_W_BF16) or uint8 codes [N, K] (ENGRAM_W_MXFP8).
- *   w_scales   uint8 [N/32, K/32] for MXFP8, NULL for bf16.
+ *   w          bf16 [N, K] (ENGRAM_W_BF16), uint8 codes [N, K] (ENGRAM_W_MXFP8)
+ *              or packed codes [N, K/2] (ENGRAM_W_MXFP4).
+ *   w_scales   uint8 [N/32, K/32] for MXFP8, [N, K/32] for MXFP4 (4-byte
+ *              aligned), NULL for bf16.
  *   kv         bf16 [T, N].
  *   workspace  device scratch of at least engram_wkv_workspace_size() bytes
  *              (NULL allowed when that size is 0). For MXFP8 it holds x's
- *              MXFP8 codes and scales. 256-byte aligned.
+ *              MXFP8 codes and scales; for MXFP4 the weight expanded to bf16
+ *              (exact) for the tiled GEMM. 256-byte aligned.
+ *   With MXFP4 weights x stays bf16 and W enters as its bf16 values, which
+ *   are exact (a value of 2^128 or more, scale bytes 253 and 254 only, is an
+ *   infinity); engram_wkv_mx takes 8-bit activations.
  *   Shapes: bf16 needs K % 8 == 0 and N % 4 == 0; MXFP8 needs K % 128 == 0
- *   and N % 32 == 0; both need K <= 2^20 (32-bit buffer offsets). Other
- *   shapes return ENGRAM_EUNSUPPORTED.
+ *   and N % 32 == 0; MXFP4 needs K % 128 == 0 and N % 4 == 0; all need
+ *   K <= 2^20 (32-bit buffer offsets). Other shapes return
+ *   ENGRAM_EUNSUPPORTED.
  *   Kernels: a tiled GEMM; for T <= 64 a weight-streaming GEMV instead
  *   (MXFP8 with K/128 <= 32; bf16 with K % 32 == 0, K <= 2048, N % 16 == 0
  *   where it beats the GEMM). The two sum in different fp32 orders, so
@@ -188,6 +199,64 @@ size_t engram_wkv_workspace_size(int64_t T, int32_t K, int32_t N,
 int engram_wkv(const void* x, int64_t T, int32_t K, const void* w,
                const uint8_t* w_scales, int32_t w_format, int32_t N, void* kv,
                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * engram_wkv_mx -- the projection from activations that are MXFP8 already,
+ *   the 8-bit output of engram_add_rms_norm or engram_mx_quantize:
+ *   kv = bf16(deq(xq, xs) . deq(W)^T), fp32 accumulation.
+ *   [P-gemv] module docstring: the GEMV takes the tokens' MXFP8 rows.
+ *   With ENGRAM_W_MXFP8 it is engram_wkv without its quantize step, bit for
+ *   bit.
+ *
+ *   xq          uint8 e4m3fn codes [T, K];  xs  uint8 E8M0 [T, K/32]; both
+ *               16-byte aligned.
+ *   w, w_scales, w_format   ENGRAM_W_MXFP8 or ENGRAM_W_MXFP4 as engram_wkv;
+ *               ENGRAM_W_BF16 returns ENGRAM_EUNSUPPORTED.
+ *   kv          bf16 [T, N].
+ *   workspace   engram_wkv_mx_workspace_size() bytes, 256-byte aligned (NULL
+ *               allowed when that size is 0).
+ *   Shapes and errors: as engram_wkv for the format.
+ */
+size_t engram_wkv_mx_workspace_size(int64_t T, int32_t K, int32_t N, int32_t w_format);
+int engram_wkv_mx(const uint8_t* xq, const uint8_t* xs, int64_t T, int32_t K, const void* w,
+                  const uint8_t* w_scales, int32_t w_format, int32_t N, void* kv, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/*
+ * engram_add_rms_norm -- residual addition and root-mean-square norm of the
+ *   streams, with the output in bf16, in MXFP8, or both in one pass.
+ *   [P-common] Engram.__init__ / forward: streams [T, hc_mult, dim] and
+ *   rms_norm_eps. For every row (t, h):
+ *     s   = x[t,h,:] + residual[t,h,:]          (fp32; x alone without residual)
+ *     y   = s / sqrt(sum(s^2)/dim + eps) * weight[h,:]
+ *     residual_out[t,h,:] = bf16(s)
+ *     out[t,h,:]          = bf16(y)
+ *     xq, xs              = the MXFP8 codes and scale bytes of y by the rule of
+ *                           engram_mx_quantize, taken on the fp32 y (one
+ *                           rounding; a non-finite 32-element block gets byte
+ *                           255 and codes 0x7F)
+ *   The norm is taken of the unrounded sum s. Sums in fp32, fixed order (an
+ *   |s| past about 1e18 overflows its square).
+ *
+ *   x, residual   bf16, element (t, h, d) at t*stride_t + h*stride_h + d
+ *                 (strides in elements, multiples of 8, >= 0: slices of wider
+ *                 tensors, or stride_h = 0 to add one row to every copy).
+ *                 residual may be NULL.
+ *   weight        bf16 [weight_hc, dim], weight_hc 1 (shared) or hc; NULL: ones.
+ *   residual_out  optional bf16 [T, hc, dim] contiguous; may be `residual`
+ *                 itself (in place) when that is contiguous.
+ *   out           optional bf16 [T, hc, dim] contiguous; may be `x` itself
+ *                 when that is contiguous. No other overlap is allowed.
+ *   xq, xs        optional, both or neither: uint8 [T, hc, dim] and
+ *                 [T, hc, dim/32]. At least one of out and xq.
+ *   eps           >= 0 (a row of zeros with eps 0 gives NaN).
+ *   Shapes: dim % 8 == 0 (dim % 32 == 0 with xq), dim <= 16384, T*hc < 2^31;
+ *   else ENGRAM_EUNSUPPORTED. All pointers but xs 16-byte aligned.
+ */
+int engram_add_rms_norm(const void* x, int64_t x_stride_t, int64_t x_stride_h, const void* residual,
+                        int64_t residual_stride_t, int64_t residual_stride_h, const void* weight,
+                        int32_t weight_hc, int64_t T, int32_t hc, int32_t dim, float eps, void* residual_out,
+                        void* out, uint8_t* xq, uint8_t* xs, void* stream);
 
 /*
  * engram_wkv_gate_partials -- the projection fused with the gate's kv-side
@@ -294,7 +363,7 @@ typedef struct engram_forward_args {
   int64_t ids_stride_t;
   int64_t ids_stride_c;
   const void* w;           /* wkv weight, see engram_wkv */
-  const uint8_t* w_scales; /* MXFP8 only */
+  const uint8_t* w_scales; /* MXFP8 and MXFP4 */
   int32_t w_format;
   const void* hidden;      /* bf16 [T, hc, dim] */
   const void* q_weight;    /* bf16 [hc, dim] */

@@ -221,6 +221,41 @@ def mx_dequantize_weight(w_codes, w_scales):
     return e4m3fn_decode(w_codes) * s_full
 
 
+def e2m1_decode(nibbles):
+    """e2m1 codes 0..15 -> float64 (OCP MX v1.0 FP4: sign, 2 exponent bits of
+    bias 1, 1 fraction bit): 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives."""
+    c = np.asarray(nibbles).astype(np.int64)
+    e, m = (c >> 1) & 3, (c & 1).astype(np.float64)
+    mag = np.where(e == 0, 0.5 * m, np.ldexp(1.0 + 0.5 * m, e - 1))
+    return np.where(c & 8, -mag, mag)
+
+
+def mxfp4_dequantize_weight(w_codes, w_scales):
+    """MXFP4 weight -> float64 ``[N, K]``: packed e2m1 codes ``[N, K/2]`` (the
+    lower k in the low nibble) and E8M0 bytes ``[N, K/32]``, one per row and
+    32 k (OCP MX v1.0); element (n, k) is scaled by 2**(S[n, k//32] - 127)."""
+    N, half = w_codes.shape
+    K = 2 * half
+    assert w_scales.shape == (N, K // MX_BLOCK)
+    codes = np.empty((N, K), dtype=np.uint8)
+    codes[:, 0::2] = w_codes & 15
+    codes[:, 1::2] = w_codes >> 4
+    return e2m1_decode(codes) * np.repeat(e8m0_decode(w_scales), MX_BLOCK, axis=1)
+
+
+def add_rms_norm(x_bits, residual_bits, weight_bits, eps):
+    """The residual addition and RMS norm of streams ``[T, hc, dim]``, in fp64:
+    returns (s, y) with s = x + residual (x alone for None) and
+    y = s / sqrt(mean(s^2) + eps) * weight (``[dim]``, ``[hc, dim]`` or None)."""
+    s = bf16_to_f64(x_bits)
+    if residual_bits is not None:
+        s = s + bf16_to_f64(residual_bits)
+    y = s / np.sqrt(np.mean(s * s, axis=-1, keepdims=True) + eps)
+    if weight_bits is not None:
+        y = y * bf16_to_f64(weight_bits)
+    return s, y
+
+
 # ---------------------------------------------------------------------------
 # Step 1: row gather
 # ---------------------------------------------------------------------------
@@ -306,11 +341,15 @@ def wkv(x_bits, w, w_scales=None):
     ``w`` is bf16 bits ``[N, K]`` when ``w_scales`` is None, else e4m3fn codes
     with ``w_scales`` E8M0 bytes ``[N/32, K/32]``; then ``x`` is first
     quantized to MXFP8 (``mx_quantize``) and both operands enter the product
-    at their dequantized values.
+    at their dequantized values. ``w`` of half as many columns as x is MXFP4
+    (``mxfp4_dequantize_weight``); x then stays bf16.
     """
     if w_scales is None:
         xa = bf16_to_f64(x_bits)
         wa = bf16_to_f64(w)
+    elif 2 * w.shape[1] == x_bits.shape[1]:
+        xa = bf16_to_f64(x_bits)
+        wa = mxfp4_dequantize_weight(w, w_scales)
     else:
         codes, sbytes = mx_quantize(x_bits)
         xa = mx_dequantize_activations(codes, sbytes)
