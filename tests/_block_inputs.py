@@ -29,13 +29,22 @@ def bf16(rng, *shape, scale=1.0):
     return torch.from_numpy(rng.standard_normal(shape).astype(np.float32) * scale).to(torch.bfloat16)
 
 
-def product_tolerance(xa, wa):
-    """Elementwise bound of bf16(fp32 sums of xa . wa^T) against the exact
-    product: K - 1 fp32 additions and the (exact) products' sums, each
-    addition off by at most one fp32 step of the running magnitude (2 * F32_U:
-    the matrix cores may truncate inside an instruction), then half a bf16
-    step of the result, or of the smallest bf16 normal below it."""
+def product_tolerance(xa, wa, scaled=False):
+    """The exact product xa . wa^T and an elementwise bound of its bf16 result
+    with fp32 sums: K - 1 fp32 additions, each off by at most one fp32 step of
+    the running magnitude (2 * F32_U: the matrix cores may cut instead of
+    rounding), then half a bf16 step of the result.
+
+    ``scaled``: MXFP8 activations, on the scaled 8-bit / 4-bit matrix
+    instructions. They add the 8 products of a run of 8 consecutive k in a
+    window of 14 bits below the run's largest product (measured: of two
+    products in one run the smaller vanishes from a ratio of 2^14 on; in
+    different runs both count to fp32's last bit), so each of the 7 others
+    loses less than 2^-13 of the largest: 7 * 2^-13 * max|x| * max|w| per run
+    at most."""
     ref = xa @ wa.T
-    mass = np.abs(xa) @ np.abs(wa).T
-    acc = 2 * F32_U * xa.shape[1] * mass
+    acc = 2 * F32_U * xa.shape[1] * (np.abs(xa) @ np.abs(wa).T)
+    if scaled:
+        runs = [np.abs(a).reshape(a.shape[0], -1, 8).max(axis=2) for a in (xa, wa)]
+        acc = acc + 7 * 2.0 ** -13 * (runs[0] @ runs[1].T)
     return ref, acc + BF16_U * (np.abs(ref) + acc) + 2.0 ** -134

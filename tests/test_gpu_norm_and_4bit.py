@@ -224,7 +224,7 @@ def test_mxfp4_products(T, K, N):
     xq, xs = mxfp8_rows(rng, T, K)
     guard.fill_(55)
     E.wkv_mx(torch.from_numpy(xq).to(DEV), torch.from_numpy(xs).to(DEV), wd, sd, kv=kv)
-    ref, tol = product_tolerance(o.mx_dequantize_activations(xq, xs), wa)
+    ref, tol = product_tolerance(o.mx_dequantize_activations(xq, xs), wa, scaled=True)
     _inside(bf16_values(bits(kv)), ref, tol, "wkv_mx mxfp4")
     assert bool((guard[T * N:] == 55).all())
 
@@ -381,7 +381,7 @@ def test_a_layer_then_norm_then_projection():
         rows = xq.view(T * hc, dim), xs.view(T * hc, dim // 32)
         for w, s, wa in ((w2, s2, o.mxfp4_dequantize_weight(w2, s2)), (w8, s8, o.mx_dequantize_weight(w8, s8))):
             kv = E.wkv_mx(*rows, dev(w), dev(s))
-            ref, tol = product_tolerance(o.mx_dequantize_activations(u8(rows[0]), u8(rows[1])), wa)
+            ref, tol = product_tolerance(o.mx_dequantize_activations(u8(rows[0]), u8(rows[1])), wa, scaled=True)
             _inside(bf16_values(bits(kv)), ref, tol, "projection")
         sref, yref = _norm_ref(branch[:, None].expand(T, hc, dim), stream, wn, 1e-6)
         _check_norm(dim, sref, yref, res, None, xq, xs)
