@@ -52,7 +52,8 @@ size_t mx_stage_bytes(int64_t T, int32_t K) {
 // MXFP4 weight expanded to bf16 for the tiled GEMM.
 size_t wkv_scratch_bytes(int64_t T, int64_t K, int64_t N, int32_t w_format) {
   if (w_format == ENGRAM_W_MXFP8) return mx_stage_bytes(T, (int32_t)K);
-  if (w_format == ENGRAM_W_MXFP4) return T > kGemvMaxT ? round_up((size_t)N * K * 2) : 0;
+  if (w_format == ENGRAM_W_MXFP4)
+    return gemv_mxfp4_supported(T, (int)K, false) ? 0 : round_up((size_t)N * K * 2);
   return 0;
 }
 
@@ -98,7 +99,7 @@ int run_wkv(const void* x, int64_t T, int32_t K, const void* w,
     return hip_status(!ep.hidden && gemv_bf16_supported(T, K, N) ? launch_gemv_bf16(x, T, K, w, N, kv, s)
                                                                  : launch_gemm_bf16(x, T, K, w, N, kv, s, ep));
   if (w_format == ENGRAM_W_MXFP4) {
-    if (T <= kGemvMaxT)
+    if (!ep.hidden && gemv_mxfp4_supported(T, K, false))
       return hip_status(launch_gemv_mxfp4(x, nullptr, T, K, w, w_scales, N, kv, s));
     if (launch_mxfp4_to_bf16(w, w_scales, N, K, workspace, s) != hipSuccess) return ENGRAM_EHIP;
     return hip_status(launch_gemm_bf16(x, T, K, workspace, N, kv, s, ep));
@@ -272,7 +273,7 @@ int engram_wkv_gate_partials(const void* x, int64_t T, int32_t K, const void* w,
   if (st != ENGRAM_OK) return st;
   if (T == 0) return ENGRAM_OK;
   if (!partials || ((uintptr_t)partials & 7u)) return ENGRAM_EINVAL;
-  if (w_format == ENGRAM_W_MXFP4 && T <= kGemvMaxT) return ENGRAM_EUNSUPPORTED;
+  if (w_format == ENGRAM_W_MXFP4 && gemv_mxfp4_supported(T, K, false)) return ENGRAM_EUNSUPPORTED;
   const size_t need = engram_wkv_workspace_size(T, K, N, w_format);
   if (workspace_bytes < need || (need && (!workspace || ((uintptr_t)workspace % kAlign))))
     return ENGRAM_EINVAL;
@@ -293,7 +294,7 @@ int engram_wkv(const void* x, int64_t T, int32_t K, const void* w,
 }
 
 size_t engram_wkv_mx_workspace_size(int64_t T, int32_t K, int32_t N, int32_t w_format) {
-  if (T <= kGemvMaxT || K <= 0 || N <= 0 || w_format != ENGRAM_W_MXFP4) return 0;
+  if (T <= 0 || K <= 0 || N <= 0 || w_format != ENGRAM_W_MXFP4 || gemv_mxfp4_supported(T, K, true)) return 0;
   return round_up((size_t)N * K * 2) + round_up((size_t)T * K * 2);
 }
 
@@ -311,7 +312,7 @@ int engram_wkv_mx(const uint8_t* xq, const uint8_t* xs, int64_t T, int32_t K, co
   hipStream_t s = (hipStream_t)stream;
   if (w_format == ENGRAM_W_MXFP8)
     return hip_status(run_mx_projection(xq, xs, T, K, w, w_scales, N, kv, s, kPlainStore));
-  if (T <= kGemvMaxT) return hip_status(launch_gemv_mxfp4(xq, xs, T, K, w, w_scales, N, kv, s));
+  if (gemv_mxfp4_supported(T, K, true)) return hip_status(launch_gemv_mxfp4(xq, xs, T, K, w, w_scales, N, kv, s));
   void* wb = workspace;
   void* xb = (uint8_t*)workspace + round_up((size_t)N * K * 2);
   if (launch_mxfp4_to_bf16(w, w_scales, N, K, wb, s) != hipSuccess) return ENGRAM_EHIP;
@@ -429,7 +430,7 @@ static int run_forward(const engram_forward_args* a, int32_t K, int32_t N, uint8
   // workspace.
   const bool tiled = a->w_format == ENGRAM_W_BF16    ? !gemv_bf16_supported(a->T, K, N)
                      : a->w_format == ENGRAM_W_MXFP8 ? !gemv_mxfp8_supported(a->T, K)
-                                                     : a->T > kGemvMaxT;
+                                                     : !gemv_mxfp4_supported(a->T, K, false);
   const bool epi = !(a->options & ENGRAM_FORWARD_STORE_KV) && tiled && a->dim % 256 == 0;
   uint16_t* value = (uint16_t*)kv;
   float2* part = (float2*)((uint8_t*)kv + round_up((size_t)a->T * a->dim * 2));

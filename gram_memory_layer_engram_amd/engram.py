@@ -176,33 +176,37 @@ def _format(w: torch.Tensor, w_scales, K: int) -> int:
 
 def _check_mxfp4(w: torch.Tensor, w_scales: torch.Tensor, N: int, K: int) -> None:
     _dense(w_scales, "w_scales")
-    if w.dtype != torch.uint8 or w_scales.dtype != torch.uint8 or tuple(w_scales.shape) != (N, K // 32):
+    if w.dtype != torch.uint8 or w_scales.dtype != torch.uint8 or w_scales.shape != (N, K // 32):
         raise ValueError("MXFP4 wkv needs uint8 codes [N, K/2] and uint8 scales [N, K/32]")
 
 
-def _device_of(*tensors) -> torch.device:
-    """The one device all given tensors (None left out) are on; the call is
-    made with it current, on its current stream."""
+def _device_of(*tensors) -> int:
+    """The one device (its index) all given tensors are on, None left out."""
     dev = None
     for t in tensors:
         if t is None:
             continue
         if not t.is_cuda:
             raise ValueError("libengram takes device tensors only")
+        i = t.get_device()
         if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}: one device is needed")
+            dev = i
+        elif i != dev:
+            raise ValueError(f"tensors on cuda:{dev} and cuda:{i}: one device is needed")
     return dev
 
 
-def _run_on(dev: torch.device, fn, *args) -> None:
-    """fn(*args, stream) with dev current, on dev's current stream."""
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, torch.cuda.current_stream().cuda_stream))
-        return
-    with torch.cuda.device(dev):
-        _check(fn(*args, torch.cuda.current_stream().cuda_stream))
+def _run_on(dev: int, fn, *args) -> None:
+    """fn(*args, stream) with device dev current, on its current stream. (The
+    raw stream number: a Stream object costs a microsecond, a fifth of a decode
+    kernel.)"""
+    if dev == torch.cuda.current_device():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        _check(status)
 
 
 def lookup(table, hash_ids: torch.Tensor, rows_out: torch.Tensor | None = None,
@@ -278,7 +282,8 @@ def wkv(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor | None = None,
         _check_mxfp4(w, w_scales, N, K)
         if x.dtype != torch.bfloat16:
             raise ValueError("MXFP4 wkv needs bf16 x (wkv_mx takes MXFP8 activations)")
-    elif w.dim() != 2 or w.shape[1] != K:
+        return _product(L, L.engram_wkv, L.engram_wkv_workspace_size, (x,), T, K, w, w_scales, fmt, N, kv, workspace)
+    if w.dim() != 2 or w.shape[1] != K:
         raise ValueError(f"w must be [N, {K}], got {tuple(w.shape)}")
     if fmt == W_MXFP8:
         _dense(w_scales, "w_scales")
@@ -297,38 +302,48 @@ def wkv(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor | None = None,
     return kv
 
 
+def _product(L, fn, workspace_size, x, T, K, w, w_scales, fmt, N, kv, workspace):
+    """Output, workspace and call of a projection whose operands are checked;
+    x is (x,) or (codes, scales)."""
+    dev = _device_of(*x, w, w_scales, kv, workspace)
+    if kv is None:
+        kv = torch.empty((T, N), dtype=torch.bfloat16, device=w.device)
+    elif kv.shape != (T, N) or kv.dtype != torch.bfloat16 or not kv.is_contiguous():
+        raise ValueError(f"kv must be bf16 [{T}, {N}], contiguous")
+    need = workspace_size(T, K, N, fmt)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=w.device)
+    if workspace is None:
+        ws, ws_bytes = None, 0
+    else:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _run_on(dev, fn, *[t.data_ptr() for t in x], T, K, w.data_ptr(), w_scales.data_ptr(), fmt, N, kv.data_ptr(), ws,
+            ws_bytes)
+    return kv
+
+
 def wkv_mx(xq: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
            kv: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """kv = bf16(deq(xq, xs) . deq(W)^T): the projection from MXFP8 activations
     (uint8 codes [T, K], E8M0 bytes [T, K/32], as mx_quantize or add_rms_norm
     give them), W in MXFP8 or MXFP4 as in ``wkv``."""
     L = load_library()
-    dev = _device_of(xq, xs, w, w_scales, kv, workspace)
     for t, n in ((xq, "xq"), (xs, "xs"), (w, "w"), (w_scales, "w_scales")):
-        _dense(t, n)
-        if t.dtype != torch.uint8 or t.dim() != 2:
-            raise ValueError(f"{n} must be a uint8 matrix")
+        if t.dtype != torch.uint8 or t.dim() != 2 or not t.is_contiguous():
+            raise ValueError(f"{n} must be a contiguous uint8 matrix")
     T, K = xq.shape
     N = w.shape[0]
-    if tuple(xs.shape) != (T, K // 32):
+    if xs.shape != (T, K // 32):
         raise ValueError(f"xs must be [{T}, {K // 32}], got {tuple(xs.shape)}")
-    fmt = _format(w, w_scales, K)
-    if fmt == W_MXFP4:
-        _check_mxfp4(w, w_scales, N, K)
-    elif tuple(w.shape) != (N, K) or tuple(w_scales.shape) != (N // 32, K // 32):
-        raise ValueError(f"w must be [N, {K}] with scales [N/32, K/32] (MXFP8) or [N, {K // 2}] with [N, K/32] (MXFP4)")
-    if kv is None:
-        kv = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
-    elif tuple(kv.shape) != (T, N) or kv.dtype != torch.bfloat16:
-        raise ValueError(f"kv must be bf16 [{T}, {N}]")
-    _dense(kv, "kv")
-    need = L.engram_wkv_mx_workspace_size(T, K, N, fmt)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _run_on(dev, L.engram_wkv_mx, xq.data_ptr(), xs.data_ptr(), T, K, w.data_ptr(), w_scales.data_ptr(), fmt, N,
-            kv.data_ptr(), None if workspace is None else workspace.data_ptr(), ws_bytes)
-    return kv
+    if 2 * w.shape[1] == K and w_scales.shape == (N, K // 32):
+        fmt = W_MXFP4
+    elif w.shape[1] == K and w_scales.shape == (N // 32, K // 32):
+        fmt = W_MXFP8
+    else:
+        raise ValueError(f"w must be [N, {K}] with scales [N/32, {K // 32}] (MXFP8) or [N, {K // 2}] with "
+                         f"[N, {K // 32}] (MXFP4)")
+    return _product(L, L.engram_wkv_mx, L.engram_wkv_mx_workspace_size, (xq, xs), T, K, w, w_scales, fmt, N, kv,
+                    workspace)
 
 
 def add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None = None, weight: torch.Tensor | None = None,
@@ -346,56 +361,68 @@ def add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None = None, weight: 
     outputs may be given (contiguous); residual_out may be residual itself and
     out may be x itself."""
     L = load_library()
-    if x.dim() not in (2, 3):
+    shape = x.shape
+    if len(shape) == 3:
+        T, hc, dim = shape
+        xst, xsh, xsd = x.stride()
+    elif len(shape) == 2:
+        (T, dim), hc = shape, 1
+        (xst, xsd), xsh = x.stride(), 0
+    else:
         raise ValueError("x must be [T, hc, dim] or [T, dim]")
     dev = _device_of(x, residual, weight, residual_out, out, xq, xs)
-    shape = tuple(x.shape)
-    T, hc, dim = shape if x.dim() == 3 else (shape[0], 1, shape[1])
-    if out_format not in ("bf16", "mxfp8", "both"):
-        raise ValueError('out_format must be "bf16", "mxfp8" or "both"')
-    for t, n in ((x, "x"), (residual, "residual")):
-        if t is None:
-            continue
-        if t.dtype != torch.bfloat16 or tuple(t.shape) != shape:
-            raise ValueError(f"{n} must be bf16 {shape}")
-        if dim > 1 and t.stride(-1) != 1:
-            raise ValueError(f"{n} must be contiguous in its last dimension")
-    whc = 1
-    if weight is not None:
-        _dense(weight, "weight")
-        if weight.dtype != torch.bfloat16 or tuple(weight.shape) not in ((dim,), (hc, dim), (1, dim)):
-            raise ValueError(f"weight must be bf16 [{dim}] or [{hc}, {dim}]")
-        whc = weight.shape[0] if weight.dim() == 2 else 1
-    if residual is None and residual_out is not None:
+    bf16 = torch.bfloat16
+    if x.dtype != bf16 or (xsd != 1 and dim > 1):
+        raise ValueError("x must be bf16, contiguous in its last dimension")
+    rp, rst, rsh, rop = None, 0, 0, None
+    if residual is not None:
+        if residual.dtype != bf16 or residual.shape != shape or (residual.stride(-1) != 1 and dim > 1):
+            raise ValueError(f"residual must be bf16 {tuple(shape)}, contiguous in its last dimension")
+        if residual_out is None:
+            residual_out = torch.empty(shape, dtype=bf16, device=x.device)
+        elif residual_out.shape != shape or residual_out.dtype != bf16 or not residual_out.is_contiguous():
+            raise ValueError(f"residual_out must be bf16 {tuple(shape)}, contiguous")
+        rp, rop, rst = residual.data_ptr(), residual_out.data_ptr(), residual.stride(0)
+        rsh = residual.stride(1) if len(shape) == 3 else 0
+    elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    if residual is not None and residual_out is None:
-        residual_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    if out_format == "mxfp8":
-        if out is not None:
-            raise ValueError('out is not written with out_format "mxfp8"')
-    elif out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    if out_format == "bf16":
-        if xq is not None or xs is not None:
-            raise ValueError('xq and xs are not written with out_format "bf16"')
-    else:
+    wp, whc = None, 1
+    if weight is not None:
+        if weight.dtype != bf16 or not weight.is_contiguous() or weight.shape not in ((dim,), (hc, dim), (1, dim)):
+            raise ValueError(f"weight must be bf16 [{dim}] or [{hc}, {dim}], contiguous")
+        wp = weight.data_ptr()
+        whc = weight.shape[0] if weight.dim() == 2 else 1
+    op = None
+    if out_format == "bf16" or out_format == "both":
+        if out is None:
+            out = torch.empty(shape, dtype=bf16, device=x.device)
+        elif out.shape != shape or out.dtype != bf16 or not out.is_contiguous():
+            raise ValueError(f"out must be bf16 {tuple(shape)}, contiguous")
+        op = out.data_ptr()
+    elif out_format != "mxfp8":
+        raise ValueError('out_format must be "bf16", "mxfp8" or "both"')
+    elif out is not None:
+        raise ValueError('out is not written with out_format "mxfp8"')
+    qp, sp = None, None
+    if out_format != "bf16":
+        scales = (*shape[:-1], dim // 32)
         if xq is None:
-            xq = torch.empty(shape, dtype=torch.uint8, device=dev)
+            xq = torch.empty(shape, dtype=torch.uint8, device=x.device)
+        elif xq.shape != shape or xq.dtype != torch.uint8 or not xq.is_contiguous():
+            raise ValueError(f"xq must be uint8 {tuple(shape)}, contiguous")
         if xs is None:
-            xs = torch.empty(shape[:-1] + (dim // 32,), dtype=torch.uint8, device=dev)
-    for t, n, dt, sh in ((residual_out, "residual_out", torch.bfloat16, shape), (out, "out", torch.bfloat16, shape),
-                         (xq, "xq", torch.uint8, shape), (xs, "xs", torch.uint8, shape[:-1] + (dim // 32,))):
-        if t is None:
-            continue
-        _dense(t, n)
-        if t.dtype != dt or tuple(t.shape) != sh:
-            raise ValueError(f"{n} must be {dt} {sh}")
-    three = x.dim() == 3
-    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+            xs = torch.empty(scales, dtype=torch.uint8, device=x.device)
+        elif xs.shape != scales or xs.dtype != torch.uint8 or not xs.is_contiguous():
+            raise ValueError(f"xs must be uint8 {scales}, contiguous")
+        qp, sp = xq.data_ptr(), xs.data_ptr()
+    elif xq is not None or xs is not None:
+        raise ValueError('xq and xs are not written with out_format "bf16"')
     # the stride of a dimension of one element is never used, whatever torch says it is
-    st = lambda t: (0, 0) if t is None else (t.stride(0) if T > 1 else 0, t.stride(1) if three and hc > 1 else 0)  # noqa: E731
-    _run_on(dev, L.engram_add_rms_norm, p(x), *st(x), p(residual), *st(residual), p(weight), whc, T, hc, dim, eps,
-            p(residual_out), p(out), p(xq), p(xs))
+    if T <= 1:
+        xst = rst = 0
+    if hc <= 1:
+        xsh = rsh = 0
+    _run_on(dev, L.engram_add_rms_norm, x.data_ptr(), xst, xsh, rp, rst, rsh, wp, whc, T, hc, dim, eps, rop, op, qp, sp)
     return residual_out, out, xq, xs
 
 

@@ -490,4 +490,6 @@ def test_argument_errors_on_the_device():
 
 class _FakeOther:
     is_cuda = True
-    device = torch.device("cuda", 7)
+
+    def get_device(self):
+        return 7
