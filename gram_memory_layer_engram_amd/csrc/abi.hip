@@ -48,12 +48,17 @@ size_t mx_stage_bytes(int64_t T, int32_t K) {
   return round_up((size_t)T * K) + round_up((size_t)T * (K / 32));
 }
 
+// MXFP4 weights: the GEMV, the tiled GEMM on the codes (K % 256 == 0), or the
+// weight expanded to bf16 in the workspace for the bf16 GEMM.
+bool mxfp4_expands(int64_t T, int64_t K, bool x_mxfp8) {
+  return K % 256 != 0 && !gemv_mxfp4_supported(T, (int)K, x_mxfp8);
+}
+
 // Scratch of a projection from bf16 x besides kv: MXFP8 staging of x, or the
 // MXFP4 weight expanded to bf16 for the tiled GEMM.
 size_t wkv_scratch_bytes(int64_t T, int64_t K, int64_t N, int32_t w_format) {
   if (w_format == ENGRAM_W_MXFP8) return mx_stage_bytes(T, (int32_t)K);
-  if (w_format == ENGRAM_W_MXFP4)
-    return gemv_mxfp4_supported(T, (int)K, false) ? 0 : round_up((size_t)N * K * 2);
+  if (w_format == ENGRAM_W_MXFP4 && mxfp4_expands(T, K, false)) return round_up((size_t)N * K * 2);
   return 0;
 }
 
@@ -90,6 +95,15 @@ hipError_t run_mx_projection(const uint8_t* xq, const uint8_t* xs, int64_t T, in
 
 constexpr GateEpi kPlainStore{nullptr, nullptr, nullptr, nullptr, nullptr, 0, 0};
 
+// The tiled GEMM with MXFP4 weights and bf16 x.
+int run_mxfp4_tiled(const void* x, int64_t T, int32_t K, const void* w, const uint8_t* w_scales, int32_t N,
+                    void* kv, void* workspace, hipStream_t s, const GateEpi& ep) {
+  if (K % 256 == 0)
+    return hip_status(launch_gemm_mxfp4(x, nullptr, T, K, (const uint8_t*)w, w_scales, N, kv, s, ep));
+  if (launch_mxfp4_to_bf16(w, w_scales, N, K, workspace, s) != hipSuccess) return ENGRAM_EHIP;
+  return hip_status(launch_gemm_bf16(x, T, K, workspace, N, kv, s, ep));
+}
+
 // Enqueue the projection given a workspace already checked to be large enough.
 int run_wkv(const void* x, int64_t T, int32_t K, const void* w,
             const uint8_t* w_scales, int32_t w_format, int32_t N, void* kv,
@@ -101,8 +115,7 @@ int run_wkv(const void* x, int64_t T, int32_t K, const void* w,
   if (w_format == ENGRAM_W_MXFP4) {
     if (!ep.hidden && gemv_mxfp4_supported(T, K, false))
       return hip_status(launch_gemv_mxfp4(x, nullptr, T, K, w, w_scales, N, kv, s));
-    if (launch_mxfp4_to_bf16(w, w_scales, N, K, workspace, s) != hipSuccess) return ENGRAM_EHIP;
-    return hip_status(launch_gemm_bf16(x, T, K, workspace, N, kv, s, ep));
+    return run_mxfp4_tiled(x, T, K, w, w_scales, N, kv, workspace, s, ep);
   }
   uint8_t* xq = (uint8_t*)workspace;
   uint8_t* xs = xq + round_up((size_t)T * K);
@@ -117,10 +130,7 @@ int run_wkv_tiled(const void* x, int64_t T, int32_t K, const void* w, const uint
                   int32_t w_format, int32_t N, void* kv, void* workspace, hipStream_t s, const GateEpi& ep) {
   if (T == 0) return ENGRAM_OK;
   if (w_format == ENGRAM_W_BF16) return hip_status(launch_gemm_bf16(x, T, K, w, N, kv, s, ep));
-  if (w_format == ENGRAM_W_MXFP4) {
-    if (launch_mxfp4_to_bf16(w, w_scales, N, K, workspace, s) != hipSuccess) return ENGRAM_EHIP;
-    return hip_status(launch_gemm_bf16(x, T, K, workspace, N, kv, s, ep));
-  }
+  if (w_format == ENGRAM_W_MXFP4) return run_mxfp4_tiled(x, T, K, w, w_scales, N, kv, workspace, s, ep);
   uint8_t* xq = (uint8_t*)workspace;
   uint8_t* xs = xq + round_up((size_t)T * K);
   if (launch_mx_quantize(x, T, K, xq, xs, s) != hipSuccess) return ENGRAM_EHIP;
@@ -273,7 +283,8 @@ int engram_wkv_gate_partials(const void* x, int64_t T, int32_t K, const void* w,
   if (st != ENGRAM_OK) return st;
   if (T == 0) return ENGRAM_OK;
   if (!partials || ((uintptr_t)partials & 7u)) return ENGRAM_EINVAL;
-  if (w_format == ENGRAM_W_MXFP4 && gemv_mxfp4_supported(T, K, false)) return ENGRAM_EUNSUPPORTED;
+  // the GEMV's share of the workspace rule does not apply: this always tiles
+  if (w_format == ENGRAM_W_MXFP4 && K % 256 != 0 && gemv_mxfp4_supported(T, K, false)) return ENGRAM_EUNSUPPORTED;
   const size_t need = engram_wkv_workspace_size(T, K, N, w_format);
   if (workspace_bytes < need || (need && (!workspace || ((uintptr_t)workspace % kAlign))))
     return ENGRAM_EINVAL;
@@ -294,7 +305,7 @@ int engram_wkv(const void* x, int64_t T, int32_t K, const void* w,
 }
 
 size_t engram_wkv_mx_workspace_size(int64_t T, int32_t K, int32_t N, int32_t w_format) {
-  if (T <= 0 || K <= 0 || N <= 0 || w_format != ENGRAM_W_MXFP4 || gemv_mxfp4_supported(T, K, true)) return 0;
+  if (T <= 0 || K <= 0 || N <= 0 || w_format != ENGRAM_W_MXFP4 || !mxfp4_expands(T, K, true)) return 0;
   return round_up((size_t)N * K * 2) + round_up((size_t)T * K * 2);
 }
 
@@ -313,6 +324,8 @@ int engram_wkv_mx(const uint8_t* xq, const uint8_t* xs, int64_t T, int32_t K, co
   if (w_format == ENGRAM_W_MXFP8)
     return hip_status(run_mx_projection(xq, xs, T, K, w, w_scales, N, kv, s, kPlainStore));
   if (gemv_mxfp4_supported(T, K, true)) return hip_status(launch_gemv_mxfp4(xq, xs, T, K, w, w_scales, N, kv, s));
+  if (K % 256 == 0)
+    return hip_status(launch_gemm_mxfp4(xq, xs, T, K, (const uint8_t*)w, w_scales, N, kv, s, kPlainStore));
   void* wb = workspace;
   void* xb = (uint8_t*)workspace + round_up((size_t)N * K * 2);
   if (launch_mxfp4_to_bf16(w, w_scales, N, K, wb, s) != hipSuccess) return ENGRAM_EHIP;

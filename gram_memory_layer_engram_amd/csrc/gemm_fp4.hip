@@ -1,0 +1,427 @@
+// Tiled projection GEMMs with MXFP4 weights: kv[T, N] = bf16(x . deq(W)^T), x
+// bf16 (gemm_fp4_bf16_kernel) or MXFP8 (gemm_fp4_mx_kernel), K % 256 == 0.
+//
+// The block (256 W rows x 256 tokens, four waves of 128x128 on 32x32 MFMA
+// tiles), tile order, DMAs and epilogue are the other tiled GEMMs' (gemm.hip).
+// W stays e2m1 all the way into LDS: a 128-byte LDS row of W holds 256 k, so a
+// 32 KiB chunk of W serves four bf16 slices of x (64 k) or two MXFP8 slices
+// (128 k), and a slice moves 40 (48) KiB from L2 instead of 64, which is what
+// bounds those kernels. LDS: two slots for W chunks, a ring of three for x.
+//
+//  * bf16 x: lane (row l%32, half h = l/32) reads, per slice, the 16 bytes of k
+//    32h .. 32h+31 of its row: one scale group. v_cvt_scalef32_pk_bf16_fp4 turns
+//    its word kk into the A fragment of v_mfma_f32_32x32x16_bf16 number kk (k
+//    32h+8kk .. +7; the order of k inside a product is free as long as x follows
+//    it: its fragment kk is piece 4h+kk). The 16 conversions of a row block run
+//    under the MFMAs, one sub-step ahead.
+//  * MXFP8 x: v_mfma_scale_f32_32x32x64_f8f6f4 takes the codes as they are:
+//    lane group g holds k 32g .. 32g+31 of the fp4 operand in its 16 bytes, of
+//    the fp8 operand k 16g.. and 32+16g.., and its E8M0 bytes scale k block
+//    [32g, 32g+32) of its own row.
+#include <type_traits>
+
+#include "gemm_tile.h"
+
+namespace engram {
+
+namespace {
+
+constexpr int kWSlots = 2, kXSlots = 3;
+static_assert((kWSlots + kXSlots) * Q_CHUNK == Q_LDS, "LDS budget");
+constexpr int SG_VALU = 0x002;
+
+template <int V> using Int = std::integral_constant<int, V>;
+
+__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const uint8_t* __restrict__ w,
+                          const uint8_t* __restrict__ ws, int N, uint16_t* __restrict__ kv, int tiles_n,
+                          int tiles_t, GateEpi ep) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  int tn, tt;
+  tile_of(blockIdx.x, tiles_n, tiles_t, tn, tt);
+  const int n0 = tn * BM, t0 = tt * BN;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = (wave >> 1) * 128, wt = (wave & 1) * 128;
+  const uint32_t wpitch = (uint32_t)K / 2u, xpitch = (uint32_t)K * 2u, kb = (uint32_t)K / 32u;
+  const rsrc_t ra = make_rsrc(w + (int64_t)n0 * wpitch, (uint32_t)min(BM, N - n0) * wpitch);
+  const rsrc_t rb = make_rsrc(x + (int64_t)t0 * K, (uint32_t)min(BN, T - t0) * xpitch);
+  const rsrc_t rs = make_rsrc(ws + (int64_t)n0 * kb, (uint32_t)min(BM, N - n0) * kb);
+  const uint32_t ooba = (uint32_t)BM * wpitch, oobb = (uint32_t)BN * xpitch;   // at or past the ranges
+  const int nk = K / 64, nc = K / 256;
+
+  const dma::Lane la = dma::lane_of(wave, lane, wpitch), lb = dma::lane_of(wave, lane, xpitch);
+  auto dma_w = [&](int slot, uint32_t kofs, int i) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(smem + slot + (wave + 4 * i) * 1024), 16,
+                                             dma::voffset(la, i, kofs, wpitch, ooba, false), 0, 0, 0);
+  };
+  auto dma_x = [&](int slot, uint32_t kofs, int i) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr_t)(smem + slot + (wave + 4 * i) * 1024), 16,
+                                             dma::voffset(lb, i, kofs, xpitch, oobb, false), 0, 0, 0);
+  };
+
+  const int lrow = lane & 31, lhalf = lane >> 5;
+  const int fsw = (lrow >> 1) & 7;
+  // the 8 scale bytes of a chunk (256 k) of this lane's four rows; byte
+  // 2*PAR + h is slice PAR's
+  uint32_t srow[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) srow[i] = (uint32_t)(wn + i * 32 + lrow) * kb;
+  auto scales8 = [&](int c, u32x2 (&s8)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s8[i] = __builtin_amdgcn_raw_buffer_load_b64(rs, srow[i] + 8u * (uint32_t)c, 0, 0);
+  };
+  // byte 2*par + h in the exponent field of an fp32 (the conversion reads no
+  // other bits of its scale)
+  const uint32_t lsh = 8u * (uint32_t)lhalf;
+  auto pick = [&](const u32x2& v, int par) {
+    return __uint_as_float(((par < 2 ? v.x : v.y) >> ((uint32_t)(16 * (par & 1)) + lsh)) << 23);
+  };
+
+  f32x16 acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+  bf16x8_t a[2][4], b[2][4];
+  i32x4 raw[4];
+  float sc[4];
+  auto read_raw = [&](int slot, int par, int i) {
+    raw[i] = *reinterpret_cast<const i32x4*>(smem + slot + (wn + i * 32 + lrow) * Q_ROW +
+                                             (((2 * par + lhalf) ^ fsw) << 4));
+  };
+  auto read_x = [&](int slot, int kk, int c, int j) {
+    b[c][j] = *reinterpret_cast<const bf16x8_t*>(smem + slot + (wt + j * 32 + lrow) * Q_ROW +
+                                                 (((4 * lhalf + kk) ^ fsw) << 4));
+  };
+  auto convert = [&](int kk, int c, int i) {
+    const uint32_t v = (uint32_t)raw[i][kk];
+    const i32x4 f = {(int)fp4_pair_to_bf16<0>(v, sc[i]), (int)fp4_pair_to_bf16<1>(v, sc[i]),
+                     (int)fp4_pair_to_bf16<2>(v, sc[i]), (int)fp4_pair_to_bf16<3>(v, sc[i])};
+    a[c][i] = __builtin_bit_cast(bf16x8_t, f);
+  };
+  auto mfma_row = [&](int c, int i) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[c][i], b[c][j], acc[i][j], 0, 0, 0);
+  };
+  auto wslot = [](int c) { return (c & 1) * Q_CHUNK; };
+
+  // prologue: W chunk 0, x slices 0 and 1; all but x slice 1's DMAs waited for
+  u32x2 s8[4], n8[4];
+  scales8(0, s8);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < Q_DMA; ++i) dma_w(0, 0u, i);
+#pragma unroll
+  for (int i = 0; i < Q_DMA; ++i) dma_x(kWSlots * Q_CHUNK, 0u, i);
+#pragma unroll
+  for (int i = 0; i < Q_DMA; ++i) dma_x((kWSlots + 1) * Q_CHUNK, (uint32_t)Q_ROW, i);
+  wait_vm<Q_DMA>();
+  // a use here keeps the scale loads ahead of the DMAs
+#pragma unroll
+  for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(s8[i]));
+  bare_barrier();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    read_raw(0, 0, i);
+    sc[i] = pick(s8[i], 0);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) read_x(kWSlots * Q_CHUNK, 0, 0, j);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) convert(0, 0, i);
+
+  int xb = 0;   // d % 3
+  // slice d (64 k), par = d % 4: x of slice d+2 and, in the chunk's first
+  // three slices, W of the next chunk are fetched; the barrier that publishes
+  // slice d+1 sits after the first 4 of the last 16 MFMAs.
+  auto slice = [&](int d, auto par) {
+    constexpr int PAR = decltype(par)::value;
+    const int c = d >> 2;
+    auto xslot = [&](int m) { const int v = xb + m; return (kWSlots + (v >= 3 ? v - 3 : v)) * Q_CHUNK; };
+    const int sb = xslot(0), sb1 = xslot(1), sb2 = xslot(2);
+    const uint32_t kx = d + 2 < nk ? (uint32_t)(d + 2) * Q_ROW : oobb;
+    const uint32_t kw = c + 1 < nc ? (uint32_t)(c + 1) * Q_ROW : ooba;
+    if (PAR == 0) scales8(min(c + 1, nc - 1), n8);   // the last chunk reloads itself, unused
+    // sub-steps 0..2: MFMAs of sub-step kk, fragments of kk+1
+#pragma unroll
+    for (int kk = 0; kk < 3; ++kk) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        __builtin_amdgcn_sched_barrier(0);
+        // W: 3 + 3 + 2 DMAs over a chunk's first three slices, ahead of x's
+        const bool dw = PAR < 3 && kk == 0 && q < (PAR == 2 ? 2 : 3);
+        if (dw) dma_w(wslot(c + 1), kw, 3 * PAR + q);
+        const int x0 = kk * 4 + q - 1;   // x: 8 DMAs from (kk 0, q 1) on
+        const bool dx = x0 >= 0 && x0 < Q_DMA;
+        if (dx) dma_x(sb2, kx, x0);
+        read_x(sb, kk + 1, (kk + 1) & 1, q);
+        convert(kk + 1, (kk + 1) & 1, q);
+        mfma_row(kk & 1, q);
+        SGB(SG_MFMA, 1);
+        if (dw) SGB(SG_VMEM, 1);
+        if (dx) SGB(SG_VMEM, 1);
+        SGB(SG_MFMA, 1); SGB(SG_DSR, 1); SGB(SG_MFMA, 1); SGB(SG_VALU, 4); SGB(SG_MFMA, 1);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    mfma_row(1, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vm<Q_DMA>();   // only x of slice d+2 may still fly
+    wait_lgkm0();
+    bare_barrier();
+    // sub-step 3, quarters 1..3: slice d+1's W words, first x fragments, conversions
+    const int sw1 = wslot(PAR == 3 ? c + 1 : c);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) read_raw(sw1, (PAR + 1) & 3, i);
+    mfma_row(1, 1);
+    SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 2);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) read_x(sb1, 0, 0, j);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sc[i] = PAR == 3 ? pick(n8[i], 0) : pick(s8[i], (PAR + 1) & 3);
+    mfma_row(1, 2);
+    SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 2);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) convert(0, 0, i);
+    mfma_row(1, 3);
+    SGB(SG_MFMA, 1); SGB(SG_VALU, 5); SGB(SG_MFMA, 1); SGB(SG_VALU, 5); SGB(SG_MFMA, 1); SGB(SG_VALU, 5);
+    SGB(SG_MFMA, 1);
+    if (PAR == 3) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s8[i] = n8[i];
+    }
+    xb = xb + 1 >= 3 ? 0 : xb + 1;
+  };
+  for (int d = 0; d < nk; d += 4) {
+    slice(d, Int<0>{});
+    slice(d + 1, Int<1>{});
+    slice(d + 2, Int<2>{});
+    slice(d + 3, Int<3>{});
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  wait_vm<0>();   // the zero-fill DMAs of the last slices land before LDS is reused
+  store_tile(acc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
+}
+
+__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restrict__ xs, int T, int K,
+                        const uint8_t* __restrict__ w, const uint8_t* __restrict__ ws, int N,
+                        uint16_t* __restrict__ kv, int tiles_n, int tiles_t, GateEpi ep) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  int tn, tt;
+  tile_of(blockIdx.x, tiles_n, tiles_t, tn, tt);
+  const int n0 = tn * BM, t0 = tt * BN;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = (wave >> 1) * 128, wt = (wave & 1) * 128;
+  const uint32_t wpitch = (uint32_t)K / 2u, xpitch = (uint32_t)K, kb = (uint32_t)K / 32u;
+  const rsrc_t ra = make_rsrc(w + (int64_t)n0 * wpitch, (uint32_t)min(BM, N - n0) * wpitch);
+  const rsrc_t rb = make_rsrc(xq + (int64_t)t0 * xpitch, (uint32_t)min(BN, T - t0) * xpitch);
+  const rsrc_t rsa = make_rsrc(ws + (int64_t)n0 * kb, (uint32_t)min(BM, N - n0) * kb);
+  const rsrc_t rsb = make_rsrc(xs + (int64_t)t0 * kb, (uint32_t)min(BN, T - t0) * kb);
+  const uint32_t ooba = (uint32_t)BM * wpitch, oobb = (uint32_t)BN * xpitch;
+  const int ns = K / 128, nc = K / 256;   // x slices (even), W chunks
+
+  const dma::Lane la = dma::lane_of(wave, lane, wpitch), lb = dma::lane_of(wave, lane, xpitch);
+  auto dma_w = [&](int slot, uint32_t kofs, int i) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(smem + slot + (wave + 4 * i) * 1024), 16,
+                                             dma::voffset(la, i, kofs, wpitch, ooba, false), 0, 0, 0);
+  };
+  auto dma_x = [&](int slot, uint32_t kofs, int i) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr_t)(smem + slot + (wave + 4 * i) * 1024), 16,
+                                             dma::voffset(lb, i, kofs, xpitch, oobb, false), 0, 0, 0);
+  };
+
+  const int lrow = lane & 31, lg = lane >> 5;
+  const int fsw = (lrow >> 1) & 7;
+  // the 8 scale bytes of a chunk (four stages of 64 k) of this lane's W and
+  // token rows; lane group g takes byte 2*stage + g
+  uint32_t arow[4], brow[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    arow[i] = (uint32_t)(wn + i * 32 + lrow) * kb;
+    brow[i] = (uint32_t)(wt + i * 32 + lrow) * kb;
+  }
+  auto scales8 = [&](int c, u32x2 (&a8)[4], u32x2 (&b8)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a8[i] = __builtin_amdgcn_raw_buffer_load_b64(rsa, arow[i] + 8u * (uint32_t)c, 0, 0);
+      b8[i] = __builtin_amdgcn_raw_buffer_load_b64(rsb, brow[i] + 8u * (uint32_t)c, 0, 0);
+    }
+  };
+  const uint32_t lsh = (uint32_t)lg * 8u;
+  auto pick = [&](const u32x2& v, int u) {   // u static: byte 2u + lg
+    return (int)(((u < 2 ? v.x : v.y) >> ((uint32_t)(16 * (u & 1)) + lsh)) & 0xffu);
+  };
+  // W fragment of stage u (0..3) of a chunk, x fragment of half h of a slice
+  auto wfrag = [&](int slot, int u, int i) {
+    return *reinterpret_cast<const i32x4*>(smem + slot + (wn + i * 32 + lrow) * Q_ROW + (((2 * u + lg) ^ fsw) << 4));
+  };
+  auto xfrag = [&](int slot, int h, int j) {
+    const char* base = smem + slot + (wt + j * 32 + lrow) * Q_ROW;
+    const i32x4 lo = *reinterpret_cast<const i32x4*>(base + (((4 * h + lg) ^ fsw) << 4));
+    const i32x4 hi = *reinterpret_cast<const i32x4*>(base + (((4 * h + 2 + lg) ^ fsw) << 4));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+
+  f32x16 acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+  i32x4 a[4], na[4];
+  i32x8 b[4], nb[4];
+  int sa[4], sb[4];
+  auto mfma_row = [&](int i) {
+    const i32x8 wa = __builtin_shufflevector(a[i], a[i], 0, 1, 2, 3, 0, 1, 2, 3);   // fp4: the first four words
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wa, b[j], acc[i][j], 4, 0, 0, sa[i], 0, sb[j]);
+  };
+  auto wslot = [](int c) { return (c & 1) * Q_CHUNK; };
+
+  u32x2 sa8[4], sb8[4], na8[4], nb8[4];
+  scales8(0, sa8, sb8);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < Q_DMA; ++i) dma_w(0, 0u, i);
+#pragma unroll
+  for (int i = 0; i < Q_DMA; ++i) dma_x(kWSlots * Q_CHUNK, 0u, i);
+#pragma unroll
+  for (int i = 0; i < Q_DMA; ++i) dma_x((kWSlots + 1) * Q_CHUNK, (uint32_t)Q_ROW, i);
+  wait_vm<Q_DMA>();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(sa8[i]), "+v"(sb8[i]));
+  bare_barrier();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a[i] = wfrag(0, 0, i);
+    b[i] = xfrag(kWSlots * Q_CHUNK, 0, i);
+    sa[i] = pick(sa8[i], 0);
+    sb[i] = pick(sb8[i], 0);
+  }
+
+  int xb = 0;   // d % 3
+  // slice d (two stages of 64 k), par = d % 2: x of slice d+2 goes out in the
+  // last six quarters, W of the next chunk in the first four of an even slice
+  auto slice = [&](int d, auto par) {
+    constexpr int PAR = decltype(par)::value;
+    const int c = d >> 1;
+    auto xslot = [&](int m) { const int v = xb + m; return (kWSlots + (v >= 3 ? v - 3 : v)) * Q_CHUNK; };
+    const int s_x = xslot(0), s_x1 = xslot(1), s_x2 = xslot(2);
+    const uint32_t kx = d + 2 < ns ? (uint32_t)(d + 2) * Q_ROW : oobb;
+    const uint32_t kw = c + 1 < nc ? (uint32_t)(c + 1) * Q_ROW : ooba;
+    if (PAR == 0) scales8(min(c + 1, nc - 1), na8, nb8);   // the last chunk reloads itself, unused
+    // stage 0; stage 1's fragments are read ahead
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (PAR == 0) {
+        dma_w(wslot(c + 1), kw, 2 * q);
+        dma_w(wslot(c + 1), kw, 2 * q + 1);
+      } else {
+        dma_x(s_x2, kx, 2 * q);
+        dma_x(s_x2, kx, 2 * q + 1);
+      }
+      na[q] = wfrag(wslot(c), 2 * PAR + 1, q);
+      nb[q] = xfrag(s_x, 1, q);
+      mfma_row(q);
+      SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_DSR, 1); SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_DSR, 1);
+      SGB(SG_MFMA, 1); SGB(SG_DSR, 1); SGB(SG_MFMA, 1);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[i] = na[i];
+      b[i] = nb[i];
+      sa[i] = pick(sa8[i], 2 * PAR + 1);
+      sb[i] = pick(sb8[i], 2 * PAR + 1);
+    }
+    // stage 1; the barrier that publishes slice d+1 after its second row block
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (PAR == 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) dma_x(s_x2, kx, 4 * q + k);
+      }
+      mfma_row(q);
+      if (PAR == 0) {
+        SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_MFMA, 1); SGB(SG_VMEM, 1);
+        SGB(SG_MFMA, 1); SGB(SG_VMEM, 1);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    // in flight may be x of slice d+2 and, in an even slice, the W chunk
+    // after this slice's (not needed before the next slice's end)
+    if (PAR == 0) wait_vm<2 * Q_DMA>();
+    else wait_vm<Q_DMA>();
+    wait_lgkm0();
+    bare_barrier();
+    const int sw1 = wslot(PAR == 1 ? c + 1 : c);
+    constexpr int u1 = PAR == 1 ? 0 : 2;
+#pragma unroll
+    for (int q = 2; q < 4; ++q) {
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 2 * q - 4; i < 2 * q - 2; ++i) {
+        na[i] = wfrag(sw1, u1, i);
+        nb[i] = xfrag(s_x1, 0, i);
+      }
+      mfma_row(q);
+      SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2);
+      SGB(SG_MFMA, 1);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[i] = na[i];
+      b[i] = nb[i];
+      if (PAR == 1) {
+        sa8[i] = na8[i];
+        sb8[i] = nb8[i];
+      }
+      sa[i] = pick(sa8[i], u1);
+      sb[i] = pick(sb8[i], u1);
+    }
+    xb = xb + 1 >= 3 ? 0 : xb + 1;
+  };
+  for (int d = 0; d < ns; d += 2) {
+    slice(d, Int<0>{});
+    slice(d + 1, Int<1>{});
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  wait_vm<0>();   // the zero-fill DMAs of the last slices land before LDS is reused
+  store_tile(acc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
+}
+
+}  // namespace
+
+hipError_t launch_gemm_mxfp4(const void* x, const uint8_t* xs, int64_t T, int K, const uint8_t* w,
+                             const uint8_t* ws, int N, void* kv, hipStream_t s, const GateEpi& ep) {
+  const int tiles_n = (N + BM - 1) / BM;
+  const int tiles_t = (int)((T + BN - 1) / BN);
+  const dim3 grid(tiles_n * tiles_t), block(THREADS);
+  hipError_t e;
+  if (xs) {
+    if ((e = set_lds((const void*)gemm_fp4_mx_kernel, Q_LDS)) != hipSuccess) return e;
+    hipLaunchKernelGGL(gemm_fp4_mx_kernel, grid, block, Q_LDS, s, (const uint8_t*)x, xs, (int)T, K, w, ws, N,
+                       (uint16_t*)kv, tiles_n, tiles_t, ep);
+  } else {
+    if ((e = set_lds((const void*)gemm_fp4_bf16_kernel, Q_LDS)) != hipSuccess) return e;
+    hipLaunchKernelGGL(gemm_fp4_bf16_kernel, grid, block, Q_LDS, s, (const uint16_t*)x, (int)T, K, w, ws, N,
+                       (uint16_t*)kv, tiles_n, tiles_t, ep);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace engram
