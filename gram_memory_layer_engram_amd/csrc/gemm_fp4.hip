@@ -27,11 +27,20 @@ namespace engram {
 namespace {
 
 constexpr int kWSlots = 2, kXSlots = 3;
-static_assert((kWSlots + kXSlots) * Q_CHUNK == Q_LDS, "LDS budget");
+// A block's token tile is 64 * NJ: 256, or 128 where that fills the compute
+// units better (launch_gemm_mxfp4).
+constexpr int x_slot(int nj) { return 64 * nj * Q_ROW; }
+constexpr int x_dma(int nj) { return 2 * nj; }                  // DMAs of a wave per x slice
+constexpr int fp4_lds(int nj) {
+  const int ring = kWSlots * Q_CHUNK + kXSlots * x_slot(nj), epi = 64 * nj * 512;
+  return ring > epi ? ring : epi;
+}
+static_assert(fp4_lds(4) == Q_LDS, "LDS budget");
 constexpr int SG_VALU = 0x002;
 
 template <int V> using Int = std::integral_constant<int, V>;
 
+template <int NJ>
 __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const uint8_t* __restrict__ w,
                           const uint8_t* __restrict__ ws, int N, uint16_t* __restrict__ kv, int tiles_n,
@@ -39,15 +48,16 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   int tn, tt;
   tile_of(blockIdx.x, tiles_n, tiles_t, tn, tt);
-  const int n0 = tn * BM, t0 = tt * BN;
+  constexpr int TN = 64 * NJ, XCH = x_slot(NJ), XD = x_dma(NJ), XBASE = kWSlots * Q_CHUNK;
+  const int n0 = tn * BM, t0 = tt * TN;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wn = (wave >> 1) * 128, wt = (wave & 1) * 128;
+  const int wn = (wave >> 1) * 128, wt = (wave & 1) * (32 * NJ);
   const uint32_t wpitch = (uint32_t)K / 2u, xpitch = (uint32_t)K * 2u, kb = (uint32_t)K / 32u;
   const rsrc_t ra = make_rsrc(w + (int64_t)n0 * wpitch, (uint32_t)min(BM, N - n0) * wpitch);
-  const rsrc_t rb = make_rsrc(x + (int64_t)t0 * K, (uint32_t)min(BN, T - t0) * xpitch);
+  const rsrc_t rb = make_rsrc(x + (int64_t)t0 * K, (uint32_t)min(TN, T - t0) * xpitch);
   const rsrc_t rs = make_rsrc(ws + (int64_t)n0 * kb, (uint32_t)min(BM, N - n0) * kb);
-  const uint32_t ooba = (uint32_t)BM * wpitch, oobb = (uint32_t)BN * xpitch;   // at or past the ranges
+  const uint32_t ooba = (uint32_t)BM * wpitch, oobb = (uint32_t)TN * xpitch;   // at or past the ranges
   const int nk = K / 64, nc = K / 256;
 
   const dma::Lane la = dma::lane_of(wave, lane, wpitch), lb = dma::lane_of(wave, lane, xpitch);
@@ -78,15 +88,15 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
     return __uint_as_float(((par < 2 ? v.x : v.y) >> ((uint32_t)(16 * (par & 1)) + lsh)) << 23);
   };
 
-  f32x16 acc[4][4];
+  f32x16 acc[4][NJ];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-  bf16x8_t a[2][4], b[2][4];
+  bf16x8_t a[2][4], b[2][NJ];
   i32x4 raw[4];
   float sc[4];
   auto read_raw = [&](int slot, int par, int i) {
@@ -105,7 +115,7 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
   };
   auto mfma_row = [&](int c, int i) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < NJ; ++j)
       acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[c][i], b[c][j], acc[i][j], 0, 0, 0);
   };
   auto wslot = [](int c) { return (c & 1) * Q_CHUNK; };
@@ -117,10 +127,10 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
 #pragma unroll
   for (int i = 0; i < Q_DMA; ++i) dma_w(0, 0u, i);
 #pragma unroll
-  for (int i = 0; i < Q_DMA; ++i) dma_x(kWSlots * Q_CHUNK, 0u, i);
+  for (int i = 0; i < XD; ++i) dma_x(XBASE, 0u, i);
 #pragma unroll
-  for (int i = 0; i < Q_DMA; ++i) dma_x((kWSlots + 1) * Q_CHUNK, (uint32_t)Q_ROW, i);
-  wait_vm<Q_DMA>();
+  for (int i = 0; i < XD; ++i) dma_x(XBASE + XCH, (uint32_t)Q_ROW, i);
+  wait_vm<XD>();
   // a use here keeps the scale loads ahead of the DMAs
 #pragma unroll
   for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(s8[i]));
@@ -131,7 +141,7 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
     sc[i] = pick(s8[i], 0);
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) read_x(kWSlots * Q_CHUNK, 0, 0, j);
+  for (int j = 0; j < NJ; ++j) read_x(XBASE, 0, 0, j);
 #pragma unroll
   for (int i = 0; i < 4; ++i) convert(0, 0, i);
 
@@ -142,7 +152,7 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
   auto slice = [&](int d, auto par) {
     constexpr int PAR = decltype(par)::value;
     const int c = d >> 2;
-    auto xslot = [&](int m) { const int v = xb + m; return (kWSlots + (v >= 3 ? v - 3 : v)) * Q_CHUNK; };
+    auto xslot = [&](int m) { const int v = xb + m; return XBASE + (v >= 3 ? v - 3 : v) * XCH; };
     const int sb = xslot(0), sb1 = xslot(1), sb2 = xslot(2);
     const uint32_t kx = d + 2 < nk ? (uint32_t)(d + 2) * Q_ROW : oobb;
     const uint32_t kw = c + 1 < nc ? (uint32_t)(c + 1) * Q_ROW : ooba;
@@ -156,22 +166,23 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
         // W: 3 + 3 + 2 DMAs over a chunk's first three slices, ahead of x's
         const bool dw = PAR < 3 && kk == 0 && q < (PAR == 2 ? 2 : 3);
         if (dw) dma_w(wslot(c + 1), kw, 3 * PAR + q);
-        const int x0 = kk * 4 + q - 1;   // x: 8 DMAs from (kk 0, q 1) on
-        const bool dx = x0 >= 0 && x0 < Q_DMA;
+        const int x0 = kk * 4 + q - 1;   // x: 8 (4) DMAs from (kk 0, q 1) on
+        const bool dx = x0 >= 0 && x0 < XD;
         if (dx) dma_x(sb2, kx, x0);
-        read_x(sb, kk + 1, (kk + 1) & 1, q);
+        if (q < NJ) read_x(sb, kk + 1, (kk + 1) & 1, q);
         convert(kk + 1, (kk + 1) & 1, q);
         mfma_row(kk & 1, q);
         SGB(SG_MFMA, 1);
         if (dw) SGB(SG_VMEM, 1);
         if (dx) SGB(SG_VMEM, 1);
-        SGB(SG_MFMA, 1); SGB(SG_DSR, 1); SGB(SG_MFMA, 1); SGB(SG_VALU, 4); SGB(SG_MFMA, 1);
+        if (NJ == 4) { SGB(SG_MFMA, 1); SGB(SG_DSR, 1); SGB(SG_MFMA, 1); SGB(SG_VALU, 4); SGB(SG_MFMA, 1); }
+        else { if (q < NJ) SGB(SG_DSR, 1); SGB(SG_VALU, 4); SGB(SG_MFMA, 1); }
       }
     }
     __builtin_amdgcn_sched_barrier(0);
     mfma_row(1, 0);
     __builtin_amdgcn_sched_barrier(0);
-    wait_vm<Q_DMA>();   // only x of slice d+2 may still fly
+    wait_vm<XD>();   // only x of slice d+2 may still fly
     wait_lgkm0();
     bare_barrier();
     // sub-step 3, quarters 1..3: slice d+1's W words, first x fragments, conversions
@@ -180,20 +191,26 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
 #pragma unroll
     for (int i = 0; i < 4; ++i) read_raw(sw1, (PAR + 1) & 3, i);
     mfma_row(1, 1);
-    SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 2);
+    if (NJ == 4) { SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 2); }
+    else { SGB(SG_MFMA, 1); SGB(SG_DSR, 4); SGB(SG_MFMA, 1); }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) read_x(sb1, 0, 0, j);
+    for (int j = 0; j < NJ; ++j) read_x(sb1, 0, 0, j);
 #pragma unroll
     for (int i = 0; i < 4; ++i) sc[i] = PAR == 3 ? pick(n8[i], 0) : pick(s8[i], (PAR + 1) & 3);
     mfma_row(1, 2);
-    SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 2);
+    if (NJ == 4) { SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 2); }
+    else { SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) convert(0, 0, i);
     mfma_row(1, 3);
-    SGB(SG_MFMA, 1); SGB(SG_VALU, 5); SGB(SG_MFMA, 1); SGB(SG_VALU, 5); SGB(SG_MFMA, 1); SGB(SG_VALU, 5);
-    SGB(SG_MFMA, 1);
+    if (NJ == 4) {
+      SGB(SG_MFMA, 1); SGB(SG_VALU, 5); SGB(SG_MFMA, 1); SGB(SG_VALU, 5); SGB(SG_MFMA, 1); SGB(SG_VALU, 5);
+      SGB(SG_MFMA, 1);
+    } else {
+      SGB(SG_MFMA, 1); SGB(SG_VALU, 8); SGB(SG_MFMA, 1);
+    }
     if (PAR == 3) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) s8[i] = n8[i];
@@ -208,9 +225,10 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
   }
   __builtin_amdgcn_sched_barrier(0);
   wait_vm<0>();   // the zero-fill DMAs of the last slices land before LDS is reused
-  store_tile(acc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
+  store_tile<NJ>(acc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
 }
 
+template <int NJ>
 __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restrict__ xs, int T, int K,
                         const uint8_t* __restrict__ w, const uint8_t* __restrict__ ws, int N,
@@ -218,16 +236,17 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   int tn, tt;
   tile_of(blockIdx.x, tiles_n, tiles_t, tn, tt);
-  const int n0 = tn * BM, t0 = tt * BN;
+  constexpr int TN = 64 * NJ, XCH = x_slot(NJ), XD = x_dma(NJ), XBASE = kWSlots * Q_CHUNK;
+  const int n0 = tn * BM, t0 = tt * TN;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wn = (wave >> 1) * 128, wt = (wave & 1) * 128;
+  const int wn = (wave >> 1) * 128, wt = (wave & 1) * (32 * NJ);
   const uint32_t wpitch = (uint32_t)K / 2u, xpitch = (uint32_t)K, kb = (uint32_t)K / 32u;
   const rsrc_t ra = make_rsrc(w + (int64_t)n0 * wpitch, (uint32_t)min(BM, N - n0) * wpitch);
-  const rsrc_t rb = make_rsrc(xq + (int64_t)t0 * xpitch, (uint32_t)min(BN, T - t0) * xpitch);
+  const rsrc_t rb = make_rsrc(xq + (int64_t)t0 * xpitch, (uint32_t)min(TN, T - t0) * xpitch);
   const rsrc_t rsa = make_rsrc(ws + (int64_t)n0 * kb, (uint32_t)min(BM, N - n0) * kb);
-  const rsrc_t rsb = make_rsrc(xs + (int64_t)t0 * kb, (uint32_t)min(BN, T - t0) * kb);
-  const uint32_t ooba = (uint32_t)BM * wpitch, oobb = (uint32_t)BN * xpitch;
+  const rsrc_t rsb = make_rsrc(xs + (int64_t)t0 * kb, (uint32_t)min(TN, T - t0) * kb);
+  const uint32_t ooba = (uint32_t)BM * wpitch, oobb = (uint32_t)TN * xpitch;
   const int ns = K / 128, nc = K / 256;   // x slices (even), W chunks
 
   const dma::Lane la = dma::lane_of(wave, lane, wpitch), lb = dma::lane_of(wave, lane, xpitch);
@@ -244,17 +263,16 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
   const int fsw = (lrow >> 1) & 7;
   // the 8 scale bytes of a chunk (four stages of 64 k) of this lane's W and
   // token rows; lane group g takes byte 2*stage + g
-  uint32_t arow[4], brow[4];
+  uint32_t arow[4], brow[NJ];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    arow[i] = (uint32_t)(wn + i * 32 + lrow) * kb;
-    brow[i] = (uint32_t)(wt + i * 32 + lrow) * kb;
-  }
-  auto scales8 = [&](int c, u32x2 (&a8)[4], u32x2 (&b8)[4]) {
+  for (int i = 0; i < 4; ++i) arow[i] = (uint32_t)(wn + i * 32 + lrow) * kb;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) brow[j] = (uint32_t)(wt + j * 32 + lrow) * kb;
+  auto scales8 = [&](int c, u32x2 (&a8)[4], u32x2 (&b8)[NJ]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       a8[i] = __builtin_amdgcn_raw_buffer_load_b64(rsa, arow[i] + 8u * (uint32_t)c, 0, 0);
-      b8[i] = __builtin_amdgcn_raw_buffer_load_b64(rsb, brow[i] + 8u * (uint32_t)c, 0, 0);
+      if (i < NJ) b8[i] = __builtin_amdgcn_raw_buffer_load_b64(rsb, brow[i] + 8u * (uint32_t)c, 0, 0);
     }
   };
   const uint32_t lsh = (uint32_t)lg * 8u;
@@ -272,44 +290,48 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
 
-  f32x16 acc[4][4];
+  f32x16 acc[4][NJ];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
   i32x4 a[4], na[4];
-  i32x8 b[4], nb[4];
-  int sa[4], sb[4];
+  i32x8 b[NJ], nb[NJ];
+  int sa[4], sb[NJ];
   auto mfma_row = [&](int i) {
     const i32x8 wa = __builtin_shufflevector(a[i], a[i], 0, 1, 2, 3, 0, 1, 2, 3);   // fp4: the first four words
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < NJ; ++j)
       acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wa, b[j], acc[i][j], 4, 0, 0, sa[i], 0, sb[j]);
   };
   auto wslot = [](int c) { return (c & 1) * Q_CHUNK; };
 
-  u32x2 sa8[4], sb8[4], na8[4], nb8[4];
+  u32x2 sa8[4], sb8[NJ], na8[4], nb8[NJ];
   scales8(0, sa8, sb8);
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int i = 0; i < Q_DMA; ++i) dma_w(0, 0u, i);
 #pragma unroll
-  for (int i = 0; i < Q_DMA; ++i) dma_x(kWSlots * Q_CHUNK, 0u, i);
+  for (int i = 0; i < XD; ++i) dma_x(XBASE, 0u, i);
 #pragma unroll
-  for (int i = 0; i < Q_DMA; ++i) dma_x((kWSlots + 1) * Q_CHUNK, (uint32_t)Q_ROW, i);
-  wait_vm<Q_DMA>();
+  for (int i = 0; i < XD; ++i) dma_x(XBASE + XCH, (uint32_t)Q_ROW, i);
+  wait_vm<XD>();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(sa8[i]), "+v"(sb8[i]));
+  for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(sa8[i]));
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) asm volatile("" : "+v"(sb8[j]));
   bare_barrier();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     a[i] = wfrag(0, 0, i);
-    b[i] = xfrag(kWSlots * Q_CHUNK, 0, i);
     sa[i] = pick(sa8[i], 0);
-    sb[i] = pick(sb8[i], 0);
+    if (i < NJ) {
+      b[i] = xfrag(XBASE, 0, i);
+      sb[i] = pick(sb8[i], 0);
+    }
   }
 
   int xb = 0;   // d % 3
@@ -318,7 +340,7 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
   auto slice = [&](int d, auto par) {
     constexpr int PAR = decltype(par)::value;
     const int c = d >> 1;
-    auto xslot = [&](int m) { const int v = xb + m; return (kWSlots + (v >= 3 ? v - 3 : v)) * Q_CHUNK; };
+    auto xslot = [&](int m) { const int v = xb + m; return XBASE + (v >= 3 ? v - 3 : v) * XCH; };
     const int s_x = xslot(0), s_x1 = xslot(1), s_x2 = xslot(2);
     const uint32_t kx = d + 2 < ns ? (uint32_t)(d + 2) * Q_ROW : oobb;
     const uint32_t kw = c + 1 < nc ? (uint32_t)(c + 1) * Q_ROW : ooba;
@@ -331,21 +353,27 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
         dma_w(wslot(c + 1), kw, 2 * q);
         dma_w(wslot(c + 1), kw, 2 * q + 1);
       } else {
-        dma_x(s_x2, kx, 2 * q);
-        dma_x(s_x2, kx, 2 * q + 1);
+#pragma unroll
+        for (int k = 0; k < XD / 4; ++k) dma_x(s_x2, kx, XD / 4 * q + k);
       }
       na[q] = wfrag(wslot(c), 2 * PAR + 1, q);
-      nb[q] = xfrag(s_x, 1, q);
+      if (q < NJ) nb[q] = xfrag(s_x, 1, q);
       mfma_row(q);
-      SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_DSR, 1); SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_DSR, 1);
-      SGB(SG_MFMA, 1); SGB(SG_DSR, 1); SGB(SG_MFMA, 1);
+      if (NJ == 4) {
+        SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_DSR, 1); SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_DSR, 1);
+        SGB(SG_MFMA, 1); SGB(SG_DSR, 1); SGB(SG_MFMA, 1);
+      } else {
+        SGB(SG_MFMA, 1); SGB(SG_VMEM, 2); SGB(SG_DSR, 3); SGB(SG_MFMA, 1);
+      }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       a[i] = na[i];
-      b[i] = nb[i];
       sa[i] = pick(sa8[i], 2 * PAR + 1);
-      sb[i] = pick(sb8[i], 2 * PAR + 1);
+      if (i < NJ) {
+        b[i] = nb[i];
+        sb[i] = pick(sb8[i], 2 * PAR + 1);
+      }
     }
     // stage 1; the barrier that publishes slice d+1 after its second row block
 #pragma unroll
@@ -353,19 +381,19 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
       __builtin_amdgcn_sched_barrier(0);
       if (PAR == 0) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) dma_x(s_x2, kx, 4 * q + k);
+        for (int k = 0; k < XD / 2; ++k) dma_x(s_x2, kx, XD / 2 * q + k);
       }
       mfma_row(q);
       if (PAR == 0) {
-        SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_MFMA, 1); SGB(SG_VMEM, 1);
-        SGB(SG_MFMA, 1); SGB(SG_VMEM, 1);
+        SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_MFMA, 1); SGB(SG_VMEM, 1);
+        if (NJ == 4) { SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); }
       }
     }
     __builtin_amdgcn_sched_barrier(0);
     // in flight may be x of slice d+2 and, in an even slice, the W chunk
     // after this slice's (not needed before the next slice's end)
-    if (PAR == 0) wait_vm<2 * Q_DMA>();
-    else wait_vm<Q_DMA>();
+    if (PAR == 0) wait_vm<Q_DMA + XD>();
+    else wait_vm<XD>();
     wait_lgkm0();
     bare_barrier();
     const int sw1 = wslot(PAR == 1 ? c + 1 : c);
@@ -376,22 +404,26 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
 #pragma unroll
       for (int i = 2 * q - 4; i < 2 * q - 2; ++i) {
         na[i] = wfrag(sw1, u1, i);
-        nb[i] = xfrag(s_x1, 0, i);
+        if (i < NJ) nb[i] = xfrag(s_x1, 0, i);
       }
       mfma_row(q);
-      SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2);
-      SGB(SG_MFMA, 1);
+      if (NJ == 4) {
+        SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2);
+        SGB(SG_MFMA, 1);
+      } else {
+        SGB(SG_MFMA, 1); SGB(SG_DSR, 6); SGB(SG_MFMA, 1);
+      }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       a[i] = na[i];
-      b[i] = nb[i];
-      if (PAR == 1) {
-        sa8[i] = na8[i];
-        sb8[i] = nb8[i];
-      }
+      if (PAR == 1) sa8[i] = na8[i];
       sa[i] = pick(sa8[i], u1);
-      sb[i] = pick(sb8[i], u1);
+      if (i < NJ) {
+        b[i] = nb[i];
+        if (PAR == 1) sb8[i] = nb8[i];
+        sb[i] = pick(sb8[i], u1);
+      }
     }
     xb = xb + 1 >= 3 ? 0 : xb + 1;
   };
@@ -401,27 +433,43 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
   }
   __builtin_amdgcn_sched_barrier(0);
   wait_vm<0>();   // the zero-fill DMAs of the last slices land before LDS is reused
-  store_tile(acc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
+  store_tile<NJ>(acc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
+}
+
+template <int NJ>
+hipError_t launch_nj(const void* x, const uint8_t* xs, int T, int K, const uint8_t* w, const uint8_t* ws, int N,
+                     uint16_t* kv, hipStream_t s, const GateEpi& ep) {
+  const int tiles_n = (N + BM - 1) / BM, tiles_t = (T + 64 * NJ - 1) / (64 * NJ);
+  const dim3 grid(tiles_n * tiles_t), block(THREADS);
+  constexpr int lds = fp4_lds(NJ);
+  hipError_t e;
+  if (xs) {
+    if ((e = set_lds((const void*)gemm_fp4_mx_kernel<NJ>, lds)) != hipSuccess) return e;
+    hipLaunchKernelGGL(gemm_fp4_mx_kernel<NJ>, grid, block, lds, s, (const uint8_t*)x, xs, T, K, w, ws, N, kv,
+                       tiles_n, tiles_t, ep);
+  } else {
+    if ((e = set_lds((const void*)gemm_fp4_bf16_kernel<NJ>, lds)) != hipSuccess) return e;
+    hipLaunchKernelGGL(gemm_fp4_bf16_kernel<NJ>, grid, block, lds, s, (const uint16_t*)x, T, K, w, ws, N, kv,
+                       tiles_n, tiles_t, ep);
+  }
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_gemm_mxfp4(const void* x, const uint8_t* xs, int64_t T, int K, const uint8_t* w,
                              const uint8_t* ws, int N, void* kv, hipStream_t s, const GateEpi& ep) {
-  const int tiles_n = (N + BM - 1) / BM;
-  const int tiles_t = (int)((T + BN - 1) / BN);
-  const dim3 grid(tiles_n * tiles_t), block(THREADS);
-  hipError_t e;
-  if (xs) {
-    if ((e = set_lds((const void*)gemm_fp4_mx_kernel, Q_LDS)) != hipSuccess) return e;
-    hipLaunchKernelGGL(gemm_fp4_mx_kernel, grid, block, Q_LDS, s, (const uint8_t*)x, xs, (int)T, K, w, ws, N,
-                       (uint16_t*)kv, tiles_n, tiles_t, ep);
-  } else {
-    if ((e = set_lds((const void*)gemm_fp4_bf16_kernel, Q_LDS)) != hipSuccess) return e;
-    hipLaunchKernelGGL(gemm_fp4_bf16_kernel, grid, block, Q_LDS, s, (const uint16_t*)x, (int)T, K, w, ws, N,
-                       (uint16_t*)kv, tiles_n, tiles_t, ep);
-  }
-  return hipGetLastError();
+  // 256-token tiles move the fewest bytes a flop; a round of 128-token tiles
+  // costs 0.57 - 0.6 of a round of them, so those are taken where they need
+  // few enough rounds (K 2048, N 20480, bf16 x: T 300 42 -> 28 us, T 1000 88 ->
+  // 79, T 1500 stays at 96 against 113; K 1024, N 10240, T 515 25 -> 17 us).
+  // The gate's epilogue has the 256-token tile only.
+  const int64_t tiles_n = (N + BM - 1) / BM, cus = dev_info().num_cus;
+  const int64_t rounds256 = (tiles_n * ((T + 255) / 256) + cus - 1) / cus;
+  const int64_t rounds128 = (tiles_n * ((T + 127) / 128) + cus - 1) / cus;
+  if (!ep.hidden && 6 * rounds128 < 10 * rounds256)
+    return launch_nj<2>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep);
+  return launch_nj<4>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep);
 }
 
 }  // namespace engram

@@ -87,14 +87,17 @@ __device__ __forceinline__ void store_nt(uint16_t* dst, const uint4& v) {
 //    bf16-rounded keys ("vllm.models.deepseek_v41.amd.engram",
 //    _engram_gate_partials_kernel, at tile granularity), into
 //    ep.part[(h*T + t) * (dim/256) + tile].
-__device__ __forceinline__ void store_tile(f32x16 (&acc)[4][4], char* smem, uint16_t* __restrict__ kv,
+// NJ: 32-token blocks of a wave (4: a 256-token tile; 2: 128 tokens, plain
+// store only).
+template <int NJ = 4>
+__device__ __forceinline__ void store_tile(f32x16 (&acc)[4][NJ], char* smem, uint16_t* __restrict__ kv,
                                            int T, int N, int t0, int n0, int wn, int wt, int lane,
                                            int wave, const GateEpi& ep) {
   const int lrow = lane & 31, lhalf = lane >> 5;
   wait_lgkm0();
   bare_barrier();
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < NJ; ++j) {
     const int t = wt + j * 32 + lrow;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -112,11 +115,11 @@ __device__ __forceinline__ void store_tile(f32x16 (&acc)[4][4], char* smem, uint
   bare_barrier();
   const int c = lane & 31;
   auto lds_row = [&](int t) { return *reinterpret_cast<const uint4*>(smem + t * 512 + ((c ^ (t & 31)) << 4)); };
-  if (!ep.hidden) {
+  if (NJ < 4 || !ep.hidden) {
     const int n = n0 + c * 8;
 #pragma unroll 4
-    for (int it = 0; it < 32; ++it) {
-      const int t = wave * 64 + it * 2 + (lane >> 5);
+    for (int it = 0; it < 8 * NJ; ++it) {
+      const int t = wave * (16 * NJ) + it * 2 + (lane >> 5);
       const uint4 v = lds_row(t);
       if (t0 + t < T) {
         uint16_t* dst = kv + (int64_t)(t0 + t) * N + n;
