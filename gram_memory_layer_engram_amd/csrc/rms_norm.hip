@@ -16,11 +16,14 @@
 // Bound: HBM. Per element 2 bytes of x, 4 of residual in and out, 2 of out or
 // 1 + 1/32 of codes and scale; the weight row comes from L2.
 //
-// Layout: TPR threads own a row, each P pieces of 8 elements at a stride of
-// TPR pieces (16-byte loads, contiguous over a wave), all kept in registers
-// between the sum and the outputs: one pass over memory. A wave owns a row up
-// to dim 64*8*P; longer rows add their waves' sums through LDS in wave order.
-// An MX block is 4 neighbouring lanes' pieces: its maximum is two exchanges.
+// Layout: a row is owned by TPR threads. Each of its waves takes a contiguous
+// run of P * 64 pieces of 8 elements, lane l the pieces l, 64 + l, .. of the
+// run (16-byte loads, contiguous over the wave), all kept in registers between
+// the sum and the outputs: one pass over memory. Waves of one row add their
+// sums through LDS in wave order. An MX block is 4 neighbouring lanes' pieces:
+// its maximum is two quad permutations; the scale bytes of a wave's run (16 a
+// piece) are contiguous and leave as one store of 16 * P bytes through LDS.
+// Outputs go non-temporal: the kernel never reads them back.
 #include "common.h"
 #include "mx_rule.h"
 
@@ -40,47 +43,65 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
                     cvt_pk_bf16(f[6], f[7]));
 }
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ void store16_nt(uint16_t* dst, const uint4& v) {
+  const u32x4 w = {v.x, v.y, v.z, v.w};
+  __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(dst));
+}
+
+// v of the lane whose index differs in bit 0 (bit 1): quad permutations
+// [1,0,3,2] and [2,3,0,1].
+__device__ __forceinline__ uint32_t quad_xor1(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xf, 0xf, true);
+}
+__device__ __forceinline__ uint32_t quad_xor2(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xf, 0xf, true);
+}
+
 // Pointers are not __restrict__: residual_out may be residual and out may be
 // x; a thread reads all of its pieces before it writes any of them.
 template <int P, int TPR>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_rms_norm_kernel(const RmsNormArgs a) {
-  constexpr int RPB = TPR < 256 ? 256 / TPR : 1;   // rows per workgroup
+__global__ __launch_bounds__(TPR < 256 && 256 % TPR == 0 ? 256 : TPR) void add_rms_norm_kernel(const RmsNormArgs a) {
+  constexpr int BS = TPR < 256 && 256 % TPR == 0 ? 256 : TPR;
+  constexpr int RPB = BS / TPR;                    // rows per workgroup
   constexpr int WPR = TPR / 64;                    // waves per row
-  __shared__ float red[RPB * WPR];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int in_row = tid % TPR;
-  const int64_t row = (int64_t)blockIdx.x * RPB + tid / TPR;
-  const bool live = row < a.rows;
+  __shared__ float red[BS / 64];
+  __shared__ uint8_t sbytes[BS / 64][16 * P];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t row = (int64_t)blockIdx.x * RPB + wave / WPR;
+  const bool live = row < a.rows;                  // uniform per wave
   const int64_t t = live ? row / a.hc : 0;
   const int h = live ? (int)(row - t * a.hc) : 0;
-  const uint4* xr = reinterpret_cast<const uint4*>(a.x + t * a.x_st + h * a.x_sh);
-  const uint4* rr = a.residual ? reinterpret_cast<const uint4*>(a.residual + t * a.r_st + h * a.r_sh) : nullptr;
-  const uint4* wr = a.weight ? reinterpret_cast<const uint4*>(a.weight + (int64_t)(a.weight_hc > 1 ? h : 0) * a.dim)
-                             : nullptr;
   const int pieces = a.dim / 8;
+  const int i0 = wave % WPR * (P * 64) + lane;     // this lane's first piece
+  const uint4* xr = reinterpret_cast<const uint4*>(a.x + t * a.x_st + h * a.x_sh) + i0;
+  const uint4* rr = reinterpret_cast<const uint4*>(a.residual + t * a.r_st + h * a.r_sh) + i0;
 
   float s[P][8];
   uint4 xv[P], rv[P];
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     xv[p] = rv[p] = make_uint4(0, 0, 0, 0);
-    const int i = p * TPR + in_row;
-    if (live && i < pieces) {
-      xv[p] = xr[i];
-      if (rr) rv[p] = rr[i];
+    if (live && i0 + p * 64 < pieces) {
+      xv[p] = xr[p * 64];
+      if (a.residual) rv[p] = rr[p * 64];
     }
   }
   float sum = 0.f;
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    float r8[8];
     unpack8(xv[p], s[p]);
-    unpack8(rv[p], r8);
+    if (a.residual) {
+      float r8[8];
+      unpack8(rv[p], r8);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (rr) s[p][e] += r8[e];
-      sum = fmaf(s[p][e], s[p][e], sum);
+      for (int e = 0; e < 8; ++e) s[p][e] += r8[e];
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = fmaf(s[p][e], s[p][e], sum);
   }
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
@@ -95,55 +116,76 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_rms_norm_kernel(con
   const float inv = 1.0f / sqrtf(sum / (float)a.dim + a.eps);
   if (!live) return;
 
-  const int64_t base = row * pieces;
+  const uint4* wr = reinterpret_cast<const uint4*>(a.weight + (int64_t)(a.weight_hc > 1 ? h : 0) * a.dim) + i0;
+  const int64_t base = row * pieces + i0;
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    const int i = p * TPR + in_row;
     // the four lanes of an MX block are live together (dim % 32 == 0 then)
-    if (i >= pieces) break;
-    if (a.residual_out) reinterpret_cast<uint4*>(a.residual_out)[base + i] = pack8(s[p]);
+    if (i0 + p * 64 >= pieces) break;
+    if (a.residual_out) store16_nt(a.residual_out + (base + p * 64) * 8, pack8(s[p]));
     float y[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = s[p][e] * inv;
-    if (wr) {
+    if (a.weight) {
       float w8[8];
-      unpack8(wr[i], w8);
+      unpack8(wr[p * 64], w8);
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] *= w8[e];
     }
-    if (a.out) reinterpret_cast<uint4*>(a.out)[base + i] = pack8(y);
+    if (a.out) store16_nt(a.out + (base + p * 64) * 8, pack8(y));
     if (a.xq) {
       uint32_t amax = 0;   // magnitudes order like unsigned integers, NaN above infinity
 #pragma unroll
       for (int e = 0; e < 8; ++e) amax = max(amax, __float_as_uint(y[e]) & 0x7fffffffu);
-      amax = max(amax, (uint32_t)__shfl_xor((int)amax, 1, 64));
-      amax = max(amax, (uint32_t)__shfl_xor((int)amax, 2, 64));
+      amax = max(amax, quad_xor1(amax));
+      amax = max(amax, quad_xor2(amax));
       uint32_t packed[2];
       const int byte = mx_piece_f32(y, amax, packed);
-      reinterpret_cast<uint2*>(a.xq)[base + i] = make_uint2(packed[0], packed[1]);
-      if ((lane & 3) == 0) a.xs[(base + i) >> 2] = (uint8_t)byte;
+      const u32x2 c = {packed[0], packed[1]};
+      __builtin_nontemporal_store(c, reinterpret_cast<u32x2*>(a.xq + (base + p * 64) * 8));
+      if ((lane & 3) == 0) sbytes[wave][p * 16 + (lane >> 2)] = (uint8_t)byte;
+    }
+  }
+  if (a.xq) {
+    // the run's scale bytes: written and read by this wave alone
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    const int n = min(P * 64, pieces - wave % WPR * (P * 64)) / 4;   // bytes of the run (negative: none)
+    uint8_t* dst = a.xs + (row * pieces + wave % WPR * (P * 64)) / 4;
+    if (lane < n) {
+#pragma unroll
+      for (int k = 0; k < (P + 3) / 4; ++k)
+        if (lane + 64 * k < n) dst[lane + 64 * k] = sbytes[wave][lane + 64 * k];
     }
   }
 }
 
 template <int P, int TPR>
 hipError_t launch(const RmsNormArgs& a, hipStream_t s) {
-  constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
-  constexpr int BS = TPR < 256 ? 256 : TPR;
+  constexpr int BS = TPR < 256 && 256 % TPR == 0 ? 256 : TPR, RPB = BS / TPR;
   hipLaunchKernelGGL((add_rms_norm_kernel<P, TPR>), dim3((uint32_t)((a.rows + RPB - 1) / RPB)), dim3(BS), 0, s, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
+// Few rows: latency counts, one piece a thread (T 1, four rows of 4096: 3.1 us
+// with 512 threads a row, 3.7 with 256). Many: four pieces a thread keep more
+// bytes in flight per wave.
 hipError_t launch_add_rms_norm(const RmsNormArgs& a, hipStream_t s) {
   const int pieces = a.dim / 8;
   if (pieces <= 64) return launch<1, 64>(a, s);
+  if (a.rows <= dev_info().num_cus) {
+    if (pieces <= 128) return launch<1, 128>(a, s);
+    if (pieces <= 256) return launch<1, 256>(a, s);
+    if (pieces <= 512) return launch<1, 512>(a, s);
+    if (pieces <= 1024) return launch<1, 1024>(a, s);
+    return launch<2, 1024>(a, s);   // dim <= 16384
+  }
   if (pieces <= 128) return launch<2, 64>(a, s);
-  if (pieces <= 256) return launch<1, 256>(a, s);
-  if (pieces <= 512) return launch<2, 256>(a, s);
+  if (pieces <= 256) return launch<4, 64>(a, s);
+  if (pieces <= 512) return launch<4, 128>(a, s);
   if (pieces <= 1024) return launch<4, 256>(a, s);
-  return launch<8, 256>(a, s);   // dim <= 16384
+  return launch<4, 512>(a, s);
 }
 
 }  // namespace engram
