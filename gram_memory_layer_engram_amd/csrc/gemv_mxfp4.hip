@@ -67,8 +67,8 @@ struct Gemv4Args {
 // x moves in units of JG token tiles of one k step, UPS units a step.
 constexpr int f4_jg(bool a8, int nt) { return a8 || nt < 2 ? nt : 2; }
 constexpr int f4_ups(bool a8, int nt) { return nt / f4_jg(a8, nt); }
-// W steps in the ring when XS units of x are in flight
-constexpr int f4_dw(bool a8, int nt, int xs) { return f4_ups(a8, nt) == 1 ? xs : 2; }
+// W steps in the ring when XS units of x are (two units a step: one at a time)
+constexpr int f4_dw(bool a8, int nt, int xs) { return f4_ups(a8, nt) == 1 ? xs : 1; }
 constexpr int f4_xunit(bool a8, int nt) { return f4_jg(a8, nt) * (a8 ? 2048 : 4096); }
 constexpr int f4_wave_bytes(bool a8, int rt, int nt, int xs) {
   return f4_dw(a8, nt, xs) * rt * 1024 + xs * f4_xunit(a8, nt);
@@ -90,7 +90,7 @@ __global__ __launch_bounds__(WAVES * 64) void gemv_mxfp4_kernel(
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   constexpr int JG = f4_jg(A8, NT), UPS = f4_ups(A8, NT), DW = f4_dw(A8, NT, XS);
   constexpr int XUNIT = f4_xunit(A8, NT), XI = XUNIT / 1024;   // DMAs of a unit of x
-  static_assert(UPS == 1 || (UPS == 2 && XS == 3), "ring schedule");
+  static_assert(UPS == 1 || XS == 1, "ring schedule");
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n0 = blockIdx.x * 16 * RT, rows = min(16 * RT, N - n0);
@@ -155,9 +155,8 @@ __global__ __launch_bounds__(WAVES * 64) void gemv_mxfp4_kernel(
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[rt][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // DMAs of the units after the one at hand that may still fly: with two units
-  // a step and three in flight one of the next two brings a W step
-  constexpr int AHEAD = UPS == 1 ? (XS - 1) * (RT + XI) : RT + 2 * XI;
+  // DMAs of the units after the one at hand that may still fly
+  constexpr int AHEAD = (XS - 1) * (RT + XI);
   for (int u = 0; u < XS; ++u)
     if (u < units) issue(u);
   // the scale bytes of all waves
@@ -288,8 +287,8 @@ hipError_t f4_small(const Gemv4Args& a, hipStream_t s) {
 
 // More x: one workgroup fills a compute unit's LDS, and each reads all of x,
 // so as few as fill the compute units once: the least row-tile count that
-// does, at most 5 (N 20480, K 2048, T 61, bf16 x: 13.5 us, two tiles in
-// three rounds 19.2), less where the scale bytes of a long K do not fit.
+// does, at most 5 (N 20480, K 2048, T 61, bf16 x: 12.2 us, two tiles in
+// three rounds 19), less where the scale bytes of a long K do not fit.
 template <bool A8, int NT, int WAVES, int XS>
 hipError_t f4_large(const Gemv4Args& a, hipStream_t s) {
   const int tiles = (a.N + 15) / 16, cus = dev_info().num_cus, kb = a.K / 32;
@@ -312,14 +311,14 @@ bool gemv_mxfp4_supported(int64_t T, int K, bool x_mxfp8) {
   if (x_mxfp8) return (T <= 16 ? f4_lds(true, 1, 1, 4, 1, kb) : T <= 32 ? f4_lds(true, 1, 2, 4, 1, kb)
                                                                         : f4_lds(true, 1, 4, 4, 2, kb)) <= kLds;
   return (T <= 16 ? f4_lds(false, 1, 1, 4, 1, kb) : T <= 32 ? f4_lds(false, 1, 2, 8, 1, kb)
-                                                            : f4_lds(false, 1, 4, 4, 3, kb)) <= kLds;
+                                                            : f4_lds(false, 1, 4, 8, 1, kb)) <= kLds;
 }
 
 hipError_t launch_gemv_mxfp4(const void* x, const uint8_t* xs, int64_t T, int K, const void* w, const uint8_t* ws,
                              int N, void* kv, hipStream_t s) {
   const Gemv4Args a{x, xs, (const uint8_t*)w, ws, (uint16_t*)kv, (int)T, K, N};
   if (xs) return T <= 16 ? f4_small<true, 1>(a, s) : T <= 32 ? f4_small<true, 2>(a, s) : f4_large<true, 4, 4, 2>(a, s);
-  return T <= 16 ? f4_small<false, 1>(a, s) : T <= 32 ? f4_large<false, 2, 8, 1>(a, s) : f4_large<false, 4, 4, 3>(a, s);
+  return T <= 16 ? f4_small<false, 1>(a, s) : T <= 32 ? f4_large<false, 2, 8, 1>(a, s) : f4_large<false, 4, 8, 1>(a, s);
 }
 
 }  // namespace engram

@@ -175,24 +175,21 @@ def _format(w: torch.Tensor, w_scales, K: int) -> int:
 
 
 def _check_mxfp4(w: torch.Tensor, w_scales: torch.Tensor, N: int, K: int) -> None:
-    _dense(w_scales, "w_scales")
-    if w.dtype != torch.uint8 or w_scales.dtype != torch.uint8 or w_scales.shape != (N, K // 32):
-        raise ValueError("MXFP4 wkv needs uint8 codes [N, K/2] and uint8 scales [N, K/32]")
+    if (w.dtype != torch.uint8 or w_scales.dtype != torch.uint8 or w_scales.shape != (N, K // 32)
+            or not w_scales.is_contiguous()):
+        raise ValueError("MXFP4 wkv needs uint8 codes [N, K/2] and contiguous uint8 scales [N, K/32]")
 
 
 def _device_of(*tensors) -> int:
     """The one device (its index) all given tensors are on, None left out."""
-    dev = None
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("libengram takes device tensors only")
-        i = t.get_device()
-        if dev is None:
-            dev = i
-        elif i != dev:
-            raise ValueError(f"tensors on cuda:{dev} and cuda:{i}: one device is needed")
+        if t is not None:
+            i = t.get_device()
+            if i < 0 or not t.is_cuda:
+                raise ValueError("libengram takes device tensors only")
+            if i != dev:
+                raise ValueError(f"tensors on cuda:{dev} and cuda:{i}: one device is needed")
     return dev
 
 
@@ -200,7 +197,7 @@ def _run_on(dev: int, fn, *args) -> None:
     """fn(*args, stream) with device dev current, on its current stream. (The
     raw stream number: a Stream object costs a microsecond, a fifth of a decode
     kernel.)"""
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
@@ -282,7 +279,8 @@ def wkv(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor | None = None,
         _check_mxfp4(w, w_scales, N, K)
         if x.dtype != torch.bfloat16:
             raise ValueError("MXFP4 wkv needs bf16 x (wkv_mx takes MXFP8 activations)")
-        return _product(L, L.engram_wkv, L.engram_wkv_workspace_size, (x,), T, K, w, w_scales, fmt, N, kv, workspace)
+        return _product(L, L.engram_wkv, L.engram_wkv_workspace_size, (x.data_ptr(),), x.get_device(), T, K, w,
+                        w_scales, fmt, N, kv, workspace)
     if w.dim() != 2 or w.shape[1] != K:
         raise ValueError(f"w must be [N, {K}], got {tuple(w.shape)}")
     if fmt == W_MXFP8:
@@ -302,23 +300,27 @@ def wkv(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor | None = None,
     return kv
 
 
-def _product(L, fn, workspace_size, x, T, K, w, w_scales, fmt, N, kv, workspace):
+def _product(L, fn, workspace_size, xp, dev, T, K, w, w_scales, fmt, N, kv, workspace):
     """Output, workspace and call of a projection whose operands are checked;
-    x is (x,) or (codes, scales)."""
-    dev = _device_of(*x, w, w_scales, kv, workspace)
+    xp: x's address, or those of its codes and scales; dev: its device."""
+    if w.get_device() != dev or w_scales.get_device() != dev or dev < 0:
+        _device_of(w, w_scales)
+        raise ValueError("x and w are on different devices")
     if kv is None:
-        kv = torch.empty((T, N), dtype=torch.bfloat16, device=w.device)
-    elif kv.shape != (T, N) or kv.dtype != torch.bfloat16 or not kv.is_contiguous():
-        raise ValueError(f"kv must be bf16 [{T}, {N}], contiguous")
-    need = workspace_size(T, K, N, fmt)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=w.device)
+        kv = w.new_empty((T, N), dtype=torch.bfloat16)
+    elif kv.shape != (T, N) or kv.dtype != torch.bfloat16 or not kv.is_contiguous() or kv.get_device() != dev:
+        raise ValueError(f"kv must be bf16 [{T}, {N}], contiguous, on x's device")
+    ws, ws_bytes = None, 0
     if workspace is None:
-        ws, ws_bytes = None, 0
+        ws_bytes = workspace_size(T, K, N, fmt)
+        if ws_bytes:
+            workspace = w.new_empty(ws_bytes)
+            ws = workspace.data_ptr()
     else:
+        if workspace.get_device() != dev:
+            raise ValueError("workspace must be on x's device")
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _run_on(dev, fn, *[t.data_ptr() for t in x], T, K, w.data_ptr(), w_scales.data_ptr(), fmt, N, kv.data_ptr(), ws,
-            ws_bytes)
+    _run_on(dev, fn, *xp, T, K, w.data_ptr(), w_scales.data_ptr(), fmt, N, kv.data_ptr(), ws, ws_bytes)
     return kv
 
 
@@ -342,8 +344,10 @@ def wkv_mx(xq: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, w_scales: torch.
     else:
         raise ValueError(f"w must be [N, {K}] with scales [N/32, {K // 32}] (MXFP8) or [N, {K // 2}] with "
                          f"[N, {K // 32}] (MXFP4)")
-    return _product(L, L.engram_wkv_mx, L.engram_wkv_mx_workspace_size, (xq, xs), T, K, w, w_scales, fmt, N, kv,
-                    workspace)
+    if xq.get_device() != xs.get_device():
+        raise ValueError("xq and xs are on different devices")
+    return _product(L, L.engram_wkv_mx, L.engram_wkv_mx_workspace_size, (xq.data_ptr(), xs.data_ptr()),
+                    xq.get_device(), T, K, w, w_scales, fmt, N, kv, workspace)
 
 
 def add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None = None, weight: torch.Tensor | None = None,
@@ -379,7 +383,7 @@ def add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None = None, weight: 
         if residual.dtype != bf16 or residual.shape != shape or (residual.stride(-1) != 1 and dim > 1):
             raise ValueError(f"residual must be bf16 {tuple(shape)}, contiguous in its last dimension")
         if residual_out is None:
-            residual_out = torch.empty(shape, dtype=bf16, device=x.device)
+            residual_out = x.new_empty(shape)
         elif residual_out.shape != shape or residual_out.dtype != bf16 or not residual_out.is_contiguous():
             raise ValueError(f"residual_out must be bf16 {tuple(shape)}, contiguous")
         rp, rop, rst = residual.data_ptr(), residual_out.data_ptr(), residual.stride(0)
@@ -395,7 +399,7 @@ def add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None = None, weight: 
     op = None
     if out_format == "bf16" or out_format == "both":
         if out is None:
-            out = torch.empty(shape, dtype=bf16, device=x.device)
+            out = x.new_empty(shape)
         elif out.shape != shape or out.dtype != bf16 or not out.is_contiguous():
             raise ValueError(f"out must be bf16 {tuple(shape)}, contiguous")
         op = out.data_ptr()
@@ -407,11 +411,11 @@ def add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None = None, weight: 
     if out_format != "bf16":
         scales = (*shape[:-1], dim // 32)
         if xq is None:
-            xq = torch.empty(shape, dtype=torch.uint8, device=x.device)
+            xq = x.new_empty(shape, dtype=torch.uint8)
         elif xq.shape != shape or xq.dtype != torch.uint8 or not xq.is_contiguous():
             raise ValueError(f"xq must be uint8 {tuple(shape)}, contiguous")
         if xs is None:
-            xs = torch.empty(scales, dtype=torch.uint8, device=x.device)
+            xs = x.new_empty(scales, dtype=torch.uint8)
         elif xs.shape != scales or xs.dtype != torch.uint8 or not xs.is_contiguous():
             raise ValueError(f"xs must be uint8 {scales}, contiguous")
         qp, sp = xq.data_ptr(), xs.data_ptr()

@@ -19,7 +19,7 @@ import torch
 
 from oracle import engram_oracle as o
 from tests._block_inputs import BF16_U, F32_U, bf16, mxfp4_weight, mxfp8_rows, product_tolerance
-from tests._util import bf16_values, bits, u8
+from tests._util import bf16_values, bits, sample_tokens, u8
 
 pytestmark = pytest.mark.gpu
 
@@ -493,3 +493,82 @@ class _FakeOther:
 
     def get_device(self):
         return 7
+
+
+@pytest.mark.parametrize("op", ["wkv", "wkv_mx"])
+@pytest.mark.parametrize("T,K,N", [(1500, 256, 20480), (4096, 512, 5120 - 4)])
+def test_mxfp4_many_tiles(op, T, K, N):
+    """More rounds of tiles than compute units, in which the 256-token tiles of
+    the GEMM run, ragged in T and N; a token from every tile and some more."""
+    E = _E()
+    rng = np.random.default_rng(K)
+    wq, ws = mxfp4_weight(rng, N, K)
+    wa = o.mxfp4_dequantize_weight(wq, ws)
+    wd, sd = torch.from_numpy(wq).to(DEV), torch.from_numpy(ws).to(DEV)
+    toks = sample_tokens(T, 48, seed=1, tile=128)
+    if op == "wkv":
+        x = bf16(rng, T, K)
+        xa = o.bf16_to_f64(bits(x))
+        kv = E.wkv(x.to(DEV), wd, sd)
+    else:
+        xq, xs = mxfp8_rows(rng, T, K)
+        xa = o.mx_dequantize_activations(xq, xs)
+        kv = E.wkv_mx(torch.from_numpy(xq).to(DEV), torch.from_numpy(xs).to(DEV), wd, sd)
+    ref, tol = product_tolerance(xa[toks], wa, scaled=op == "wkv_mx")
+    _inside(bf16_values(bits(kv[torch.from_numpy(toks).to(DEV)])), ref, tol, op)
+
+
+@pytest.mark.parametrize("T,K,N", [(1, 32768, 36), (20, 32768, 36), (50, 36864, 20), (40, 131072, 32), (3, 163840, 8),
+                                   (64, 131072 + 128, 4)])
+def test_mxfp4_long_k(T, K, N):
+    """K past what a compute unit's LDS holds scale bytes for: the tiled GEMM,
+    and the GEMV just below that."""
+    E = _E()
+    rng = np.random.default_rng(K + T)
+    wq, ws = mxfp4_weight(rng, N, K)
+    wa = o.mxfp4_dequantize_weight(wq, ws)
+    wd, sd = torch.from_numpy(wq).to(DEV), torch.from_numpy(ws).to(DEV)
+    x = bf16(rng, T, K)
+    ref, tol = product_tolerance(o.bf16_to_f64(bits(x)), wa)
+    _inside(bf16_values(bits(E.wkv(x.to(DEV), wd, sd))), ref, tol, "wkv")
+    xq, xs = mxfp8_rows(rng, T, K)
+    got = E.wkv_mx(torch.from_numpy(xq).to(DEV), torch.from_numpy(xs).to(DEV), wd, sd)
+    ref, tol = product_tolerance(o.mx_dequantize_activations(xq, xs), wa, scaled=True)
+    _inside(bf16_values(bits(got)), ref, tol, "wkv_mx")
+
+
+@pytest.mark.parametrize("T,dim,hc,K", [(1, 256, 1, 512), (64, 512, 2, 256), (300, 768, 2, 512), (70, 256, 3, 384)])
+def test_mxfp4_gate_partials(T, dim, hc, K):
+    """The projection fused with the gate's sums: the value block within the
+    product's tolerance, the sums those of the bf16 keys of engram_wkv's tiled
+    kernel to the gate tests' tolerance."""
+    E = _E()
+    rng = np.random.default_rng(T + dim)
+    N = (hc + 1) * dim
+    wq, ws = mxfp4_weight(rng, N, K, 116, 122)
+    wa = o.mxfp4_dequantize_weight(wq, ws)
+    x, hidden = bf16(rng, T, K), bf16(rng, T, hc, dim)
+    q = (1 + 0.1 * bf16(rng, hc, dim).float()).to(torch.bfloat16)
+    k = (1 + 0.1 * bf16(rng, hc, dim).float()).to(torch.bfloat16)
+    args = [t.to(DEV) for t in (x, torch.from_numpy(wq), torch.from_numpy(ws), hidden, q, k)]
+    value, parts = E.wkv_gate_partials(*args)
+    ref, tol = product_tolerance(o.bf16_to_f64(bits(x)), wa)
+    _inside(bf16_values(bits(value)), ref[:, hc * dim:], tol[:, hc * dim:], "value")
+    keys = ref[:, :hc * dim].reshape(T, hc, dim // 256, 256)
+    kt = tol[:, :hc * dim].reshape(T, hc, dim // 256, 256)
+    h = o.bf16_to_f64(bits(hidden)).reshape(T, hc, dim // 256, 256)
+    qk = (o.bf16_to_f64(bits(q)) * o.bf16_to_f64(bits(k))).reshape(1, hc, dim // 256, 256)
+    got = parts.cpu().numpy().astype(np.float64)
+    for i, c in ((0, h * qk), (1, None)):
+        if c is None:
+            want = (keys ** 2).sum(-1)
+            lim = (2 * np.abs(keys) * kt + kt ** 2).sum(-1)
+            mass = want
+        else:
+            want = (c * keys).sum(-1)
+            lim = (np.abs(c) * kt).sum(-1)
+            mass = (np.abs(c * keys)).sum(-1)
+        # each key within its tolerance, then 256 fp32 products (3 roundings) and their sum
+        lim = lim + (256 + 4) * F32_U * (mass + lim)
+        err = np.abs(got[..., i] - want.transpose(1, 0, 2))
+        assert np.all(err <= lim.transpose(1, 0, 2)), (i, float((err - lim.transpose(1, 0, 2)).max()))

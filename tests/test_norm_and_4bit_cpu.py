@@ -78,11 +78,14 @@ def test_mxfp4_projection_refusals(lib):
         assert wkv(**bad) == INV, bad
     for bad in (dict(K=192), dict(K=1 << 21), dict(N=66)):
         assert wkv(**bad) == UNS, bad
-    need = lib.engram_wkv_workspace_size(300, 256, 64, F4)
-    assert need > 0
-    assert wkv(T=300, nbytes=need - 1) == INV
-    assert wkv(T=300, ws=None) == INV
-    assert wkv(T=300, ws=P + 16) == INV
+    # a workspace only where the weight is expanded: past the GEMV and K % 256 != 0
+    assert lib.engram_wkv_workspace_size(300, 256, 64, F4) == 0
+    assert lib.engram_wkv_workspace_size(64, 384, 64, F4) == 0
+    need = lib.engram_wkv_workspace_size(300, 384, 64, F4)
+    assert need >= 384 * 64 * 2
+    assert wkv(T=300, K=384, nbytes=need - 1) == INV
+    assert wkv(T=300, K=384, ws=None) == INV
+    assert wkv(T=300, K=384, ws=P + 16) == INV
     assert lib.engram_wkv_workspace_size(0, 256, 64, F4) == 0
 
     def mx(T=4, K=256, N=64, xq=P, xs=P, w=P, s=P, f=F4, kv=P, ws=P, nbytes=big):
@@ -97,20 +100,21 @@ def test_mxfp4_projection_refusals(lib):
     assert mx(f=F8, N=36) == UNS
     assert mx(f=BF, s=None) == UNS
     assert mx(f=7) == INV
-    need = lib.engram_wkv_mx_workspace_size(300, 256, 64, F4)
-    assert need > 0 and lib.engram_wkv_mx_workspace_size(300, 256, 64, F8) == 0
-    assert mx(T=300, nbytes=need - 1) == INV and mx(T=300, ws=None) == INV
+    assert lib.engram_wkv_mx_workspace_size(300, 256, 64, F4) == 0
+    need = lib.engram_wkv_mx_workspace_size(300, 384, 64, F4)
+    assert need >= 384 * 64 * 2 + 300 * 384 * 2 and lib.engram_wkv_mx_workspace_size(300, 384, 64, F8) == 0
+    assert mx(T=300, K=384, nbytes=need - 1) == INV and mx(T=300, K=384, ws=None) == INV
 
 
 def test_forward_mxfp4_refusals_and_workspace(lib):
     from gram_memory_layer_engram_amd import engram
 
     a = engram.ForwardArgs()
-    a.T, a.hc, a.dim, a.n_cols, a.head_dim = 300, 4, 4096, 16, 128
+    a.T, a.hc, a.dim, a.n_cols, a.head_dim = 500, 4, 4096, 3, 128
     a.w_format = engram.W_BF16
     plain = lib.engram_forward_workspace_size(ctypes.byref(a))
     a.w_format = engram.W_MXFP4
-    assert lib.engram_forward_workspace_size(ctypes.byref(a)) >= plain + 20480 * 2048
+    assert lib.engram_forward_workspace_size(ctypes.byref(a)) >= plain + 20480 * 384 * 2
     # the expanded weight does not fit the fixed scratch
     a.table = a.hash_ids = a.w = a.w_scales = a.hidden = a.q_weight = a.k_weight = a.out = P
     a.num_rows, a.ids_stride_t, a.ids_stride_c = 10, 16, 1
