@@ -374,51 +374,67 @@ def add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None = None, weight: 
         (xst, xsd), xsh = x.stride(), 0
     else:
         raise ValueError("x must be [T, hc, dim] or [T, dim]")
-    dev = _device_of(x, residual, weight, residual_out, out, xq, xs)
-    bf16 = torch.bfloat16
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError("libengram takes device tensors only")
+    bf16, u8 = torch.bfloat16, torch.uint8
     if x.dtype != bf16 or (xsd != 1 and dim > 1):
         raise ValueError("x must be bf16, contiguous in its last dimension")
+
+    def given(t, name, dtype, size):
+        if t.dtype != dtype or t.shape != size or not t.is_contiguous() or t.get_device() != dev:
+            raise ValueError(f"{name} must be {dtype} {tuple(size)}, contiguous, on x's device")
+        return t.data_ptr()
+
     rp, rst, rsh, rop = None, 0, 0, None
     if residual is not None:
-        if residual.dtype != bf16 or residual.shape != shape or (residual.stride(-1) != 1 and dim > 1):
+        rstride = residual.stride()
+        if residual.dtype != bf16 or residual.shape != shape or (rstride[-1] != 1 and dim > 1):
             raise ValueError(f"residual must be bf16 {tuple(shape)}, contiguous in its last dimension")
+        if residual.get_device() != dev:
+            _device_of(x, residual)
+        rp, rst, rsh = residual.data_ptr(), rstride[0], rstride[1] if len(shape) == 3 else 0
         if residual_out is None:
             residual_out = x.new_empty(shape)
-        elif residual_out.shape != shape or residual_out.dtype != bf16 or not residual_out.is_contiguous():
-            raise ValueError(f"residual_out must be bf16 {tuple(shape)}, contiguous")
-        rp, rop, rst = residual.data_ptr(), residual_out.data_ptr(), residual.stride(0)
-        rsh = residual.stride(1) if len(shape) == 3 else 0
+            rop = residual_out.data_ptr()
+        else:
+            rop = given(residual_out, "residual_out", bf16, shape)
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     wp, whc = None, 1
     if weight is not None:
-        if weight.dtype != bf16 or not weight.is_contiguous() or weight.shape not in ((dim,), (hc, dim), (1, dim)):
+        ws = weight.shape
+        if len(ws) == 2:
+            whc = ws[0]
+        if weight.dtype != bf16 or not weight.is_contiguous() or not 1 <= len(ws) <= 2 or ws[-1] != dim or (
+                whc != 1 and whc != hc):
             raise ValueError(f"weight must be bf16 [{dim}] or [{hc}, {dim}], contiguous")
+        if weight.get_device() != dev:
+            _device_of(x, weight)
         wp = weight.data_ptr()
-        whc = weight.shape[0] if weight.dim() == 2 else 1
-    op = None
-    if out_format == "bf16" or out_format == "both":
+    op = qp = sp = None
+    if out_format != "mxfp8":
+        if out_format != "bf16" and out_format != "both":
+            raise ValueError('out_format must be "bf16", "mxfp8" or "both"')
         if out is None:
             out = x.new_empty(shape)
-        elif out.shape != shape or out.dtype != bf16 or not out.is_contiguous():
-            raise ValueError(f"out must be bf16 {tuple(shape)}, contiguous")
-        op = out.data_ptr()
-    elif out_format != "mxfp8":
-        raise ValueError('out_format must be "bf16", "mxfp8" or "both"')
+            op = out.data_ptr()
+        else:
+            op = given(out, "out", bf16, shape)
     elif out is not None:
         raise ValueError('out is not written with out_format "mxfp8"')
-    qp, sp = None, None
     if out_format != "bf16":
-        scales = (*shape[:-1], dim // 32)
         if xq is None:
-            xq = x.new_empty(shape, dtype=torch.uint8)
-        elif xq.shape != shape or xq.dtype != torch.uint8 or not xq.is_contiguous():
-            raise ValueError(f"xq must be uint8 {tuple(shape)}, contiguous")
+            xq = x.new_empty(shape, dtype=u8)
+            qp = xq.data_ptr()
+        else:
+            qp = given(xq, "xq", u8, shape)
+        scales = shape[:-1] + (dim // 32,)
         if xs is None:
-            xs = x.new_empty(scales, dtype=torch.uint8)
-        elif xs.shape != scales or xs.dtype != torch.uint8 or not xs.is_contiguous():
-            raise ValueError(f"xs must be uint8 {scales}, contiguous")
-        qp, sp = xq.data_ptr(), xs.data_ptr()
+            xs = x.new_empty(scales, dtype=u8)
+            sp = xs.data_ptr()
+        else:
+            sp = given(xs, "xs", u8, scales)
     elif xq is not None or xs is not None:
         raise ValueError('xq and xs are not written with out_format "bf16"')
     # the stride of a dimension of one element is never used, whatever torch says it is
