@@ -27,37 +27,38 @@ namespace engram {
 namespace {
 
 constexpr int kWSlots = 2, kXSlots = 3;
-// A block's token tile is 64 * NJ: 256, or 128 where that fills the compute
-// units better (launch_gemm_mxfp4).
-constexpr int x_slot(int nj) { return 64 * nj * Q_ROW; }
-constexpr int x_dma(int nj) { return 2 * nj; }                  // DMAs of a wave per x slice
-constexpr int fp4_lds(int nj) {
-  const int ring = kWSlots * Q_CHUNK + kXSlots * x_slot(nj), epi = 64 * nj * 512;
+// A block is 64 * NI W rows x 64 * NJ tokens: 256 x 256, 256 x 128, or 128 x
+// 128 with two workgroups on a compute unit (launch_gemm_mxfp4).
+constexpr int op_slot(int n) { return 64 * n * Q_ROW; }       // an operand's chunk or slice in LDS
+constexpr int op_dma(int n) { return 2 * n; }                 // a wave's DMAs for it
+constexpr int fp4_lds(int ni, int nj) {
+  const int ring = kWSlots * op_slot(ni) + kXSlots * op_slot(nj), epi = 64 * nj * 128 * ni;
   return ring > epi ? ring : epi;
 }
-static_assert(fp4_lds(4) == Q_LDS, "LDS budget");
+static_assert(fp4_lds(4, 4) == Q_LDS && 2 * fp4_lds(2, 2) <= Q_LDS, "LDS budget");
 constexpr int SG_VALU = 0x002;
 
 template <int V> using Int = std::integral_constant<int, V>;
 
-template <int NJ>
-__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(1, 1)))
+template <int NI, int NJ>
+__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(NI == 4 ? 1 : 2, NI == 4 ? 1 : 2)))
 void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const uint8_t* __restrict__ w,
                           const uint8_t* __restrict__ ws, int N, uint16_t* __restrict__ kv, int tiles_n,
                           int tiles_t, GateEpi ep) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   int tn, tt;
   tile_of(blockIdx.x, tiles_n, tiles_t, tn, tt);
-  constexpr int TN = 64 * NJ, XCH = x_slot(NJ), XD = x_dma(NJ), XBASE = kWSlots * Q_CHUNK;
-  const int n0 = tn * BM, t0 = tt * TN;
+  constexpr int TM = 64 * NI, TN = 64 * NJ, WCH = op_slot(NI), XCH = op_slot(NJ), WD = op_dma(NI), XD = op_dma(NJ);
+  constexpr int XBASE = kWSlots * WCH;
+  const int n0 = tn * TM, t0 = tt * TN;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wn = (wave >> 1) * 128, wt = (wave & 1) * (32 * NJ);
+  const int wn = (wave >> 1) * (32 * NI), wt = (wave & 1) * (32 * NJ);
   const uint32_t wpitch = (uint32_t)K / 2u, xpitch = (uint32_t)K * 2u, kb = (uint32_t)K / 32u;
-  const rsrc_t ra = make_rsrc(w + (int64_t)n0 * wpitch, (uint32_t)min(BM, N - n0) * wpitch);
+  const rsrc_t ra = make_rsrc(w + (int64_t)n0 * wpitch, (uint32_t)min(TM, N - n0) * wpitch);
   const rsrc_t rb = make_rsrc(x + (int64_t)t0 * K, (uint32_t)min(TN, T - t0) * xpitch);
-  const rsrc_t rs = make_rsrc(ws + (int64_t)n0 * kb, (uint32_t)min(BM, N - n0) * kb);
-  const uint32_t ooba = (uint32_t)BM * wpitch, oobb = (uint32_t)TN * xpitch;   // at or past the ranges
+  const rsrc_t rs = make_rsrc(ws + (int64_t)n0 * kb, (uint32_t)min(TM, N - n0) * kb);
+  const uint32_t ooba = (uint32_t)TM * wpitch, oobb = (uint32_t)TN * xpitch;   // at or past the ranges
   const int nk = K / 64, nc = K / 256;
 
   const dma::Lane la = dma::lane_of(wave, lane, wpitch), lb = dma::lane_of(wave, lane, xpitch);
@@ -74,12 +75,12 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
   const int fsw = (lrow >> 1) & 7;
   // the 8 scale bytes of a chunk (256 k) of this lane's four rows; byte
   // 2*PAR + h is slice PAR's
-  uint32_t srow[4];
+  uint32_t srow[NI];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) srow[i] = (uint32_t)(wn + i * 32 + lrow) * kb;
-  auto scales8 = [&](int c, u32x2 (&s8)[4]) {
+  for (int i = 0; i < NI; ++i) srow[i] = (uint32_t)(wn + i * 32 + lrow) * kb;
+  auto scales8 = [&](int c, u32x2 (&s8)[NI]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s8[i] = __builtin_amdgcn_raw_buffer_load_b64(rs, srow[i] + 8u * (uint32_t)c, 0, 0);
+    for (int i = 0; i < NI; ++i) s8[i] = __builtin_amdgcn_raw_buffer_load_b64(rs, srow[i] + 8u * (uint32_t)c, 0, 0);
   };
   // byte 2*par + h in the exponent field of an fp32 (the conversion reads no
   // other bits of its scale)
@@ -88,17 +89,17 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
     return __uint_as_float(((par < 2 ? v.x : v.y) >> ((uint32_t)(16 * (par & 1)) + lsh)) << 23);
   };
 
-  f32x16 acc[4][NJ];
+  f32x16 acc[NI][NJ];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < NI; ++i)
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-  bf16x8_t a[2][4], b[2][NJ];
-  i32x4 raw[4];
-  float sc[4];
+  bf16x8_t a[2][NI], b[2][NJ];
+  i32x4 raw[NI];
+  float sc[NI];
   auto read_raw = [&](int slot, int par, int i) {
     raw[i] = *reinterpret_cast<const i32x4*>(smem + slot + (wn + i * 32 + lrow) * Q_ROW +
                                              (((2 * par + lhalf) ^ fsw) << 4));
@@ -118,14 +119,14 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
     for (int j = 0; j < NJ; ++j)
       acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[c][i], b[c][j], acc[i][j], 0, 0, 0);
   };
-  auto wslot = [](int c) { return (c & 1) * Q_CHUNK; };
+  auto wslot = [](int c) { return (c & 1) * WCH; };
 
   // prologue: W chunk 0, x slices 0 and 1; all but x slice 1's DMAs waited for
-  u32x2 s8[4], n8[4];
+  u32x2 s8[NI], n8[NI];
   scales8(0, s8);
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int i = 0; i < Q_DMA; ++i) dma_w(0, 0u, i);
+  for (int i = 0; i < WD; ++i) dma_w(0, 0u, i);
 #pragma unroll
   for (int i = 0; i < XD; ++i) dma_x(XBASE, 0u, i);
 #pragma unroll
@@ -133,17 +134,17 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
   wait_vm<XD>();
   // a use here keeps the scale loads ahead of the DMAs
 #pragma unroll
-  for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(s8[i]));
+  for (int i = 0; i < NI; ++i) asm volatile("" : "+v"(s8[i]));
   bare_barrier();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < NI; ++i) {
     read_raw(0, 0, i);
     sc[i] = pick(s8[i], 0);
   }
 #pragma unroll
   for (int j = 0; j < NJ; ++j) read_x(XBASE, 0, 0, j);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) convert(0, 0, i);
+  for (int i = 0; i < NI; ++i) convert(0, 0, i);
 
   int xb = 0;   // d % 3
   // slice d (64 k), par = d % 4: x of slice d+2 and, in the chunk's first
@@ -161,12 +162,13 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
 #pragma unroll
     for (int kk = 0; kk < 3; ++kk) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < NI; ++q) {
         __builtin_amdgcn_sched_barrier(0);
-        // W: 3 + 3 + 2 DMAs over a chunk's first three slices, ahead of x's
-        const bool dw = PAR < 3 && kk == 0 && q < (PAR == 2 ? 2 : 3);
-        if (dw) dma_w(wslot(c + 1), kw, 3 * PAR + q);
-        const int x0 = kk * 4 + q - 1;   // x: 8 (4) DMAs from (kk 0, q 1) on
+        // W: 3 + 3 + 2 (2 + 1 + 1) DMAs over a chunk's first three slices
+        constexpr int w0 = NI == 4 ? 3 * PAR : PAR + (PAR > 0), wd = NI == 4 ? (PAR == 2 ? 2 : 3) : (PAR ? 1 : 2);
+        const bool dw = PAR < 3 && kk == 0 && q < wd;
+        if (dw) dma_w(wslot(c + 1), kw, w0 + q);
+        const int x0 = kk * NI + q - (NI == 4);   // x: one each from (kk 0, q 1 or 0) on
         const bool dx = x0 >= 0 && x0 < XD;
         if (dx) dma_x(sb2, kx, x0);
         if (q < NJ) read_x(sb, kk + 1, (kk + 1) & 1, q);
@@ -185,35 +187,45 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
     wait_vm<XD>();   // only x of slice d+2 may still fly
     wait_lgkm0();
     bare_barrier();
-    // sub-step 3, quarters 1..3: slice d+1's W words, first x fragments, conversions
+    // the rest of sub-step 3: slice d+1's W words, first x fragments, conversions
     const int sw1 = wslot(PAR == 3 ? c + 1 : c);
+    auto next_w = [&]() {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) read_raw(sw1, (PAR + 1) & 3, i);
+    };
+    auto next_x = [&]() {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) read_x(sb1, 0, 0, j);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) sc[i] = PAR == 3 ? pick(n8[i], 0) : pick(s8[i], (PAR + 1) & 3);
+    };
     __builtin_amdgcn_sched_barrier(0);
+    next_w();
+    if constexpr (NI == 4) {
+      mfma_row(1, 1);
+      if (NJ == 4) { SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 2); }
+      else { SGB(SG_MFMA, 1); SGB(SG_DSR, 4); SGB(SG_MFMA, 1); }
+      __builtin_amdgcn_sched_barrier(0);
+      next_x();
+      mfma_row(1, 2);
+      if (NJ == 4) { SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 2); }
+      else { SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); }
+      __builtin_amdgcn_sched_barrier(0);
+    } else {
+      next_x();
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) read_raw(sw1, (PAR + 1) & 3, i);
-    mfma_row(1, 1);
-    if (NJ == 4) { SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 2); }
-    else { SGB(SG_MFMA, 1); SGB(SG_DSR, 4); SGB(SG_MFMA, 1); }
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) read_x(sb1, 0, 0, j);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sc[i] = PAR == 3 ? pick(n8[i], 0) : pick(s8[i], (PAR + 1) & 3);
-    mfma_row(1, 2);
-    if (NJ == 4) { SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 2); }
-    else { SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); }
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) convert(0, 0, i);
-    mfma_row(1, 3);
+    for (int i = 0; i < NI; ++i) convert(0, 0, i);
+    mfma_row(1, NI - 1);
     if (NJ == 4) {
       SGB(SG_MFMA, 1); SGB(SG_VALU, 5); SGB(SG_MFMA, 1); SGB(SG_VALU, 5); SGB(SG_MFMA, 1); SGB(SG_VALU, 5);
       SGB(SG_MFMA, 1);
-    } else {
+    } else if (NI == 4) {
       SGB(SG_MFMA, 1); SGB(SG_VALU, 8); SGB(SG_MFMA, 1);
     }
     if (PAR == 3) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s8[i] = n8[i];
+      for (int i = 0; i < NI; ++i) s8[i] = n8[i];
     }
     xb = xb + 1 >= 3 ? 0 : xb + 1;
   };
@@ -225,28 +237,29 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
   }
   __builtin_amdgcn_sched_barrier(0);
   wait_vm<0>();   // the zero-fill DMAs of the last slices land before LDS is reused
-  store_tile<NJ>(acc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
+  store_tile<NI, NJ>(acc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
 }
 
-template <int NJ>
-__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(1, 1)))
+template <int NI, int NJ>
+__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(NI == 4 ? 1 : 2, NI == 4 ? 1 : 2)))
 void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restrict__ xs, int T, int K,
                         const uint8_t* __restrict__ w, const uint8_t* __restrict__ ws, int N,
                         uint16_t* __restrict__ kv, int tiles_n, int tiles_t, GateEpi ep) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   int tn, tt;
   tile_of(blockIdx.x, tiles_n, tiles_t, tn, tt);
-  constexpr int TN = 64 * NJ, XCH = x_slot(NJ), XD = x_dma(NJ), XBASE = kWSlots * Q_CHUNK;
-  const int n0 = tn * BM, t0 = tt * TN;
+  constexpr int TM = 64 * NI, TN = 64 * NJ, WCH = op_slot(NI), XCH = op_slot(NJ), WD = op_dma(NI), XD = op_dma(NJ);
+  constexpr int XBASE = kWSlots * WCH;
+  const int n0 = tn * TM, t0 = tt * TN;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wn = (wave >> 1) * 128, wt = (wave & 1) * (32 * NJ);
+  const int wn = (wave >> 1) * (32 * NI), wt = (wave & 1) * (32 * NJ);
   const uint32_t wpitch = (uint32_t)K / 2u, xpitch = (uint32_t)K, kb = (uint32_t)K / 32u;
-  const rsrc_t ra = make_rsrc(w + (int64_t)n0 * wpitch, (uint32_t)min(BM, N - n0) * wpitch);
+  const rsrc_t ra = make_rsrc(w + (int64_t)n0 * wpitch, (uint32_t)min(TM, N - n0) * wpitch);
   const rsrc_t rb = make_rsrc(xq + (int64_t)t0 * xpitch, (uint32_t)min(TN, T - t0) * xpitch);
-  const rsrc_t rsa = make_rsrc(ws + (int64_t)n0 * kb, (uint32_t)min(BM, N - n0) * kb);
+  const rsrc_t rsa = make_rsrc(ws + (int64_t)n0 * kb, (uint32_t)min(TM, N - n0) * kb);
   const rsrc_t rsb = make_rsrc(xs + (int64_t)t0 * kb, (uint32_t)min(TN, T - t0) * kb);
-  const uint32_t ooba = (uint32_t)BM * wpitch, oobb = (uint32_t)TN * xpitch;
+  const uint32_t ooba = (uint32_t)TM * wpitch, oobb = (uint32_t)TN * xpitch;
   const int ns = K / 128, nc = K / 256;   // x slices (even), W chunks
 
   const dma::Lane la = dma::lane_of(wave, lane, wpitch), lb = dma::lane_of(wave, lane, xpitch);
@@ -263,14 +276,14 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
   const int fsw = (lrow >> 1) & 7;
   // the 8 scale bytes of a chunk (four stages of 64 k) of this lane's W and
   // token rows; lane group g takes byte 2*stage + g
-  uint32_t arow[4], brow[NJ];
+  uint32_t arow[NI], brow[NJ];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) arow[i] = (uint32_t)(wn + i * 32 + lrow) * kb;
+  for (int i = 0; i < NI; ++i) arow[i] = (uint32_t)(wn + i * 32 + lrow) * kb;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) brow[j] = (uint32_t)(wt + j * 32 + lrow) * kb;
-  auto scales8 = [&](int c, u32x2 (&a8)[4], u32x2 (&b8)[NJ]) {
+  auto scales8 = [&](int c, u32x2 (&a8)[NI], u32x2 (&b8)[NJ]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < NI; ++i) {
       a8[i] = __builtin_amdgcn_raw_buffer_load_b64(rsa, arow[i] + 8u * (uint32_t)c, 0, 0);
       if (i < NJ) b8[i] = __builtin_amdgcn_raw_buffer_load_b64(rsb, brow[i] + 8u * (uint32_t)c, 0, 0);
     }
@@ -290,42 +303,42 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
 
-  f32x16 acc[4][NJ];
+  f32x16 acc[NI][NJ];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < NI; ++i)
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-  i32x4 a[4], na[4];
+  i32x4 a[NI], na[NI];
   i32x8 b[NJ], nb[NJ];
-  int sa[4], sb[NJ];
+  int sa[NI], sb[NJ];
   auto mfma_row = [&](int i) {
     const i32x8 wa = __builtin_shufflevector(a[i], a[i], 0, 1, 2, 3, 0, 1, 2, 3);   // fp4: the first four words
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
       acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wa, b[j], acc[i][j], 4, 0, 0, sa[i], 0, sb[j]);
   };
-  auto wslot = [](int c) { return (c & 1) * Q_CHUNK; };
+  auto wslot = [](int c) { return (c & 1) * WCH; };
 
-  u32x2 sa8[4], sb8[NJ], na8[4], nb8[NJ];
+  u32x2 sa8[NI], sb8[NJ], na8[NI], nb8[NJ];
   scales8(0, sa8, sb8);
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int i = 0; i < Q_DMA; ++i) dma_w(0, 0u, i);
+  for (int i = 0; i < WD; ++i) dma_w(0, 0u, i);
 #pragma unroll
   for (int i = 0; i < XD; ++i) dma_x(XBASE, 0u, i);
 #pragma unroll
   for (int i = 0; i < XD; ++i) dma_x(XBASE + XCH, (uint32_t)Q_ROW, i);
   wait_vm<XD>();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(sa8[i]));
+  for (int i = 0; i < NI; ++i) asm volatile("" : "+v"(sa8[i]));
 #pragma unroll
   for (int j = 0; j < NJ; ++j) asm volatile("" : "+v"(sb8[j]));
   bare_barrier();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < NI; ++i) {
     a[i] = wfrag(0, 0, i);
     sa[i] = pick(sa8[i], 0);
     if (i < NJ) {
@@ -347,14 +360,14 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
     if (PAR == 0) scales8(min(c + 1, nc - 1), na8, nb8);   // the last chunk reloads itself, unused
     // stage 0; stage 1's fragments are read ahead
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < NI; ++q) {
       __builtin_amdgcn_sched_barrier(0);
       if (PAR == 0) {
         dma_w(wslot(c + 1), kw, 2 * q);
         dma_w(wslot(c + 1), kw, 2 * q + 1);
       } else {
 #pragma unroll
-        for (int k = 0; k < XD / 4; ++k) dma_x(s_x2, kx, XD / 4 * q + k);
+        for (int k = 0; k < XD / NI; ++k) dma_x(s_x2, kx, XD / NI * q + k);
       }
       na[q] = wfrag(wslot(c), 2 * PAR + 1, q);
       if (q < NJ) nb[q] = xfrag(s_x, 1, q);
@@ -367,7 +380,7 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < NI; ++i) {
       a[i] = na[i];
       sa[i] = pick(sa8[i], 2 * PAR + 1);
       if (i < NJ) {
@@ -375,13 +388,13 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
         sb[i] = pick(sb8[i], 2 * PAR + 1);
       }
     }
-    // stage 1; the barrier that publishes slice d+1 after its second row block
+    // stage 1; the barrier that publishes slice d+1 after half its row blocks
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
+    for (int q = 0; q < NI / 2; ++q) {
       __builtin_amdgcn_sched_barrier(0);
       if (PAR == 0) {
 #pragma unroll
-        for (int k = 0; k < XD / 2; ++k) dma_x(s_x2, kx, XD / 2 * q + k);
+        for (int k = 0; k < 2 * XD / NI; ++k) dma_x(s_x2, kx, 2 * XD / NI * q + k);
       }
       mfma_row(q);
       if (PAR == 0) {
@@ -392,17 +405,17 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
     __builtin_amdgcn_sched_barrier(0);
     // in flight may be x of slice d+2 and, in an even slice, the W chunk
     // after this slice's (not needed before the next slice's end)
-    if (PAR == 0) wait_vm<Q_DMA + XD>();
+    if (PAR == 0) wait_vm<WD + XD>();
     else wait_vm<XD>();
     wait_lgkm0();
     bare_barrier();
     const int sw1 = wslot(PAR == 1 ? c + 1 : c);
     constexpr int u1 = PAR == 1 ? 0 : 2;
 #pragma unroll
-    for (int q = 2; q < 4; ++q) {
+    for (int q = NI / 2; q < NI; ++q) {
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 2 * q - 4; i < 2 * q - 2; ++i) {
+      for (int i = 2 * q - NI; i < 2 * q - NI + 2; ++i) {
         na[i] = wfrag(sw1, u1, i);
         if (i < NJ) nb[i] = xfrag(s_x1, 0, i);
       }
@@ -415,7 +428,7 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < NI; ++i) {
       a[i] = na[i];
       if (PAR == 1) sa8[i] = na8[i];
       sa[i] = pick(sa8[i], u1);
@@ -433,24 +446,24 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
   }
   __builtin_amdgcn_sched_barrier(0);
   wait_vm<0>();   // the zero-fill DMAs of the last slices land before LDS is reused
-  store_tile<NJ>(acc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
+  store_tile<NI, NJ>(acc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
 }
 
-template <int NJ>
-hipError_t launch_nj(const void* x, const uint8_t* xs, int T, int K, const uint8_t* w, const uint8_t* ws, int N,
-                     uint16_t* kv, hipStream_t s, const GateEpi& ep) {
-  const int tiles_n = (N + BM - 1) / BM, tiles_t = (T + 64 * NJ - 1) / (64 * NJ);
+template <int NI, int NJ>
+hipError_t launch_tile(const void* x, const uint8_t* xs, int T, int K, const uint8_t* w, const uint8_t* ws, int N,
+                       uint16_t* kv, hipStream_t s, const GateEpi& ep) {
+  const int tiles_n = (N + 64 * NI - 1) / (64 * NI), tiles_t = (T + 64 * NJ - 1) / (64 * NJ);
   const dim3 grid(tiles_n * tiles_t), block(THREADS);
-  constexpr int lds = fp4_lds(NJ);
+  constexpr int lds = fp4_lds(NI, NJ);
   hipError_t e;
   if (xs) {
-    if ((e = set_lds((const void*)gemm_fp4_mx_kernel<NJ>, lds)) != hipSuccess) return e;
-    hipLaunchKernelGGL(gemm_fp4_mx_kernel<NJ>, grid, block, lds, s, (const uint8_t*)x, xs, T, K, w, ws, N, kv,
-                       tiles_n, tiles_t, ep);
+    const auto fn = gemm_fp4_mx_kernel<NI, NJ>;
+    if ((e = set_lds((const void*)fn, lds)) != hipSuccess) return e;
+    hipLaunchKernelGGL(fn, grid, block, lds, s, (const uint8_t*)x, xs, T, K, w, ws, N, kv, tiles_n, tiles_t, ep);
   } else {
-    if ((e = set_lds((const void*)gemm_fp4_bf16_kernel<NJ>, lds)) != hipSuccess) return e;
-    hipLaunchKernelGGL(gemm_fp4_bf16_kernel<NJ>, grid, block, lds, s, (const uint16_t*)x, T, K, w, ws, N, kv,
-                       tiles_n, tiles_t, ep);
+    const auto fn = gemm_fp4_bf16_kernel<NI, NJ>;
+    if ((e = set_lds((const void*)fn, lds)) != hipSuccess) return e;
+    hipLaunchKernelGGL(fn, grid, block, lds, s, (const uint16_t*)x, T, K, w, ws, N, kv, tiles_n, tiles_t, ep);
   }
   return hipGetLastError();
 }
@@ -459,17 +472,23 @@ hipError_t launch_nj(const void* x, const uint8_t* xs, int T, int K, const uint8
 
 hipError_t launch_gemm_mxfp4(const void* x, const uint8_t* xs, int64_t T, int K, const uint8_t* w,
                              const uint8_t* ws, int N, void* kv, hipStream_t s, const GateEpi& ep) {
-  // 256-token tiles move the fewest bytes a flop; a round of 128-token tiles
-  // costs 0.57 - 0.6 of a round of them, so those are taken where they need
-  // few enough rounds (K 2048, N 20480, bf16 x: T 300 42 -> 28 us, T 1000 88 ->
-  // 79, T 1500 stays at 96 against 113; K 1024, N 10240, T 515 25 -> 17 us).
-  // The gate's epilogue has the 256-token tile only.
-  const int64_t tiles_n = (N + BM - 1) / BM, cus = dev_info().num_cus;
-  const int64_t rounds256 = (tiles_n * ((T + 255) / 256) + cus - 1) / cus;
-  const int64_t rounds128 = (tiles_n * ((T + 127) / 128) + cus - 1) / cus;
-  if (!ep.hidden && 6 * rounds128 < 10 * rounds256)
-    return launch_nj<2>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep);
-  return launch_nj<4>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep);
+  // The tile by what its rounds cost, a full round of 256x256 tiles being 100.
+  // Larger tiles move fewer bytes a flop; smaller ones fill the compute units
+  // where there are few, and end sooner. Measured at K 2048, bf16 x: a round
+  // of 256x128 tiles costs 60 of that, one of 128x128 tiles 60 as well with
+  // two workgroups on a compute unit and 42 with one (N 20480: T 128 in 40 / 24
+  // / 18 us for 256x256 / 256x128 / 128x128, T 515 50 / 53 / 52, T 1000 90 / 83
+  // / 74, T 8192 490 / 540 / 550). The gate's epilogue has the 256x256 tile
+  // only.
+  const int64_t cus = dev_info().num_cus;
+  auto tiles = [&](int tm, int tt) { return ((int64_t)N + tm - 1) / tm * ((T + tt - 1) / tt); };
+  auto rounds = [&](int64_t n) { return (n + cus - 1) / cus; };
+  const int64_t n22 = tiles(128, 128), last = n22 % (2 * cus);
+  const int64_t c44 = 100 * rounds(tiles(256, 256)), c42 = 60 * rounds(tiles(256, 128));
+  const int64_t c22 = 60 * (n22 / (2 * cus)) + (last > cus ? 60 : last > 0 ? 42 : 0);
+  if (ep.hidden || (c44 <= c42 && c44 <= c22)) return launch_tile<4, 4>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep);
+  if (c42 <= c22) return launch_tile<4, 2>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep);
+  return launch_tile<2, 2>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep);
 }
 
 }  // namespace engram

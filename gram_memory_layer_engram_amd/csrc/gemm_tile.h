@@ -87,12 +87,13 @@ __device__ __forceinline__ void store_nt(uint16_t* dst, const uint4& v) {
 //    bf16-rounded keys ("vllm.models.deepseek_v41.amd.engram",
 //    _engram_gate_partials_kernel, at tile granularity), into
 //    ep.part[(h*T + t) * (dim/256) + tile].
-// NJ: 32-token blocks of a wave (4: a 256-token tile; 2: 128 tokens, plain
-// store only).
-template <int NJ = 4>
-__device__ __forceinline__ void store_tile(f32x16 (&acc)[4][NJ], char* smem, uint16_t* __restrict__ kv,
+// NI, NJ: 32-row and 32-token blocks of a wave (4, 4: the 256x256 tile;
+// smaller ones have the plain store only).
+template <int NI = 4, int NJ = 4>
+__device__ __forceinline__ void store_tile(f32x16 (&acc)[NI][NJ], char* smem, uint16_t* __restrict__ kv,
                                            int T, int N, int t0, int n0, int wn, int wt, int lane,
                                            int wave, const GateEpi& ep) {
+  constexpr int RB = 128 * NI, CPR = 8 * NI;   // bytes and 16-byte chunks of a staged row
   const int lrow = lane & 31, lhalf = lane >> 5;
   wait_lgkm0();
   bare_barrier();
@@ -100,7 +101,7 @@ __device__ __forceinline__ void store_tile(f32x16 (&acc)[4][NJ], char* smem, uin
   for (int j = 0; j < NJ; ++j) {
     const int t = wt + j * 32 + lrow;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         // accumulator r of lane l: n = 8*(r/4) + 4*(l/32) + r%4, token = l%32
@@ -108,18 +109,20 @@ __device__ __forceinline__ void store_tile(f32x16 (&acc)[4][NJ], char* smem, uin
         uint2 o;
         o.x = cvt_pk_bf16(acc[i][j][4 * g + 0], acc[i][j][4 * g + 1]);
         o.y = cvt_pk_bf16(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]);
-        *reinterpret_cast<uint2*>(smem + t * 512 + (((n >> 3) ^ (t & 31)) << 4) + (n & 7) * 2) = o;
+        *reinterpret_cast<uint2*>(smem + t * RB + (((n >> 3) ^ (t & (CPR - 1))) << 4) + (n & 7) * 2) = o;
       }
   }
   wait_lgkm0();
   bare_barrier();
-  const int c = lane & 31;
-  auto lds_row = [&](int t) { return *reinterpret_cast<const uint4*>(smem + t * 512 + ((c ^ (t & 31)) << 4)); };
-  if (NJ < 4 || !ep.hidden) {
+  const int c = lane & (CPR - 1);
+  auto lds_row = [&](int t) {
+    return *reinterpret_cast<const uint4*>(smem + t * RB + ((c ^ (t & (CPR - 1))) << 4));
+  };
+  if (NI < 4 || NJ < 4 || !ep.hidden) {
     const int n = n0 + c * 8;
 #pragma unroll 4
-    for (int it = 0; it < 8 * NJ; ++it) {
-      const int t = wave * (16 * NJ) + it * 2 + (lane >> 5);
+    for (int it = 0; it < 2 * NI * NJ; ++it) {
+      const int t = wave * (16 * NJ) + it * (64 / CPR) + lane / CPR;
       const uint4 v = lds_row(t);
       if (t0 + t < T) {
         uint16_t* dst = kv + (int64_t)(t0 + t) * N + n;

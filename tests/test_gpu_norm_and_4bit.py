@@ -496,10 +496,12 @@ class _FakeOther:
 
 
 @pytest.mark.parametrize("op", ["wkv", "wkv_mx"])
-@pytest.mark.parametrize("T,K,N", [(1500, 256, 20480), (4096, 512, 5120 - 4)])
+@pytest.mark.parametrize("T,K,N", [(1500, 256, 20480), (1500, 512, 20476), (300, 768, 20480), (515, 256, 10236),
+                                   (4096, 512, 5116)])
 def test_mxfp4_many_tiles(op, T, K, N):
-    """More rounds of tiles than compute units, in which the 256-token tiles of
-    the GEMM run, ragged in T and N; a token from every tile and some more."""
+    """Enough tiles that the GEMM's larger ones run (256x256 in the first two,
+    256x128 in the next two, 128x128 in the last, on 256 compute units), ragged
+    in T and N; a token from every tile and some more."""
     E = _E()
     rng = np.random.default_rng(K)
     wq, ws = mxfp4_weight(rng, N, K)
