@@ -74,8 +74,8 @@ int check_wkv(const void* x, int64_t T, int32_t K, const void* w,
     if (T > 0 && (!w_scales || ((uintptr_t)w_scales & 3u))) return ENGRAM_EINVAL;
     if (K % 128 != 0 || N % 32 != 0) return ENGRAM_EUNSUPPORTED;
   } else if (w_format == ENGRAM_W_MXFP4) {
-    if (T > 0 && (!w_scales || ((uintptr_t)w_scales & 3u))) return ENGRAM_EINVAL;
-    if (K % 128 != 0 || N % 4 != 0) return ENGRAM_EUNSUPPORTED;
+    if (T > 0 && (!w_scales || !aligned16(w_scales))) return ENGRAM_EINVAL;
+    if (K % 128 != 0 || N % 4 != 0 || N > (1 << 28)) return ENGRAM_EUNSUPPORTED;
   } else {
     return ENGRAM_EINVAL;
   }
@@ -348,6 +348,15 @@ int engram_add_rms_norm(const void* x, int64_t x_stride_t, int64_t x_stride_h, c
   if (!x || (!out && !xq)) return ENGRAM_EINVAL;
   for (const void* p : {x, residual, weight, (const void*)residual_out, (const void*)out, (const void*)xq})
     if (!aligned16(p)) return ENGRAM_EINVAL;
+  // in place (residual_out on residual, out on x) row by row only, and never
+  // two outputs on one buffer
+  auto rows_dense = [&](int64_t st, int64_t sh) {
+    return (T == 1 || st == (int64_t)hc * dim) && (hc == 1 || sh == dim);
+  };
+  if (residual_out && residual_out == residual && !rows_dense(residual_stride_t, residual_stride_h))
+    return ENGRAM_EINVAL;
+  if (out && out == x && !rows_dense(x_stride_t, x_stride_h)) return ENGRAM_EINVAL;
+  if (out && out == residual_out) return ENGRAM_EINVAL;
   const RmsNormArgs a{(const uint16_t*)x, x_stride_t, x_stride_h, (const uint16_t*)residual,
                       residual_stride_t, residual_stride_h, (const uint16_t*)weight, weight_hc, T * hc, hc,
                       dim, eps, (uint16_t*)residual_out, (uint16_t*)out, xq, xs};

@@ -43,6 +43,9 @@ __device__ __forceinline__ uint32_t cvt_pk_bf16(float lo, float hi) {
 
 // Byte B of a word of e2m1 codes (two codes, the lower k in the low nibble)
 // times a power of two -> a pair of bf16 (v_cvt_scalef32_pk_bf16_fp4; exact).
+// Of its scale the instruction takes the exponent field alone, as E8M0: field
+// 0 is 2^-127, 255 NaN (checked for every field, with and without the other
+// bits set).
 template <int B>
 __device__ __forceinline__ uint32_t fp4_pair_to_bf16(uint32_t codes, float scale) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, B));

@@ -24,6 +24,8 @@
 // its maximum is two quad permutations; the scale bytes of a wave's run (16 a
 // piece) are contiguous and leave as one store of 16 * P bytes through LDS.
 // Outputs go non-temporal: the kernel never reads them back.
+#include <algorithm>
+
 #include "common.h"
 #include "mx_rule.h"
 
@@ -71,7 +73,7 @@ __global__ __launch_bounds__(TPR < 256 && 256 % TPR == 0 ? 256 : TPR) void add_r
   __shared__ uint8_t sbytes[BS / 64][16 * P];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t row = (int64_t)blockIdx.x * RPB + wave / WPR;
+  const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * RPB + wave / WPR;
   const bool live = row < a.rows;                  // uniform per wave
   const int64_t t = live ? row / a.hc : 0;
   const int h = live ? (int)(row - t * a.hc) : 0;
@@ -162,7 +164,11 @@ __global__ __launch_bounds__(TPR < 256 && 256 % TPR == 0 ? 256 : TPR) void add_r
 template <int P, int TPR>
 hipError_t launch(const RmsNormArgs& a, hipStream_t s) {
   constexpr int BS = TPR < 256 && 256 % TPR == 0 ? 256 : TPR, RPB = BS / TPR;
-  hipLaunchKernelGGL((add_rms_norm_kernel<P, TPR>), dim3((uint32_t)((a.rows + RPB - 1) / RPB)), dim3(BS), 0, s, a);
+  // a grid dimension holds fewer than 2^32 threads: past 2^20 workgroups the
+  // rows run on into y
+  const int64_t blocks = (a.rows + RPB - 1) / RPB, gx = std::min<int64_t>(blocks, 1 << 20);
+  hipLaunchKernelGGL((add_rms_norm_kernel<P, TPR>), dim3((uint32_t)gx, (uint32_t)((blocks + gx - 1) / gx)), dim3(BS),
+                     0, s, a);
   return hipGetLastError();
 }
 

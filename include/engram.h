@@ -175,24 +175,26 @@ int engram_mx_quantize(const void* x, int64_t T, int32_t K, uint8_t* xq,
  *   x          bf16 [T, K] (the staged rows [T, C, head_dim] viewed flat).
  *   w          bf16 [N, K] (ENGRAM_W_BF16), uint8 codes [N, K] (ENGRAM_W_MXFP8)
  *              or packed codes [N, K/2] (ENGRAM_W_MXFP4).
- *   w_scales   uint8 [N/32, K/32] for MXFP8, [N, K/32] for MXFP4 (4-byte
- *              aligned), NULL for bf16.
+ *   w_scales   uint8 [N/32, K/32] for MXFP8 (4-byte aligned), [N, K/32] for
+ *              MXFP4 (16-byte aligned), NULL for bf16.
  *   kv         bf16 [T, N].
  *   workspace  device scratch of at least engram_wkv_workspace_size() bytes
  *              (NULL allowed when that size is 0). For MXFP8 it holds x's
- *              MXFP8 codes and scales; for MXFP4 the weight expanded to bf16
- *              (exact) for the tiled GEMM. 256-byte aligned.
+ *              MXFP8 codes and scales; for MXFP4 it is needed only for
+ *              K % 256 != 0 past the GEMV's token counts: the weight
+ *              expanded to bf16 (exact). 256-byte aligned.
  *   With MXFP4 weights x stays bf16 and W enters as its bf16 values, which
  *   are exact (a value of 2^128 or more, scale bytes 253 and 254 only, is an
  *   infinity); engram_wkv_mx takes 8-bit activations.
  *   Shapes: bf16 needs K % 8 == 0 and N % 4 == 0; MXFP8 needs K % 128 == 0
- *   and N % 32 == 0; MXFP4 needs K % 128 == 0 and N % 4 == 0; all need
- *   K <= 2^20 (32-bit buffer offsets). Other shapes return
+ *   and N % 32 == 0; MXFP4 needs K % 128 == 0, N % 4 == 0 and N <= 2^28; all
+ *   need K <= 2^20 (32-bit buffer offsets). Other shapes return
  *   ENGRAM_EUNSUPPORTED.
  *   Kernels: a tiled GEMM; for T <= 64 a weight-streaming GEMV instead
  *   (MXFP8 with K/128 <= 32; bf16 with K % 32 == 0, K <= 2048, N % 16 == 0
- *   where it beats the GEMM). The two sum in different fp32 orders, so
- *   their kv can differ in the last bit.
+ *   where it beats the GEMM; MXFP4 with a row's scale bytes in LDS, K up to
+ *   36000 at least). The two sum in different fp32 orders, so their kv can
+ *   differ in the last bit.
  */
 size_t engram_wkv_workspace_size(int64_t T, int32_t K, int32_t N,
                                  int32_t w_format);
@@ -244,9 +246,10 @@ int engram_wkv_mx(const uint8_t* xq, const uint8_t* xs, int64_t T, int32_t K, co
  *                 residual may be NULL.
  *   weight        bf16 [weight_hc, dim], weight_hc 1 (shared) or hc; NULL: ones.
  *   residual_out  optional bf16 [T, hc, dim] contiguous; may be `residual`
- *                 itself (in place) when that is contiguous.
+ *                 itself (in place) when that is contiguous (else EINVAL).
  *   out           optional bf16 [T, hc, dim] contiguous; may be `x` itself
- *                 when that is contiguous. No other overlap is allowed.
+ *                 when that is contiguous (else EINVAL). No other overlap
+ *                 is allowed.
  *   xq, xs        optional, both or neither: uint8 [T, hc, dim] and
  *                 [T, hc, dim/32]. At least one of out and xq.
  *   eps           >= 0 (a row of zeros with eps 0 gives NaN).
@@ -280,8 +283,9 @@ int engram_add_rms_norm(const void* x, int64_t x_stride_t, int64_t x_stride_h, c
  *   workspace   engram_wkv_workspace_size(T, K, (hc+1)*dim, w_format) bytes
  *   Errors: ENGRAM_EINVAL for hc or dim <= 0, a NULL or misaligned pointer,
  *   or a short workspace; T = 0 is a no-op. Asynchronous on `stream`.
- *   Shapes: as engram_wkv, plus dim % 256 == 0 and 1 <= hc <= 8; other
- *   shapes return ENGRAM_EUNSUPPORTED. This always runs the tiled GEMM
+ *   Shapes: as engram_wkv, plus dim % 256 == 0 and 1 <= hc <= 8 (MXFP4 at
+ *   T <= 64: K % 256 == 0 as well); other shapes return
+ *   ENGRAM_EUNSUPPORTED. This always runs the tiled GEMM
  *   (engram_wkv may take a GEMV for T <= 64).
  */
 int engram_wkv_gate_partials(const void* x, int64_t T, int32_t K, const void* w,
@@ -342,7 +346,8 @@ int engram_gate(const void* hidden, const void* kv, const void* q_weight,
 
 /*
  * engram_forward -- one Engram layer forward: lookup -> (MXFP8 quantize) ->
- *   wkv -> gate, all on `stream`.
+ *   wkv -> gate, all on `stream`. With ENGRAM_W_MXFP4 the staged rows stay
+ *   bf16 (no quantize step), as engram_wkv.
  *   [P-common] Engram.forward: kv = wkv(embed(hash_ids).flatten(-2)), then the
  *   fused gate over [T, hc, dim]; the staged rows and kv live in the caller's
  *   workspace (the pages keep them as persistent buffers: Engram.staged_rows,
@@ -363,7 +368,7 @@ typedef struct engram_forward_args {
   int64_t ids_stride_t;
   int64_t ids_stride_c;
   const void* w;           /* wkv weight, see engram_wkv */
-  const uint8_t* w_scales; /* MXFP8 and MXFP4 */
+  const uint8_t* w_scales; /* MXFP8 and MXFP4, see engram_wkv */
   int32_t w_format;
   const void* hidden;      /* bf16 [T, hc, dim] */
   const void* q_weight;    /* bf16 [hc, dim] */

@@ -86,7 +86,9 @@ def _norm_ref(x, r, w, eps):
 
 @pytest.mark.parametrize("T,hc,dim", [(1, 1, 32), (1, 4, 4096), (3, 2, 64), (5, 3, 544), (17, 1, 1024), (2, 8, 2080),
                                       (33, 4, 2048), (4, 2, 4128), (9, 1, 7168), (3, 4, 8192), (2, 1, 8224), (3, 2, 16384),
-                                      (700, 4, 256), (1030, 1, 512)])
+                                      (700, 4, 256), (1030, 1, 512), (150, 2, 544), (300, 1, 1024), (131, 3, 2048),
+                                      (97, 4, 2080), (70, 4, 4096), (65, 4, 4128), (259, 1, 7168), (90, 3, 8224),
+                                      (260, 1, 16384)])
 def test_norm_both_outputs(T, hc, dim):
     E = _E()
     rng = np.random.default_rng(dim * 7 + T)
@@ -113,6 +115,19 @@ def test_norm_bf16_odd_dims(dim):
     x, r, w = bf16(rng, 5, 3, dim), bf16(rng, 5, 3, dim), bf16(rng, dim)
     res, out, _, _ = E.add_rms_norm(x.to(DEV), r.to(DEV), w.to(DEV))
     _check_norm(dim, *_norm_ref(x, r, w, 1e-6), res, out, None, None)
+
+
+def test_norm_more_rows_than_one_grid_dimension():
+    """Rows past what one grid dimension holds (2^20 workgroups of 4 rows)."""
+    E = _E()
+    T, dim = (1 << 22) + 4099, 8
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn((T, dim), generator=g, device=DEV).to(torch.bfloat16)
+    _, out, _, _ = E.add_rms_norm(x, None, None, 1e-6)
+    at = torch.cat([torch.arange(0, 9), torch.arange((1 << 22) - 9, T), torch.randint(0, T, (4096,))]).to(DEV)
+    s, y = _norm_ref(x[at][:, None].cpu(), None, None, 1e-6)
+    _check_norm(dim, s, y, None, out[at][:, None], None, None)
+    assert bool(torch.isfinite(out).all())
 
 
 def test_norm_strides_broadcast_two_dims_and_in_place():
@@ -301,6 +316,20 @@ def test_mxfp4_infinite_and_nan_activations_stay_in_their_token(T):
     got = E.wkv(x.to(DEV), torch.from_numpy(wq).to(DEV), torch.from_numpy(ws).to(DEV)).cpu().float()
     assert bool((got[1] == float("inf")).all()) and bool(torch.isnan(got[2]).all())
     assert bool(torch.isfinite(got[0]).all()) and bool(torch.isfinite(got[3:]).all())
+
+
+@pytest.mark.parametrize("T", [4, 40, 70])
+def test_wkv_mx_nan_blocks_stay_in_their_token(T):
+    """A NaN scale byte or a NaN code in one token's activations."""
+    E = _E()
+    K, N = 256, 96
+    rng = np.random.default_rng(T)
+    wq, ws = mxfp4_weight(rng, N, K)
+    xq, xs = mxfp8_rows(rng, T, K)
+    xs[1, 3], xq[3, 200] = 255, 0x7F
+    got = E.wkv_mx(*[torch.from_numpy(a).to(DEV) for a in (xq, xs, wq, ws)]).cpu().float()
+    assert bool(torch.isnan(got[[1, 3]]).all()) and bool(torch.isfinite(got[[0, 2]]).all())
+    assert bool(torch.isfinite(got[4:]).all())
 
 
 @pytest.mark.parametrize("T", [1, 9, 16, 40, 64, 65, 300])

@@ -48,8 +48,8 @@ def test_oracle_norm_closed_forms():
     assert np.all(y == 0)
 
 
-def norm(lib, x=P, xst=128, xsh=64, r=P, rst=128, rsh=64, w=P, whc=2, T=4, hc=2, dim=64, eps=1e-6, ro=P, out=P,
-         xq=P, xs=P):
+def norm(lib, x=P, xst=128, xsh=64, r=2 * P, rst=128, rsh=64, w=3 * P, whc=2, T=4, hc=2, dim=64, eps=1e-6, ro=4 * P,
+         out=5 * P, xq=6 * P, xs=7 * P):
     return lib.engram_add_rms_norm(x, xst, xsh, r, rst, rsh, w, whc, T, hc, dim, eps, ro, out, xq, xs, None)
 
 
@@ -62,6 +62,13 @@ def test_add_rms_norm_refusals(lib):
         assert norm(lib, **bad) == INV, bad
     for bad in (dict(dim=60), dict(dim=72), dict(dim=16416), dict(xst=129), dict(rsh=4), dict(T=2**31 // 2)):
         assert norm(lib, **bad) == UNS, bad
+    # in place on rows that are not dense, and two outputs on one buffer
+    R, O = 0x20000, 0x30000
+    assert norm(lib, r=R, ro=R, rst=256, out=O) == INV
+    assert norm(lib, r=R, ro=R, rsh=0, rst=64, out=O) == INV
+    assert norm(lib, x=O, out=O, xst=136, ro=None) == INV
+    assert norm(lib, x=O, out=O, xsh=0, xst=64, ro=None) == INV
+    assert norm(lib, out=O, ro=O) == INV
     assert norm(lib, T=0, dim=72, xq=None, xs=None) == OK   # bf16 output: dim % 8
 
 
@@ -74,9 +81,9 @@ def test_mxfp4_projection_refusals(lib):
 
     assert wkv(T=0, x=None, w=None, s=None, kv=None, ws=None, nbytes=0) == OK
     for bad in (dict(T=-1), dict(K=0), dict(N=0), dict(x=None), dict(w=None), dict(s=None), dict(kv=None),
-                dict(x=P + 2), dict(w=P + 8), dict(s=P + 1)):
+                dict(x=P + 2), dict(w=P + 8), dict(s=P + 1), dict(s=P + 4)):
         assert wkv(**bad) == INV, bad
-    for bad in (dict(K=192), dict(K=1 << 21), dict(N=66)):
+    for bad in (dict(K=192), dict(K=1 << 21), dict(N=66), dict(N=(1 << 28) + 4)):
         assert wkv(**bad) == UNS, bad
     # a workspace only where the weight is expanded: past the GEMV and K % 256 != 0
     assert lib.engram_wkv_workspace_size(300, 256, 64, F4) == 0
