@@ -270,17 +270,17 @@ def wkv(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor | None = None,
     scales [N/32, K/32]) or MXFP4 (w = uint8 packed codes [N, K/2], scales
     [N, K/32]), told apart by w's shape."""
     L = load_library()
-    _dense(x, "x")
-    _dense(w, "w")
+    if not x.is_contiguous() or not w.is_contiguous():
+        raise ValueError("x and w must be contiguous")
     T, K = x.shape
     N = w.shape[0]
-    fmt = _format(w, w_scales, K)
-    if fmt == W_MXFP4:
+    if w_scales is not None and w.dim() == 2 and 2 * w.shape[1] == K:
         _check_mxfp4(w, w_scales, N, K)
         if x.dtype != torch.bfloat16:
             raise ValueError("MXFP4 wkv needs bf16 x (wkv_mx takes MXFP8 activations)")
         return _product(L, L.engram_wkv, L.engram_wkv_workspace_size, (x.data_ptr(),), x.get_device(), T, K, w,
-                        w_scales, fmt, N, kv, workspace)
+                        w_scales, W_MXFP4, N, kv, workspace)
+    fmt = W_BF16 if w_scales is None else W_MXFP8
     if w.dim() != 2 or w.shape[1] != K:
         raise ValueError(f"w must be [N, {K}], got {tuple(w.shape)}")
     if fmt == W_MXFP8:
@@ -312,7 +312,8 @@ def _product(L, fn, workspace_size, xp, dev, T, K, w, w_scales, fmt, N, kv, work
         raise ValueError(f"kv must be bf16 [{T}, {N}], contiguous, on x's device")
     ws, ws_bytes = None, 0
     if workspace is None:
-        ws_bytes = workspace_size(T, K, N, fmt)
+        # no workspace where K % 256 == 0 (MXFP8 from MXFP8 activations: never)
+        ws_bytes = workspace_size(T, K, N, fmt) if K & 255 else 0
         if ws_bytes:
             workspace = w.new_empty(ws_bytes)
             ws = workspace.data_ptr()
@@ -320,7 +321,13 @@ def _product(L, fn, workspace_size, xp, dev, T, K, w, w_scales, fmt, N, kv, work
         if workspace.get_device() != dev:
             raise ValueError("workspace must be on x's device")
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _run_on(dev, fn, *xp, T, K, w.data_ptr(), w_scales.data_ptr(), fmt, N, kv.data_ptr(), ws, ws_bytes)
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*xp, T, K, w.data_ptr(), w_scales.data_ptr(), fmt, N, kv.data_ptr(), ws, ws_bytes,
+                    torch._C._cuda_getCurrentRawStream(dev))
+        if status:
+            _check(status)
+    else:
+        _run_on(dev, fn, *xp, T, K, w.data_ptr(), w_scales.data_ptr(), fmt, N, kv.data_ptr(), ws, ws_bytes)
     return kv
 
 
