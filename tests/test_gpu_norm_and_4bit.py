@@ -217,7 +217,7 @@ def test_norm_codes_match_the_quantizer_where_y_is_bf16():
     assert (a == b)[keep].mean() > 0.95
 
 
-KN = [(128, 4), (256, 64), (384, 100), (2048, 272), (4224, 96), (1024, 20480 // 8), (640, 1284), (2560, 5 * 16 * 3 + 36)]
+KN = [(128, 4), (256, 64), (384, 100), (4096, 36), (8192, 20), (2048, 272), (4224, 96), (1024, 20480 // 8), (640, 1284), (2560, 5 * 16 * 3 + 36)]
 
 
 @pytest.mark.parametrize("K,N", KN)
