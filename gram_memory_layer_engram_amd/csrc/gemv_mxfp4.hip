@@ -32,6 +32,13 @@
 // 64 bytes of W, 4 x 256 or 8 x 128 bytes of x) cost 8 to 16, and the
 // workgroup's scale bytes are one contiguous run. The rings are private to a
 // wave: it waits for its own DMAs only, no barrier in the loop.
+//
+// Measured (N 20480, K 2048, 22.3 MB of weight; graph replay, about 2.5 us of
+// it an empty kernel's): x bf16, T 1 / 16 / 32 / 61 in 7.0 / 7.3 / 9.0 / 12.2 us
+// (fragments straight from memory: 9.0 / 10.5 / 12.9 / 17), x MXFP8 6.2 / 6.4 /
+// 7.7 / 9.8 us. Up to 16 tokens the weight's stream bounds it (5 TB/s past the
+// launch); beyond 32, x: 256 workgroups read its 250 KB (bf16, T 61) each from
+// L2, three times the weight's bytes.
 #include <algorithm>
 
 #include "common.h"
