@@ -130,6 +130,23 @@ def test_norm_more_rows_than_one_grid_dimension():
     assert bool(torch.isfinite(out).all())
 
 
+def test_norm_offsets_past_32_bits():
+    """More than 2^32 elements: the last rows, and rows on both sides of the
+    2^31- and 2^32-element marks."""
+    E = _E()
+    T, dim = (1 << 20) + 37, 4096
+    g = torch.Generator(device=DEV).manual_seed(2)
+    part = torch.randn((4099, dim), generator=g, device=DEV).to(torch.bfloat16)
+    x = part.repeat((T + 4098) // 4099, 1)[:T]
+    r = part[:1].expand(T, dim)
+    w = (1 + 0.1 * torch.randn((dim,), generator=g, device=DEV)).to(torch.bfloat16)
+    res, out, xq, xs = E.add_rms_norm(x, r, w, out_format="both")
+    at = torch.cat([torch.arange(0, 5), torch.arange((1 << 19) - 3, (1 << 19) + 3),
+                    torch.arange((1 << 20) - 3, T)]).to(DEV)
+    s, y = _norm_ref(x[at][:, None].cpu(), r[at][:, None].cpu(), w.cpu(), 1e-6)
+    _check_norm(dim, s, y, res[at][:, None], out[at][:, None], xq[at][:, None], xs[at][:, None])
+
+
 def test_norm_strides_broadcast_two_dims_and_in_place():
     E = _E()
     rng = np.random.default_rng(3)
@@ -344,15 +361,15 @@ def test_wkv_mx_with_mxfp8_weights_is_wkv_without_its_quantizer(T, K, N):
     assert torch.equal(E.wkv_mx(xq, xs, w, s), E.wkv(x, w, s))
 
 
-@pytest.mark.parametrize("T,dim,hc", [(1, 512, 4), (16, 256, 2), (40, 136, 2), (64, 512, 1), (65, 512, 2), (300, 512, 4),
-                                      (257, 264, 2)])
+@pytest.mark.parametrize("T,dim,hc,C", [(1, 512, 4, 8), (16, 256, 2, 8), (40, 136, 2, 8), (64, 512, 1, 6), (65, 512, 2, 8),
+                                        (300, 512, 4, 8), (257, 264, 2, 8), (90, 256, 2, 6), (90, 136, 2, 6)])
 @pytest.mark.parametrize("fp8_table", [False, True])
-def test_forward_mxfp4(T, dim, hc, fp8_table):
+def test_forward_mxfp4(T, dim, hc, C, fp8_table):
     """The layer's forward on a 4-bit wkv weight, every route, against the
     oracle's forward (gate tolerance as the other formats' tests)."""
     E = _E()
     rng = np.random.default_rng(T + dim)
-    C, hd, R = 8, 64, 501
+    hd, R = 64, 501      # C 6: K 384, the weight expanded past the GEMV
     K, N = C * hd, (hc + 1) * dim
     wq, ws = mxfp4_weight(rng, N, K, 122, 126)
     ids = torch.from_numpy(rng.integers(0, R, size=(T, C)).astype(np.int32)).to(DEV)
@@ -380,6 +397,10 @@ def test_forward_mxfp4(T, dim, hc, fp8_table):
         assert np.all(np.abs(got - ref) <= 2e-2 + 1e-2 * np.abs(ref))
         assert torch.equal(out[~mask], hidden[~mask])
         outs.append(out)
+    plan = E.ForwardPlan(table, ids, wd, sd, hidden, q, k, mask, table_scales=ts)
+    for _ in range(2):
+        plan.out.zero_()
+        assert torch.equal(plan.run(), outs[0])
     if T <= 64:
         a = E.forward_noalloc(table, ids, wd, sd, hidden, q, k, mask, table_scales=ts)
         assert torch.equal(a, outs[0])
@@ -547,6 +568,29 @@ def test_mxfp4_many_tiles(op, T, K, N):
         kv = E.wkv_mx(torch.from_numpy(xq).to(DEV), torch.from_numpy(xs).to(DEV), wd, sd)
     ref, tol = product_tolerance(xa[toks], wa, scaled=op == "wkv_mx")
     _inside(bf16_values(bits(kv[torch.from_numpy(toks).to(DEV)])), ref, tol, op)
+
+
+@pytest.mark.parametrize("op", ["wkv", "wkv_mx"])
+def test_mxfp4_output_offsets_past_32_bits(op):
+    """kv of more than 2^32 elements (and x rows past 2^31 bytes of kv)."""
+    E = _E()
+    T, K, N = 70003, 256, 65536
+    rng = np.random.default_rng(5)
+    wq, ws = mxfp4_weight(rng, N, K)
+    wd, sd = torch.from_numpy(wq).to(DEV), torch.from_numpy(ws).to(DEV)
+    toks = np.concatenate([np.arange(3), [32767, 32768, 65535, 65536], np.arange(T - 5, T)])
+    cols = np.concatenate([np.arange(8), np.arange(N // 2 - 4, N // 2 + 4), np.arange(N - 300, N)])
+    if op == "wkv":
+        x = bf16(rng, T, K)
+        xa = o.bf16_to_f64(bits(x[torch.from_numpy(toks)]))
+        kv = E.wkv(x.to(DEV), wd, sd)
+    else:
+        xq, xs = mxfp8_rows(rng, T, K)
+        xa = o.mx_dequantize_activations(xq[toks], xs[toks])
+        kv = E.wkv_mx(torch.from_numpy(xq).to(DEV), torch.from_numpy(xs).to(DEV), wd, sd)
+    ref, tol = product_tolerance(xa, o.mxfp4_dequantize_weight(wq[cols], ws[cols]), scaled=op == "wkv_mx")
+    got = kv[torch.from_numpy(toks).to(DEV)][:, torch.from_numpy(cols).to(DEV)]
+    _inside(bf16_values(bits(got)), ref, tol, op)
 
 
 @pytest.mark.parametrize("T,K,N", [(1, 32768, 36), (20, 32768, 36), (50, 36864, 20), (40, 131072, 32), (3, 163840, 8),
