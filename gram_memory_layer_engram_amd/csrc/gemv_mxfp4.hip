@@ -42,6 +42,7 @@
 #include <algorithm>
 
 #include "common.h"
+#include "gemv_fp4_dma.h"
 
 namespace engram {
 
@@ -122,13 +123,10 @@ __global__ __launch_bounds__(WAVES * 64) void gemv_mxfp4_kernel(
   // word of each of 16 rows, kb bytes apart. SWAP (kb % 128 == 0: those words
   // share one or two banks of 16): the 16-byte pieces of row r are swapped by
   // 3 or 4 bits of r, for 8 or 16 | kb / 16, which puts them on distinct banks.
-  auto swap = [&](int row) { return SWAP ? (kb % 256 == 0 ? (row & 15) : (row & 15) >> 1) << 4 : 0; };
   {
     const rsrc_t rs = make_rsrc(ws + (int64_t)n0 * kb, (uint32_t)rows * (uint32_t)kb);
     for (int q = wave; q * 1024 < 16 * RT * kb; q += WAVES) {
-      const uint32_t ofs = (uint32_t)(q * 1024 + lane * 16);
-      const uint32_t row = SWAP ? ofs / (uint32_t)kb : 0u;
-      const uint32_t vo = row * kb + ((ofs - row * kb) ^ (uint32_t)swap((int)row));
+      const uint32_t vo = fp4::s_source(SWAP, (uint32_t)(q * 1024 + lane * 16), (uint32_t)kb);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(lds + q * 1024), 16, vo, 0, 0, 0);
     }
     if constexpr (A8) {
@@ -139,10 +137,7 @@ __global__ __launch_bounds__(WAVES * 64) void gemv_mxfp4_kernel(
     }
   }
 
-  // W: a DMA fills 16 rows x 64 bytes, piece p of row r at p ^ ((r >> 1) & 3);
-  // x bf16: 4 rows x 256 bytes, x MXFP8: 8 rows x 128 bytes, piece p of row r
-  // at p ^ (r & 7). Eight rows' reads of one piece then fall on distinct banks.
-  const uint32_t wvo = (uint32_t)((lane >> 2) * wpitch + (((lane & 3) ^ ((lane >> 3) & 3)) << 4));
+  // the DMAs' lane offsets and the fragments' LDS addresses: gemv_fp4_dma.h
   auto issue = [&](int u) {   // unit u of this wave: W with a step's first unit, then x
     const int s = s0 + u / UPS, j0 = u % UPS * JG;
     if (j0 == 0) {
@@ -150,17 +145,13 @@ __global__ __launch_bounds__(WAVES * 64) void gemv_mxfp4_kernel(
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_ptr_t)(lds + slot + rt * 1024), 16,
-                                                 wvo + (uint32_t)(rt * 16 * wpitch), s * 64, 0, 0);
+                                                 fp4::w_voffset(lane, rt, wpitch), s * fp4::kWStep, 0, 0);
     }
     const int slot = xring + u % XS * XUNIT;
-    constexpr int RPI = A8 ? 8 : 4, PPR = 64 / RPI;   // rows of a DMA, pieces of a row
 #pragma unroll
-    for (int i = 0; i < XI; ++i) {
-      const int row = i * RPI + lane / PPR;
-      const uint32_t vo = (uint32_t)((j0 * 16 + row) * xpitch + (((lane % PPR) ^ (row & 7)) << 4));
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_ptr_t)(lds + slot + i * 1024), 16, vo, s * (A8 ? 128 : 256),
-                                               0, 0);
-    }
+    for (int i = 0; i < XI; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_ptr_t)(lds + slot + i * 1024), 16,
+                                               fp4::x_voffset(A8, lane, j0 * 16, i, xpitch), s * fp4::x_step(A8), 0, 0);
   };
 
   f32x4 acc[RT][NT];
@@ -180,9 +171,9 @@ __global__ __launch_bounds__(WAVES * 64) void gemv_mxfp4_kernel(
 
   auto multiply = [&](int u, int p) {   // p: u % UPS, static
     const int s = s0 + u / UPS;
-    const char* wl = lds + ring + (s - s0) % DW * (RT * 1024) + r * 64 + ((g ^ ((r >> 1) & 3)) << 4);
-    const char* xl = lds + xring + u % XS * XUNIT + r * (A8 ? 128 : 256);
-    const uint8_t* sl = reinterpret_cast<const uint8_t*>(lds) + r * kb + ((s * 4) ^ swap(r)) + g;
+    const char* wl = lds + ring + (s - s0) % DW * (RT * 1024) + fp4::w_read(r, g);
+    const char* xl = lds + xring + u % XS * XUNIT;
+    const uint8_t* sl = reinterpret_cast<const uint8_t*>(lds) + fp4::s_read(SWAP, (uint32_t)r, (uint32_t)(s * 4), (uint32_t)kb) + g;
     i32x4 wv[RT];
     uint32_t sc[RT];
 #pragma unroll
@@ -193,8 +184,8 @@ __global__ __launch_bounds__(WAVES * 64) void gemv_mxfp4_kernel(
     if constexpr (A8) {
 #pragma unroll
       for (int j = 0; j < JG; ++j) {
-        const i32x4 lo = *reinterpret_cast<const i32x4*>(xl + j * 2048 + ((g ^ (r & 7)) << 4));
-        const i32x4 hi = *reinterpret_cast<const i32x4*>(xl + j * 2048 + (((4 + g) ^ (r & 7)) << 4));
+        const i32x4 lo = *reinterpret_cast<const i32x4*>(xl + j * 2048 + fp4::x_read(true, r, g));
+        const i32x4 hi = *reinterpret_cast<const i32x4*>(xl + j * 2048 + fp4::x_read(true, r, 4 + g));
         const int xsc = sl[xsl + j * 16 * kb];
         const i32x8 xb = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
@@ -211,7 +202,7 @@ __global__ __launch_bounds__(WAVES * 64) void gemv_mxfp4_kernel(
         bf16x8_t xb[JG];
 #pragma unroll
         for (int j = 0; j < JG; ++j)
-          xb[j] = *reinterpret_cast<const bf16x8_t*>(xl + j * 4096 + (((4 * g + i) ^ (r & 7)) << 4));
+          xb[j] = *reinterpret_cast<const bf16x8_t*>(xl + j * 4096 + fp4::x_read(false, r, 4 * g + i));
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
           const float scale = __uint_as_float(sc[rt] << 23);
