@@ -453,7 +453,12 @@ static int run_forward(const engram_forward_args* a, int32_t K, int32_t N, uint8
   const bool tiled = a->w_format == ENGRAM_W_BF16    ? !gemv_bf16_supported(a->T, K, N)
                      : a->w_format == ENGRAM_W_MXFP8 ? !gemv_mxfp8_supported(a->T, K)
                                                      : !gemv_mxfp4_supported(a->T, K, false);
-  const bool epi = !(a->options & ENGRAM_FORWARD_STORE_KV) && tiled && a->dim % 256 == 0;
+  // MXFP4 weights: only where the plain store would take the epilogue's
+  // 256x256 tile as well; smaller tiles and a gate from kv beat it elsewhere (N
+  // 20480, K 2048: T 65 49 -> 24 us a forward, T 300 57 -> 41, T 1000 113 -> 95).
+  const bool epi = !(a->options & ENGRAM_FORWARD_STORE_KV) && tiled && a->dim % 256 == 0 &&
+                   (a->w_format != ENGRAM_W_MXFP4 || K % 256 != 0 ||
+                    gemm_mxfp4_tile(a->T, N) == MxFp4Tile::k256x256);
   uint16_t* value = (uint16_t*)kv;
   float2* part = (float2*)((uint8_t*)kv + round_up((size_t)a->T * a->dim * 2));
   const GateEpi ep = epi ? GateEpi{(const uint16_t*)a->hidden, (const uint16_t*)a->q_weight,

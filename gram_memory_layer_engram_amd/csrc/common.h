@@ -133,6 +133,10 @@ hipError_t launch_gemv_mxfp8(const uint8_t* xq, const uint8_t* xs, int64_t T,
                              int K, const uint8_t* w, const uint8_t* ws, int N,
                              void* kv, hipStream_t s);
 
+// Tile (W rows x tokens) the MXFP4 GEMM stores kv with for (T, N).
+enum class MxFp4Tile { k256x256, k256x128, k128x128 };
+MxFp4Tile gemm_mxfp4_tile(int64_t T, int N);
+
 // Tiled GEMM with MXFP4 weights (K % 256 == 0, N % 4 == 0): x bf16, or MXFP8
 // codes when xs is not null.
 hipError_t launch_gemm_mxfp4(const void* x, const uint8_t* xs, int64_t T, int K, const uint8_t* w,

@@ -475,25 +475,31 @@ hipError_t launch_tile(const void* x, const uint8_t* xs, int T, int K, const uin
 
 }  // namespace
 
-hipError_t launch_gemm_mxfp4(const void* x, const uint8_t* xs, int64_t T, int K, const uint8_t* w,
-                             const uint8_t* ws, int N, void* kv, hipStream_t s, const GateEpi& ep) {
-  // The tile by what its rounds cost, a full round of 256x256 tiles being 100.
-  // Larger tiles move fewer bytes a flop; smaller ones fill the compute units
-  // where there are few, and end sooner. Measured at K 2048, bf16 x: a round
-  // of 256x128 tiles costs 60 of that, one of 128x128 tiles 60 as well with
-  // two workgroups on a compute unit and 42 with one (N 20480: T 128 in 40 / 24
-  // / 18 us for 256x256 / 256x128 / 128x128, T 515 50 / 53 / 52, T 1000 90 / 83
-  // / 74, T 8192 490 / 540 / 550). The gate's epilogue has the 256x256 tile
-  // only.
+// The tile by what its rounds cost, a full round of 256x256 tiles being 100.
+// Larger tiles move fewer bytes a flop; smaller ones fill the compute units
+// where there are few, and end sooner. Measured at K 2048, bf16 x: a round of
+// 256x128 tiles costs 60 of that, one of 128x128 tiles 60 as well with two
+// workgroups on a compute unit and 42 with one (N 20480: T 128 in 40 / 24 / 18
+// us for 256x256 / 256x128 / 128x128, T 515 50 / 53 / 52, T 1000 90 / 83 / 74, T
+// 8192 490 / 540 / 550).
+MxFp4Tile gemm_mxfp4_tile(int64_t T, int N) {
   const int64_t cus = dev_info().num_cus;
   auto tiles = [&](int tm, int tt) { return ((int64_t)N + tm - 1) / tm * ((T + tt - 1) / tt); };
   auto rounds = [&](int64_t n) { return (n + cus - 1) / cus; };
   const int64_t n22 = tiles(128, 128), last = n22 % (2 * cus);
   const int64_t c44 = 100 * rounds(tiles(256, 256)), c42 = 60 * rounds(tiles(256, 128));
   const int64_t c22 = 60 * (n22 / (2 * cus)) + (last > cus ? 60 : last > 0 ? 42 : 0);
-  if (ep.hidden || (c44 <= c42 && c44 <= c22)) return launch_tile<4, 4>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep);
-  if (c42 <= c22) return launch_tile<4, 2>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep);
-  return launch_tile<2, 2>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep);
+  return c44 <= c42 && c44 <= c22 ? MxFp4Tile::k256x256 : c42 <= c22 ? MxFp4Tile::k256x128 : MxFp4Tile::k128x128;
+}
+
+// The gate's epilogue has the 256x256 tile only.
+hipError_t launch_gemm_mxfp4(const void* x, const uint8_t* xs, int64_t T, int K, const uint8_t* w,
+                             const uint8_t* ws, int N, void* kv, hipStream_t s, const GateEpi& ep) {
+  switch (ep.hidden ? MxFp4Tile::k256x256 : gemm_mxfp4_tile(T, N)) {
+    case MxFp4Tile::k256x256: return launch_tile<4, 4>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep);
+    case MxFp4Tile::k256x128: return launch_tile<4, 2>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep);
+    default: return launch_tile<2, 2>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep);
+  }
 }
 
 }  // namespace engram

@@ -404,7 +404,9 @@ typedef struct engram_forward_args {
  *   value, so the keys never reach HBM; a small finish kernel then forms the
  *   gate and the update. ENGRAM_FORWARD_STORE_KV turns this off: kv is
  *   stored whole and the plain gate kernel reads it back (the composition of
- *   engram_wkv and engram_gate). Elsewhere the option has no effect. The two
+ *   engram_wkv and engram_gate). With ENGRAM_W_MXFP4 and
+ *   K % 256 == 0 the epilogue is used only where T and N fill the compute
+ *   units with 256x256 tiles. Elsewhere the option has no effect. The two
  *   routes agree to the rounding of the gate's sums (the same bf16 keys
  *   summed in another order).
  */

@@ -406,6 +406,38 @@ def test_forward_mxfp4(T, dim, hc, C, fp8_table):
         assert torch.equal(a, outs[0])
 
 
+def test_forward_mxfp4_gate_epilogue():
+    """Enough tokens that the forward's default is the GEMM's gate epilogue (6
+    x 80 tiles of 256x256 on 256 compute units), and the route that stores kv:
+    sampled tokens against the oracle, the two against each other."""
+    E = _E()
+    rng = np.random.default_rng(21)
+    T, dim, hc, C, hd, R = 1491, 4096, 4, 4, 64, 301
+    K, N = C * hd, (hc + 1) * dim
+    wq, ws = mxfp4_weight(rng, N, K, 122, 126)
+    table = bf16(rng, R, hd, scale=0.1).to(DEV)
+    ids = torch.from_numpy(rng.integers(0, R, size=(T, C)).astype(np.int32)).to(DEV)
+    hidden = bf16(rng, T, hc, dim).to(DEV)
+    q = (1 + 0.1 * bf16(rng, hc, dim).float()).to(torch.bfloat16).to(DEV)
+    k = (1 + 0.1 * bf16(rng, hc, dim).float()).to(torch.bfloat16).to(DEV)
+    mask = torch.from_numpy(rng.random(T) > 0.2).to(DEV)
+    wd, sd = torch.from_numpy(wq).to(DEV), torch.from_numpy(ws).to(DEV)
+    gates = [torch.full((T, hc), -1.0, dtype=torch.float32, device=DEV) for _ in range(2)]
+    outs = [E.forward(table, ids, wd, sd, hidden, q, k, mask, gate_out=g, store_kv=sk)
+            for g, sk in zip(gates, (False, True))]
+    assert float((gates[0] - gates[1]).abs().max()) < 1e-3
+    toks = sample_tokens(T, 24, seed=2)
+    at = torch.from_numpy(toks).to(DEV)
+    rows, _ = o.gather_rows(bits(table), ids[at].cpu().numpy())
+    kv_bits, _ = o.wkv(rows.reshape(len(toks), K), wq, ws)
+    want, g = o.gate(bits(hidden[at]), kv_bits, bits(q), bits(k), mask[at].cpu().numpy(), 1e-6, 1e-6)
+    ref = o.bf16_to_f64(want)
+    for out, gate in zip(outs, gates):
+        assert np.abs(gate[at].cpu().numpy() - g).max() < 2e-2
+        assert np.all(np.abs(bf16_values(bits(out[at])) - ref) <= 2e-2 + 1e-2 * np.abs(ref))
+        assert torch.equal(out[~mask], hidden[~mask])
+
+
 def test_a_layer_then_norm_then_projection():
     """The operators as they are used: the layer's forward, its streams added
     to a branch and normalized into MXFP8, and that multiplied with 4-bit and
