@@ -93,6 +93,16 @@ hipError_t run_mx_projection(const uint8_t* xq, const uint8_t* xs, int64_t T, in
              : launch_gemm_mxfp8(xq, xs, T, K, (const uint8_t*)w, w_scales, N, kv, s, ep);
 }
 
+// A tensor's address range; no range where the pointer is null.
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+inline bool meet(const Span& a, const Span& b) {
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  return x && y && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+}
+
 constexpr GateEpi kPlainStore{nullptr, nullptr, nullptr, nullptr, nullptr, 0, 0};
 
 // The tiled GEMM with MXFP4 weights and bf16 x.
@@ -348,15 +358,24 @@ int engram_add_rms_norm(const void* x, int64_t x_stride_t, int64_t x_stride_h, c
   if (!x || (!out && !xq)) return ENGRAM_EINVAL;
   for (const void* p : {x, residual, weight, (const void*)residual_out, (const void*)out, (const void*)xq})
     if (!aligned16(p)) return ENGRAM_EINVAL;
-  // in place (residual_out on residual, out on x) row by row only, and never
-  // two outputs on one buffer
-  auto rows_dense = [&](int64_t st, int64_t sh) {
-    return (T == 1 || st == (int64_t)hc * dim) && (hc == 1 || sh == dim);
+  // in place is row by row: residual_out on residual and out on x, dense and
+  // whole; any other overlap of an output with another tensor is refused
+  const int64_t n = T * hc * dim;
+  const Span sx{x, 2 * ((T - 1) * x_stride_t + (hc - 1) * x_stride_h + dim)};
+  const Span sr{residual, 2 * ((T - 1) * residual_stride_t + (hc - 1) * residual_stride_h + dim)};
+  const Span sw{weight, 2 * (int64_t)weight_hc * dim};
+  const Span so[4] = {{residual_out, 2 * n}, {out, 2 * n}, {xq, n}, {xs, n / 32}};
+  auto in_place = [&](const Span& o, const Span& i, int64_t st, int64_t sh) {
+    return o.p == i.p && (T == 1 || st == (int64_t)hc * dim) && (hc == 1 || sh == dim);
   };
-  if (residual_out && residual_out == residual && !rows_dense(residual_stride_t, residual_stride_h))
-    return ENGRAM_EINVAL;
-  if (out && out == x && !rows_dense(x_stride_t, x_stride_h)) return ENGRAM_EINVAL;
-  if (out && out == residual_out) return ENGRAM_EINVAL;
+  for (int i = 0; i < 4; ++i) {
+    if (meet(so[i], sw)) return ENGRAM_EINVAL;
+    if (meet(so[i], sx) && !(i == 1 && in_place(so[i], sx, x_stride_t, x_stride_h))) return ENGRAM_EINVAL;
+    if (meet(so[i], sr) && !(i == 0 && in_place(so[i], sr, residual_stride_t, residual_stride_h)))
+      return ENGRAM_EINVAL;
+    for (int j = 0; j < i; ++j)
+      if (meet(so[i], so[j])) return ENGRAM_EINVAL;
+  }
   const RmsNormArgs a{(const uint16_t*)x, x_stride_t, x_stride_h, (const uint16_t*)residual,
                       residual_stride_t, residual_stride_h, (const uint16_t*)weight, weight_hc, T * hc, hc,
                       dim, eps, (uint16_t*)residual_out, (uint16_t*)out, xq, xs};

@@ -248,8 +248,9 @@ int engram_wkv_mx(const uint8_t* xq, const uint8_t* xs, int64_t T, int32_t K, co
  *   residual_out  optional bf16 [T, hc, dim] contiguous; may be `residual`
  *                 itself (in place) when that is contiguous (else EINVAL).
  *   out           optional bf16 [T, hc, dim] contiguous; may be `x` itself
- *                 when that is contiguous (else EINVAL). No other overlap
- *                 is allowed.
+ *                 when that is contiguous (else EINVAL). Any other overlap
+ *                 of an output with another tensor's address range is
+ *                 EINVAL.
  *   xq, xs        optional, both or neither: uint8 [T, hc, dim] and
  *                 [T, hc, dim/32]. At least one of out and xq.
  *   eps           >= 0 (a row of zeros with eps 0 gives NaN).

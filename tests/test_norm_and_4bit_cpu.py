@@ -62,7 +62,12 @@ def test_add_rms_norm_refusals(lib):
         assert norm(lib, **bad) == INV, bad
     for bad in (dict(dim=60), dict(dim=72), dict(dim=16416), dict(xst=129), dict(rsh=4), dict(T=2**31 // 2)):
         assert norm(lib, **bad) == UNS, bad
-    # in place on rows that are not dense, and two outputs on one buffer
+    # in place on rows that are not dense, and any other overlap with an output (a tensor is 1 KiB of bf16)
+    assert norm(lib, ro=2 * P + 16) == INV and norm(lib, out=P + 512) == INV       # shifted on its own input
+    assert norm(lib, ro=P) == INV and norm(lib, out=2 * P) == INV                  # on the other input
+    assert norm(lib, out=3 * P) == INV and norm(lib, xs=3 * P + 255) == INV        # on the weight
+    assert norm(lib, xq=5 * P + 1008) == INV and norm(lib, xs=6 * P + 511) == INV  # on another output
+    assert norm(lib, out=P + 1536, xst=512) == INV                                 # inside a strided input's range
     R, O = 0x20000, 0x30000
     assert norm(lib, r=R, ro=R, rst=256, out=O) == INV
     assert norm(lib, r=R, ro=R, rsh=0, rst=64, out=O) == INV
