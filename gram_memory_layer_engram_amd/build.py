@@ -13,8 +13,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libengram.so")
 SOURCES = ["abi.hip", "lookup.hip", "gate.hip", "mxq.hip", "gemm.hip", "gemv_mxfp8.hip", "gemv_bf16.hip", "decode_forward.hip",
-           "probe.hip", "rms_norm.hip", "mxfp4.hip", "gemv_mxfp4.hip",
-           "gemm_fp4.hip"]
+           "probe.hip", "rms_norm.hip", "gemv_mxfp4.hip", "gemm_fp4.hip"]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

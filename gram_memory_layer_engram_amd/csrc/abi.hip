@@ -48,18 +48,9 @@ size_t mx_stage_bytes(int64_t T, int32_t K) {
   return round_up((size_t)T * K) + round_up((size_t)T * (K / 32));
 }
 
-// MXFP4 weights: the GEMV, the tiled GEMM on the codes (K % 256 == 0), or the
-// weight expanded to bf16 in the workspace for the bf16 GEMM.
-bool mxfp4_expands(int64_t T, int64_t K, bool x_mxfp8) {
-  return K % 256 != 0 && !gemv_mxfp4_supported(T, (int)K, x_mxfp8);
-}
-
-// Scratch of a projection from bf16 x besides kv: MXFP8 staging of x, or the
-// MXFP4 weight expanded to bf16 for the tiled GEMM.
-size_t wkv_scratch_bytes(int64_t T, int64_t K, int64_t N, int32_t w_format) {
-  if (w_format == ENGRAM_W_MXFP8) return mx_stage_bytes(T, (int32_t)K);
-  if (w_format == ENGRAM_W_MXFP4 && mxfp4_expands(T, K, false)) return round_up((size_t)N * K * 2);
-  return 0;
+// Scratch of a projection from bf16 x besides kv: MXFP8 staging of x.
+size_t wkv_scratch_bytes(int64_t T, int64_t K, int32_t w_format) {
+  return w_format == ENGRAM_W_MXFP8 ? mx_stage_bytes(T, (int32_t)K) : 0;
 }
 
 int check_wkv(const void* x, int64_t T, int32_t K, const void* w,
@@ -105,15 +96,6 @@ inline bool meet(const Span& a, const Span& b) {
 
 constexpr GateEpi kPlainStore{nullptr, nullptr, nullptr, nullptr, nullptr, 0, 0};
 
-// The tiled GEMM with MXFP4 weights and bf16 x.
-int run_mxfp4_tiled(const void* x, int64_t T, int32_t K, const void* w, const uint8_t* w_scales, int32_t N,
-                    void* kv, void* workspace, hipStream_t s, const GateEpi& ep) {
-  if (K % 256 == 0)
-    return hip_status(launch_gemm_mxfp4(x, nullptr, T, K, (const uint8_t*)w, w_scales, N, kv, s, ep));
-  if (launch_mxfp4_to_bf16(w, w_scales, N, K, workspace, s) != hipSuccess) return ENGRAM_EHIP;
-  return hip_status(launch_gemm_bf16(x, T, K, workspace, N, kv, s, ep));
-}
-
 // Enqueue the projection given a workspace already checked to be large enough.
 int run_wkv(const void* x, int64_t T, int32_t K, const void* w,
             const uint8_t* w_scales, int32_t w_format, int32_t N, void* kv,
@@ -125,7 +107,7 @@ int run_wkv(const void* x, int64_t T, int32_t K, const void* w,
   if (w_format == ENGRAM_W_MXFP4) {
     if (!ep.hidden && gemv_mxfp4_supported(T, K, false))
       return hip_status(launch_gemv_mxfp4(x, nullptr, T, K, w, w_scales, N, kv, s));
-    return run_mxfp4_tiled(x, T, K, w, w_scales, N, kv, workspace, s, ep);
+    return hip_status(launch_gemm_mxfp4(x, nullptr, T, K, (const uint8_t*)w, w_scales, N, kv, s, ep));
   }
   uint8_t* xq = (uint8_t*)workspace;
   uint8_t* xs = xq + round_up((size_t)T * K);
@@ -140,7 +122,8 @@ int run_wkv_tiled(const void* x, int64_t T, int32_t K, const void* w, const uint
                   int32_t w_format, int32_t N, void* kv, void* workspace, hipStream_t s, const GateEpi& ep) {
   if (T == 0) return ENGRAM_OK;
   if (w_format == ENGRAM_W_BF16) return hip_status(launch_gemm_bf16(x, T, K, w, N, kv, s, ep));
-  if (w_format == ENGRAM_W_MXFP4) return run_mxfp4_tiled(x, T, K, w, w_scales, N, kv, workspace, s, ep);
+  if (w_format == ENGRAM_W_MXFP4)
+    return hip_status(launch_gemm_mxfp4(x, nullptr, T, K, (const uint8_t*)w, w_scales, N, kv, s, ep));
   uint8_t* xq = (uint8_t*)workspace;
   uint8_t* xs = xq + round_up((size_t)T * K);
   if (launch_mx_quantize(x, T, K, xq, xs, s) != hipSuccess) return ENGRAM_EHIP;
@@ -273,8 +256,8 @@ int engram_mx_quantize(const void* x, int64_t T, int32_t K, uint8_t* xq,
 
 size_t engram_wkv_workspace_size(int64_t T, int32_t K, int32_t N,
                                  int32_t w_format) {
-  if (T <= 0 || K <= 0 || (N <= 0 && w_format == ENGRAM_W_MXFP4)) return 0;
-  return wkv_scratch_bytes(T, K, N, w_format);
+  (void)N;
+  return T <= 0 || K <= 0 ? 0 : wkv_scratch_bytes(T, K, w_format);
 }
 
 int engram_wkv_gate_partials(const void* x, int64_t T, int32_t K, const void* w,
@@ -293,8 +276,6 @@ int engram_wkv_gate_partials(const void* x, int64_t T, int32_t K, const void* w,
   if (st != ENGRAM_OK) return st;
   if (T == 0) return ENGRAM_OK;
   if (!partials || ((uintptr_t)partials & 7u)) return ENGRAM_EINVAL;
-  // the GEMV's share of the workspace rule does not apply: this always tiles
-  if (w_format == ENGRAM_W_MXFP4 && K % 256 != 0 && gemv_mxfp4_supported(T, K, false)) return ENGRAM_EUNSUPPORTED;
   const size_t need = engram_wkv_workspace_size(T, K, N, w_format);
   if (workspace_bytes < need || (need && (!workspace || ((uintptr_t)workspace % kAlign))))
     return ENGRAM_EINVAL;
@@ -314,33 +295,18 @@ int engram_wkv(const void* x, int64_t T, int32_t K, const void* w,
   return run_wkv(x, T, K, w, w_scales, w_format, N, kv, workspace, (hipStream_t)stream);
 }
 
-size_t engram_wkv_mx_workspace_size(int64_t T, int32_t K, int32_t N, int32_t w_format) {
-  if (T <= 0 || K <= 0 || N <= 0 || w_format != ENGRAM_W_MXFP4 || !mxfp4_expands(T, K, true)) return 0;
-  return round_up((size_t)N * K * 2) + round_up((size_t)T * K * 2);
-}
-
 int engram_wkv_mx(const uint8_t* xq, const uint8_t* xs, int64_t T, int32_t K, const void* w,
-                  const uint8_t* w_scales, int32_t w_format, int32_t N, void* kv, void* workspace,
-                  size_t workspace_bytes, void* stream) {
+                  const uint8_t* w_scales, int32_t w_format, int32_t N, void* kv, void* stream) {
   int st = check_wkv(xq, T, K, w, w_scales, w_format, N, kv);
   if (st != ENGRAM_OK) return st;
   if (w_format == ENGRAM_W_BF16) return ENGRAM_EUNSUPPORTED;
   if (T == 0) return ENGRAM_OK;
   if (!xs || !aligned16(xs)) return ENGRAM_EINVAL;
-  const size_t need = engram_wkv_mx_workspace_size(T, K, N, w_format);
-  if (workspace_bytes < need || (need && (!workspace || ((uintptr_t)workspace % kAlign))))
-    return ENGRAM_EINVAL;
   hipStream_t s = (hipStream_t)stream;
   if (w_format == ENGRAM_W_MXFP8)
     return hip_status(run_mx_projection(xq, xs, T, K, w, w_scales, N, kv, s, kPlainStore));
   if (gemv_mxfp4_supported(T, K, true)) return hip_status(launch_gemv_mxfp4(xq, xs, T, K, w, w_scales, N, kv, s));
-  if (K % 256 == 0)
-    return hip_status(launch_gemm_mxfp4(xq, xs, T, K, (const uint8_t*)w, w_scales, N, kv, s, kPlainStore));
-  void* wb = workspace;
-  void* xb = (uint8_t*)workspace + round_up((size_t)N * K * 2);
-  if (launch_mxfp4_to_bf16(w, w_scales, N, K, wb, s) != hipSuccess) return ENGRAM_EHIP;
-  if (launch_mxfp8_to_bf16(xq, xs, T, K, xb, s) != hipSuccess) return ENGRAM_EHIP;
-  return hip_status(launch_gemm_bf16(xb, T, K, wb, N, kv, s, kPlainStore));
+  return hip_status(launch_gemm_mxfp4(xq, xs, T, K, (const uint8_t*)w, w_scales, N, kv, s, kPlainStore));
 }
 
 int engram_add_rms_norm(const void* x, int64_t x_stride_t, int64_t x_stride_h, const void* residual,
@@ -420,7 +386,7 @@ size_t engram_forward_workspace_size(const engram_forward_args* a) {
   const int64_t K = (int64_t)a->n_cols * a->head_dim;
   const int64_t N = (int64_t)(a->hc + 1) * a->dim;
   size_t bytes = round_up((size_t)a->T * K * 2) + round_up((size_t)a->T * N * 2);
-  if (K <= INT32_MAX && N <= INT32_MAX) bytes += wkv_scratch_bytes(a->T, K, N, a->w_format);
+  if (K <= INT32_MAX && N <= INT32_MAX) bytes += wkv_scratch_bytes(a->T, K, a->w_format);
   if (K <= INT32_MAX && N <= INT32_MAX && use_decode_path(a, (int32_t)K, (int32_t)N))
     bytes = std::max(bytes, decode_forward_scratch_bytes(a->T, (int)K, (int)N, a->dim));
   return kSyncBytes + bytes;
@@ -476,8 +442,7 @@ static int run_forward(const engram_forward_args* a, int32_t K, int32_t N, uint8
   // 256x256 tile as well; smaller tiles and a gate from kv beat it elsewhere (N
   // 20480, K 2048: T 65 49 -> 24 us a forward, T 300 57 -> 41, T 1000 113 -> 95).
   const bool epi = !(a->options & ENGRAM_FORWARD_STORE_KV) && tiled && a->dim % 256 == 0 &&
-                   (a->w_format != ENGRAM_W_MXFP4 || K % 256 != 0 ||
-                    gemm_mxfp4_tile(a->T, N) == MxFp4Tile::k256x256);
+                   (a->w_format != ENGRAM_W_MXFP4 || gemm_mxfp4_tile(a->T, N) == MxFp4Tile::k256x256);
   uint16_t* value = (uint16_t*)kv;
   float2* part = (float2*)((uint8_t*)kv + round_up((size_t)a->T * a->dim * 2));
   const GateEpi ep = epi ? GateEpi{(const uint16_t*)a->hidden, (const uint16_t*)a->q_weight,

@@ -137,15 +137,10 @@ hipError_t launch_gemv_mxfp8(const uint8_t* xq, const uint8_t* xs, int64_t T,
 enum class MxFp4Tile { k256x256, k256x128, k128x128 };
 MxFp4Tile gemm_mxfp4_tile(int64_t T, int N);
 
-// Tiled GEMM with MXFP4 weights (K % 256 == 0, N % 4 == 0): x bf16, or MXFP8
+// Tiled GEMM with MXFP4 weights (K % 128 == 0, N % 4 == 0): x bf16, or MXFP8
 // codes when xs is not null.
 hipError_t launch_gemm_mxfp4(const void* x, const uint8_t* xs, int64_t T, int K, const uint8_t* w,
                              const uint8_t* ws, int N, void* kv, hipStream_t s, const GateEpi& ep);
-
-// MXFP4 weights (e2m1 [N, K/2], E8M0 [N, K/32]) and MXFP8 rows expanded to
-// bf16 (exact); K % 32 == 0.
-hipError_t launch_mxfp4_to_bf16(const void* w, const uint8_t* scales, int64_t N, int K, void* out, hipStream_t s);
-hipError_t launch_mxfp8_to_bf16(const uint8_t* xq, const uint8_t* xs, int64_t T, int K, void* out, hipStream_t s);
 
 // Largest T the decode GEMV serves; above it the tiled GEMM runs.
 constexpr int kGemvMaxT = 64;

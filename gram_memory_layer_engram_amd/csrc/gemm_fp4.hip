@@ -1,5 +1,5 @@
 // Tiled projection GEMMs with MXFP4 weights: kv[T, N] = bf16(x . deq(W)^T), x
-// bf16 (gemm_fp4_bf16_kernel) or MXFP8 (gemm_fp4_mx_kernel), K % 256 == 0.
+// bf16 (gemm_fp4_bf16_kernel) or MXFP8 (gemm_fp4_mx_kernel), K % 128 == 0.
 //
 // The block (256 W rows x 256 tokens, four waves of 128x128 on 32x32 MFMA
 // tiles), tile order, DMAs and epilogue are the other tiled GEMMs' (gemm.hip).
@@ -7,6 +7,9 @@
 // 32 KiB chunk of W serves four bf16 slices of x (64 k) or two MXFP8 slices
 // (128 k), and a slice moves 40 (48) KiB from L2 instead of 64, which is what
 // bounds those kernels. LDS: two slots for W chunks, a ring of three for x.
+// Where K % 256 == 128 the last chunk is half: its rows' second 64 bytes are
+// the next row's (zeros past the tile), as the second half of its scale bytes
+// is, and the loop ends before the slices that would use them.
 //
 //  * bf16 x: lane (row l%32, half h = l/32) reads, per slice, the 16 bytes of k
 //    32h .. 32h+31 of its row: one scale group. v_cvt_scalef32_pk_bf16_fp4 turns
@@ -45,7 +48,7 @@ constexpr int SG_VALU = 0x002;
 
 template <int V> using Int = std::integral_constant<int, V>;
 
-template <int NI, int NJ>
+template <int NI, int NJ, bool HALF>
 __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(NI == 4 ? 1 : 2, NI == 4 ? 1 : 2)))
 void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const uint8_t* __restrict__ w,
                           const uint8_t* __restrict__ ws, int N, uint16_t* __restrict__ kv, int tiles_n,
@@ -64,7 +67,7 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
   const rsrc_t rb = make_rsrc(x + (int64_t)t0 * K, (uint32_t)min(TN, T - t0) * xpitch);
   const rsrc_t rs = make_rsrc(ws + (int64_t)n0 * kb, (uint32_t)min(TM, N - n0) * kb);
   const uint32_t ooba = (uint32_t)TM * wpitch, oobb = (uint32_t)TN * xpitch;   // at or past the ranges
-  const int nk = K / 64, nc = K / 256;
+  const int nk = K / 64, nc = K / 256 + HALF;   // x slices (even), W chunks
 
   const dma::Lane la = dma::lane_of(wave, lane, wpitch), lb = dma::lane_of(wave, lane, xpitch);
   auto dma_w = [&](int slot, uint32_t kofs, int i) {
@@ -234,18 +237,22 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
     }
     xb = xb + 1 >= 3 ? 0 : xb + 1;
   };
-  for (int d = 0; d < nk; d += 4) {
+  for (int d = 0; d < (HALF ? nk - 2 : nk); d += 4) {
     slice(d, Int<0>{});
     slice(d + 1, Int<1>{});
     slice(d + 2, Int<2>{});
     slice(d + 3, Int<3>{});
+  }
+  if constexpr (HALF) {
+    slice(nk - 2, Int<0>{});
+    slice(nk - 1, Int<1>{});
   }
   __builtin_amdgcn_sched_barrier(0);
   wait_vm<0>();   // the zero-fill DMAs of the last slices land before LDS is reused
   store_tile<NI, NJ>(acc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
 }
 
-template <int NI, int NJ>
+template <int NI, int NJ, bool HALF>
 __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(NI == 4 ? 1 : 2, NI == 4 ? 1 : 2)))
 void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restrict__ xs, int T, int K,
                         const uint8_t* __restrict__ w, const uint8_t* __restrict__ ws, int N,
@@ -265,7 +272,7 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
   const rsrc_t rsa = make_rsrc(ws + (int64_t)n0 * kb, (uint32_t)min(TM, N - n0) * kb);
   const rsrc_t rsb = make_rsrc(xs + (int64_t)t0 * kb, (uint32_t)min(TN, T - t0) * kb);
   const uint32_t ooba = (uint32_t)TM * wpitch, oobb = (uint32_t)TN * xpitch;
-  const int ns = K / 128, nc = K / 256;   // x slices (even), W chunks
+  const int ns = K / 128, nc = K / 256 + HALF;   // x slices, W chunks
 
   const dma::Lane la = dma::lane_of(wave, lane, wpitch), lb = dma::lane_of(wave, lane, xpitch);
   auto dma_w = [&](int slot, uint32_t kofs, int i) {
@@ -445,32 +452,42 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
     }
     xb = xb + 1 >= 3 ? 0 : xb + 1;
   };
-  for (int d = 0; d < ns; d += 2) {
+  for (int d = 0; d < (HALF ? ns - 1 : ns); d += 2) {
     slice(d, Int<0>{});
     slice(d + 1, Int<1>{});
   }
+  if constexpr (HALF) slice(ns - 1, Int<0>{});
   __builtin_amdgcn_sched_barrier(0);
   wait_vm<0>();   // the zero-fill DMAs of the last slices land before LDS is reused
   store_tile<NI, NJ>(acc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
 }
 
-template <int NI, int NJ>
-hipError_t launch_tile(const void* x, const uint8_t* xs, int T, int K, const uint8_t* w, const uint8_t* ws, int N,
+template <int NI, int NJ, bool HALF>
+hipError_t launch_half(const void* x, const uint8_t* xs, int T, int K, const uint8_t* w, const uint8_t* ws, int N,
                        uint16_t* kv, hipStream_t s, const GateEpi& ep) {
   const int tiles_n = (N + 64 * NI - 1) / (64 * NI), tiles_t = (T + 64 * NJ - 1) / (64 * NJ);
   const dim3 grid(tiles_n * tiles_t), block(THREADS);
   constexpr int lds = fp4_lds(NI, NJ);
   hipError_t e;
   if (xs) {
-    const auto fn = gemm_fp4_mx_kernel<NI, NJ>;
+    const auto fn = gemm_fp4_mx_kernel<NI, NJ, HALF>;
     if ((e = set_lds((const void*)fn, lds)) != hipSuccess) return e;
     hipLaunchKernelGGL(fn, grid, block, lds, s, (const uint8_t*)x, xs, T, K, w, ws, N, kv, tiles_n, tiles_t, ep);
   } else {
-    const auto fn = gemm_fp4_bf16_kernel<NI, NJ>;
+    const auto fn = gemm_fp4_bf16_kernel<NI, NJ, HALF>;
     if ((e = set_lds((const void*)fn, lds)) != hipSuccess) return e;
     hipLaunchKernelGGL(fn, grid, block, lds, s, (const uint16_t*)x, T, K, w, ws, N, kv, tiles_n, tiles_t, ep);
   }
   return hipGetLastError();
+}
+
+// The half chunk at the end is code of its own behind the loop: one that the
+// loop leaves early for cost the accumulators' registers (1000 spilled).
+template <int NI, int NJ>
+hipError_t launch_tile(const void* x, const uint8_t* xs, int T, int K, const uint8_t* w, const uint8_t* ws, int N,
+                       uint16_t* kv, hipStream_t s, const GateEpi& ep) {
+  return K % 256 ? launch_half<NI, NJ, true>(x, xs, T, K, w, ws, N, kv, s, ep)
+                 : launch_half<NI, NJ, false>(x, xs, T, K, w, ws, N, kv, s, ep);
 }
 
 }  // namespace

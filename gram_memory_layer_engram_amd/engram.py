@@ -56,8 +56,7 @@ EXPORTS = {
     "engram_wkv": (_i32, [_vp, _i64, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _sz, _vp]),
     "engram_wkv_gate_partials": (_i32, [_vp, _i64, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp,
                                         _vp, _sz, _vp]),
-    "engram_wkv_mx_workspace_size": (_sz, [_i64, _i32, _i32, _i32]),
-    "engram_wkv_mx": (_i32, [_vp, _vp, _i64, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _sz, _vp]),
+    "engram_wkv_mx": (_i32, [_vp, _vp, _i64, _i32, _vp, _vp, _i32, _i32, _vp, _vp]),
     "engram_add_rms_norm": (_i32, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i32, _i64, _i32, _i32, _f32, _vp, _vp,
                                    _vp, _vp, _vp]),
     "engram_gate": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _f32, _f32, _vp, _vp, _vp]),
@@ -274,8 +273,8 @@ def wkv(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor | None = None,
         _check_mxfp4(w, w_scales, N, K)
         if x.dtype != torch.bfloat16:
             raise ValueError("MXFP4 wkv needs bf16 x (wkv_mx takes MXFP8 activations)")
-        return _product(L, L.engram_wkv, L.engram_wkv_workspace_size, (x.data_ptr(),), x.get_device(), T, K, w,
-                        w_scales, W_MXFP4, N, kv, workspace)
+        # no workspace in this format
+        return _product(L.engram_wkv, (x.data_ptr(),), x.get_device(), T, K, w, w_scales, W_MXFP4, N, kv, (None, 0))
     fmt = W_BF16 if w_scales is None else W_MXFP8
     if w.dim() != 2 or w.shape[1] != K:
         raise ValueError(f"w must be [N, {K}], got {tuple(w.shape)}")
@@ -296,9 +295,10 @@ def wkv(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor | None = None,
     return kv
 
 
-def _product(L, fn, workspace_size, xp, dev, T, K, w, w_scales, fmt, N, kv, workspace):
-    """Output, workspace and call of a projection whose operands are checked;
-    xp: x's address, or those of its codes and scales; dev: its device."""
+def _product(fn, xp, dev, T, K, w, w_scales, fmt, N, kv, tail=()):
+    """Output and call of a projection whose operands are checked; xp: x's
+    address, or those of its codes and scales; dev: its device; tail: arguments
+    past kv."""
     if w.get_device() != dev or w_scales.get_device() != dev or dev < 0:
         _device_of(w, w_scales)
         raise ValueError("x and w are on different devices")
@@ -307,29 +307,18 @@ def _product(L, fn, workspace_size, xp, dev, T, K, w, w_scales, fmt, N, kv, work
         kv = torch.empty_strided((T, N), (N, 1), dtype=torch.bfloat16, device=w.device)
     elif kv.shape != (T, N) or kv.dtype != torch.bfloat16 or not kv.is_contiguous() or kv.get_device() != dev:
         raise ValueError(f"kv must be bf16 [{T}, {N}], contiguous, on x's device")
-    ws, ws_bytes = None, 0
-    if workspace is None:
-        # no workspace where K % 256 == 0 (MXFP8 from MXFP8 activations: never)
-        ws_bytes = workspace_size(T, K, N, fmt) if K & 255 else 0
-        if ws_bytes:
-            workspace = w.new_empty(ws_bytes)
-            ws = workspace.data_ptr()
-    else:
-        if workspace.get_device() != dev:
-            raise ValueError("workspace must be on x's device")
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if dev == torch._C._cuda_getDevice():
-        status = fn(*xp, T, K, w.data_ptr(), w_scales.data_ptr(), fmt, N, kv.data_ptr(), ws, ws_bytes,
+        status = fn(*xp, T, K, w.data_ptr(), w_scales.data_ptr(), fmt, N, kv.data_ptr(), *tail,
                     torch._C._cuda_getCurrentRawStream(dev))
         if status:
             _check(status)
     else:
-        _run_on(dev, fn, *xp, T, K, w.data_ptr(), w_scales.data_ptr(), fmt, N, kv.data_ptr(), ws, ws_bytes)
+        _run_on(dev, fn, *xp, T, K, w.data_ptr(), w_scales.data_ptr(), fmt, N, kv.data_ptr(), *tail)
     return kv
 
 
 def wkv_mx(xq: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
-           kv: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+           kv: torch.Tensor | None = None) -> torch.Tensor:
     """kv = bf16(deq(xq, xs) . deq(W)^T): the projection from MXFP8 activations
     (uint8 codes [T, K], E8M0 bytes [T, K/32], as mx_quantize or add_rms_norm
     give them), W in MXFP8 or MXFP4 as in ``wkv``."""
@@ -352,8 +341,7 @@ def wkv_mx(xq: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, w_scales: torch.
                          f"[N, {K // 32}] (MXFP4)")
     if xq.get_device() != xs.get_device():
         raise ValueError("xq and xs are on different devices")
-    return _product(L, L.engram_wkv_mx, L.engram_wkv_mx_workspace_size, (xq.data_ptr(), xs.data_ptr()),
-                    xq.get_device(), T, K, w, w_scales, fmt, N, kv, workspace)
+    return _product(L.engram_wkv_mx, (xq.data_ptr(), xs.data_ptr()), xq.get_device(), T, K, w, w_scales, fmt, N, kv)
 
 
 def add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None = None, weight: torch.Tensor | None = None,

@@ -180,9 +180,7 @@ int engram_mx_quantize(const void* x, int64_t T, int32_t K, uint8_t* xq,
  *   kv         bf16 [T, N].
  *   workspace  device scratch of at least engram_wkv_workspace_size() bytes
  *              (NULL allowed when that size is 0). For MXFP8 it holds x's
- *              MXFP8 codes and scales; for MXFP4 it is needed only for
- *              K % 256 != 0 past the GEMV's token counts: the weight
- *              expanded to bf16 (exact). 256-byte aligned.
+ *              MXFP8 codes and scales. 256-byte aligned.
  *   With MXFP4 weights x stays bf16 and W enters as its bf16 values, which
  *   are exact (a value of 2^128 or more, scale bytes 253 and 254 only, is an
  *   infinity); engram_wkv_mx takes 8-bit activations.
@@ -215,14 +213,10 @@ int engram_wkv(const void* x, int64_t T, int32_t K, const void* w,
  *   w, w_scales, w_format   ENGRAM_W_MXFP8 or ENGRAM_W_MXFP4 as engram_wkv;
  *               ENGRAM_W_BF16 returns ENGRAM_EUNSUPPORTED.
  *   kv          bf16 [T, N].
- *   workspace   engram_wkv_mx_workspace_size() bytes, 256-byte aligned (NULL
- *               allowed when that size is 0).
  *   Shapes and errors: as engram_wkv for the format.
  */
-size_t engram_wkv_mx_workspace_size(int64_t T, int32_t K, int32_t N, int32_t w_format);
 int engram_wkv_mx(const uint8_t* xq, const uint8_t* xs, int64_t T, int32_t K, const void* w,
-                  const uint8_t* w_scales, int32_t w_format, int32_t N, void* kv, void* workspace,
-                  size_t workspace_bytes, void* stream);
+                  const uint8_t* w_scales, int32_t w_format, int32_t N, void* kv, void* stream);
 
 /*
  * engram_add_rms_norm -- residual addition and root-mean-square norm of the
@@ -284,9 +278,8 @@ int engram_add_rms_norm(const void* x, int64_t x_stride_t, int64_t x_stride_h, c
  *   workspace   engram_wkv_workspace_size(T, K, (hc+1)*dim, w_format) bytes
  *   Errors: ENGRAM_EINVAL for hc or dim <= 0, a NULL or misaligned pointer,
  *   or a short workspace; T = 0 is a no-op. Asynchronous on `stream`.
- *   Shapes: as engram_wkv, plus dim % 256 == 0 and 1 <= hc <= 8 (MXFP4 at
- *   T <= 64: K % 256 == 0 as well); other shapes return
- *   ENGRAM_EUNSUPPORTED. This always runs the tiled GEMM
+ *   Shapes: as engram_wkv, plus dim % 256 == 0 and 1 <= hc <= 8; other
+ *   shapes return ENGRAM_EUNSUPPORTED. This always runs the tiled GEMM
  *   (engram_wkv may take a GEMV for T <= 64).
  */
 int engram_wkv_gate_partials(const void* x, int64_t T, int32_t K, const void* w,
@@ -405,8 +398,8 @@ typedef struct engram_forward_args {
  *   value, so the keys never reach HBM; a small finish kernel then forms the
  *   gate and the update. ENGRAM_FORWARD_STORE_KV turns this off: kv is
  *   stored whole and the plain gate kernel reads it back (the composition of
- *   engram_wkv and engram_gate). With ENGRAM_W_MXFP4 and
- *   K % 256 == 0 the epilogue is used only where T and N fill the compute
+ *   engram_wkv and engram_gate). With ENGRAM_W_MXFP4
+ *   the epilogue is used only where T and N fill the compute
  *   units with 256x256 tiles. Elsewhere the option has no effect. The two
  *   routes agree to the rounding of the gate's sums (the same bf16 keys
  *   summed in another order).

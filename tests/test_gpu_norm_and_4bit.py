@@ -369,7 +369,7 @@ def test_forward_mxfp4(T, dim, hc, C, fp8_table):
     oracle's forward (gate tolerance as the other formats' tests)."""
     E = _E()
     rng = np.random.default_rng(T + dim)
-    hd, R = 64, 501      # C 6: K 384, the weight expanded past the GEMV
+    hd, R = 64, 501      # C 6: K 384, a half chunk at the end
     K, N = C * hd, (hc + 1) * dim
     wq, ws = mxfp4_weight(rng, N, K, 122, 126)
     ids = torch.from_numpy(rng.integers(0, R, size=(T, C)).astype(np.int32)).to(DEV)
@@ -406,13 +406,14 @@ def test_forward_mxfp4(T, dim, hc, C, fp8_table):
         assert torch.equal(a, outs[0])
 
 
-def test_forward_mxfp4_gate_epilogue():
+@pytest.mark.parametrize("C", [4, 6])
+def test_forward_mxfp4_gate_epilogue(C):
     """Enough tokens that the forward's default is the GEMM's gate epilogue (6
     x 80 tiles of 256x256 on 256 compute units), and the route that stores kv:
     sampled tokens against the oracle, the two against each other."""
     E = _E()
     rng = np.random.default_rng(21)
-    T, dim, hc, C, hd, R = 1491, 4096, 4, 4, 64, 301
+    T, dim, hc, hd, R = 1491, 4096, 4, 64, 301
     K, N = C * hd, (hc + 1) * dim
     wq, ws = mxfp4_weight(rng, N, K, 122, 126)
     table = bf16(rng, R, hd, scale=0.1).to(DEV)
@@ -483,15 +484,12 @@ def test_graph_replays_and_side_stream():
         res, out = torch.empty_like(r), torch.empty_like(x)
         xq = torch.empty((T, hc, dim), dtype=torch.uint8, device=DEV)
         xs = torch.empty((T, hc, dim // 32), dtype=torch.uint8, device=DEV)
-        L = E.load_library()
-        ws = torch.empty(max(1, L.engram_wkv_mx_workspace_size(T * hc, dim, N, E.W_MXFP4)), dtype=torch.uint8, device=DEV)
-        ws2 = torch.empty(max(1, L.engram_wkv_workspace_size(T * hc, dim, N, E.W_MXFP4)), dtype=torch.uint8, device=DEV)
         kv, kv2 = (torch.empty((T * hc, N), dtype=torch.bfloat16, device=DEV) for _ in range(2))
 
         def go():
             E.add_rms_norm(x, r, wn, out_format="both", residual_out=res, out=out, xq=xq, xs=xs)
-            E.wkv_mx(xq.view(T * hc, dim), xs.view(T * hc, dim // 32), w2, s2, kv=kv, workspace=ws)
-            E.wkv(out.view(T * hc, dim), w2, s2, kv=kv2, workspace=ws2)
+            E.wkv_mx(xq.view(T * hc, dim), xs.view(T * hc, dim // 32), w2, s2, kv=kv)
+            E.wkv(out.view(T * hc, dim), w2, s2, kv=kv2)
 
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
@@ -579,11 +577,13 @@ class _FakeOther:
 
 @pytest.mark.parametrize("op", ["wkv", "wkv_mx"])
 @pytest.mark.parametrize("T,K,N", [(1500, 256, 20480), (1500, 512, 20476), (300, 768, 20480), (515, 256, 10236),
-                                   (4096, 512, 5116)])
+                                   (4096, 512, 5116), (1500, 384, 20476), (1500, 128, 20480), (300, 640, 20480),
+                                   (515, 128, 10236), (4096, 384, 5116)])
 def test_mxfp4_many_tiles(op, T, K, N):
     """Enough tiles that the GEMM's larger ones run (256x256 in the first two,
-    256x128 in the next two, 128x128 in the last, on 256 compute units), ragged
-    in T and N; a token from every tile and some more."""
+    256x128 in the next two, 128x128 in the fifth, on 256 compute units; then
+    the same with a half chunk at K's end), ragged in T and N; a token from
+    every tile and some more."""
     E = _E()
     rng = np.random.default_rng(K)
     wq, ws = mxfp4_weight(rng, N, K)
@@ -644,7 +644,8 @@ def test_mxfp4_long_k(T, K, N):
     _inside(bf16_values(bits(got)), ref, tol, "wkv_mx")
 
 
-@pytest.mark.parametrize("T,dim,hc,K", [(1, 256, 1, 512), (64, 512, 2, 256), (300, 768, 2, 512), (70, 256, 3, 384)])
+@pytest.mark.parametrize("T,dim,hc,K", [(1, 256, 1, 512), (64, 512, 2, 256), (300, 768, 2, 512), (70, 256, 3, 384),
+                                         (9, 256, 1, 128), (300, 512, 2, 640)])
 def test_mxfp4_gate_partials(T, dim, hc, K):
     """The projection fused with the gate's sums: the value block within the
     product's tolerance, the sums those of the bf16 keys of engram_wkv's tiled
