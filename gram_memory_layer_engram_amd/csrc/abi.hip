@@ -439,10 +439,13 @@ static int run_forward(const engram_forward_args* a, int32_t K, int32_t N, uint8
                      : a->w_format == ENGRAM_W_MXFP8 ? !gemv_mxfp8_supported(a->T, K)
                                                      : !gemv_mxfp4_supported(a->T, K, false);
   // MXFP4 weights: only where the plain store would take the epilogue's
-  // 256x256 tile as well; smaller tiles and a gate from kv beat it elsewhere (N
-  // 20480, K 2048: T 65 49 -> 24 us a forward, T 300 57 -> 41, T 1000 113 -> 95).
+  // 256x256 tile as well, or kv is too large to wait for the gate in the
+  // Infinity Cache; elsewhere 128x128 tiles and a gate from kv beat it (hc 4,
+  // dim 4096, epilogue / kv stored: K 2048, T 300 59 / 43 us, T 1000 118 / 100, T
+  // 4096 340 / 358; K 256, T 1000 51 / 42, T 4096 139 / 155).
   const bool epi = !(a->options & ENGRAM_FORWARD_STORE_KV) && tiled && a->dim % 256 == 0 &&
-                   (a->w_format != ENGRAM_W_MXFP4 || gemm_mxfp4_tile(a->T, N) == MxFp4Tile::k256x256);
+                   (a->w_format != ENGRAM_W_MXFP4 || !gemm_mxfp4_small_tiles(a->T, N, K, false) ||
+                    a->T * (int64_t)N * 2 > (128 << 20));
   uint16_t* value = (uint16_t*)kv;
   float2* part = (float2*)((uint8_t*)kv + round_up((size_t)a->T * a->dim * 2));
   const GateEpi ep = epi ? GateEpi{(const uint16_t*)a->hidden, (const uint16_t*)a->q_weight,

@@ -40,10 +40,9 @@
 //    publishes slice d+1 sits after the first 4 of the last 16 MFMAs of
 //    slice d, and the next slice's first fragments are read under the other
 //    12.
-//  * MXFP8 (K % 256 == 0): the same ring of five 32 KiB chunks, a slice
-//    being 128 e4m3 per row (gemm_mx_ring_kernel, described above it).
-//    Other K: a plain two-stage kernel with 128-byte k stages (piece p of
-//    row r at p ^ ((r >> 1) & 7)).
+//  * MXFP8: the same ring of five 32 KiB chunks, a slice being 128 e4m3 per
+//    row (gemm_mx_ring_kernel, described above it), or of five 16 KiB chunks
+//    for 128x128 tiles, two workgroups on a compute unit.
 //  * Epilogue: the bf16 tile is staged in LDS as [token][n] (512-byte rows,
 //    16-byte chunks XOR-swizzled by token) and written back as whole rows,
 //    16 bytes per lane: 8 full cache lines per store instruction instead of
@@ -64,40 +63,6 @@
 namespace engram {
 
 namespace {
-
-// MXFP8, two-stage kernel: 128-byte k stages
-constexpr int ROW_BYTES = 128;
-constexpr int PIECES = ROW_BYTES / 16;
-constexpr int TILE_BYTES = BM * ROW_BYTES;       // 32 KiB
-constexpr int STAGE_BYTES = 2 * TILE_BYTES;      // A + B
-static_assert(2 * STAGE_BYTES == LDS_BYTES, "LDS budget");
-
-__device__ __forceinline__ int swz(int row, int piece) {
-  return row * PIECES + (piece ^ ((row >> 1) & 7));
-}
-
-__device__ __forceinline__ i32x8 cat8(const uint4& lo, const uint4& hi) {
-  return __builtin_shufflevector(__builtin_bit_cast(i32x4, lo), __builtin_bit_cast(i32x4, hi),
-                                 0, 1, 2, 3, 4, 5, 6, 7);
-}
-
-// One MXFP8 k stage of both operand tiles, global -> LDS. Wave w issues 8
-// DMA instructions per operand; instruction i fills rows 8*(w + 4*i) .. +8.
-// `kb` is the stage's byte offset inside a row; `row_bytes` the global row
-// pitch.
-__device__ __forceinline__ void stage_load(rsrc_t ra, rsrc_t rb, char* lds_stage, int wave, int lane,
-                                           uint32_t row_bytes, uint32_t kb) {
-  const int sub = lane >> 3, pp = lane & 7;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int blk = wave + 4 * i;
-    const int r = blk * 8 + sub;
-    const int p = pp ^ ((r >> 1) & 7);
-    const uint32_t off = (uint32_t)r * row_bytes + kb + (uint32_t)p * 16u;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(lds_stage + blk * 1024), 16, off, 0, 0, 0);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr_t)(lds_stage + TILE_BYTES + blk * 1024), 16, off, 0, 0, 0);
-  }
-}
 
 // bf16 wkv GEMM (see the file comment). KTAIL: K % 64 != 0, the last slice's
 // pieces past the row end are loaded from past the range (zeros).
@@ -234,100 +199,9 @@ void gemm_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const uint16
   store_tile(acc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
 }
 
-__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(1, 1)))
-void gemm_mxfp8_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restrict__ xs, int T, int K,
-                       const uint8_t* __restrict__ w, const uint8_t* __restrict__ ws, int N,
-                       uint16_t* __restrict__ kv, int tiles_n, int tiles_t, GateEpi ep) {
-  extern __shared__ __attribute__((aligned(1024))) char smem[];
-  int tn, tt;
-  tile_of(blockIdx.x, tiles_n, tiles_t, tn, tt);
-  const int n0 = tn * BM, t0 = tt * BN;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wn = (wave >> 1) * 128, wt = (wave & 1) * 128;
-  const uint32_t row_bytes = (uint32_t)K;
-  const rsrc_t ra = make_rsrc(w + (int64_t)n0 * K, (uint32_t)min(BM, N - n0) * row_bytes);
-  const rsrc_t rb = make_rsrc(xq + (int64_t)t0 * K, (uint32_t)min(BN, T - t0) * row_bytes);
-  const int nk = K / 128;
-  const int kb = K / 32;
-  const int lrow = lane & 31, lg = lane >> 5;
-
-  // per-lane scale words (4 E8M0 bytes = one k stage) of its A and B tiles
-  const uint32_t* wsa[4];
-  const uint32_t* xsb[4];
-  bool live_t[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int nb = min((n0 + wn + i * 32) / 32, N / 32 - 1);
-    wsa[i] = reinterpret_cast<const uint32_t*>(ws + (int64_t)nb * kb);
-    const int t = t0 + wt + i * 32 + lrow;
-    live_t[i] = t < T;
-    xsb[i] = reinterpret_cast<const uint32_t*>(xs + (int64_t)(live_t[i] ? t : 0) * kb);
-  }
-  uint32_t sa[4], sb[4];
-  auto scale_load = [&](int kt) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      sa[i] = wsa[i][kt];
-      sb[i] = live_t[i] ? xsb[i][kt] : 0u;
-    }
-  };
-
-  f32x16 acc[4][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-
-  stage_load(ra, rb, smem, wave, lane, row_bytes, 0);
-  scale_load(0);
-  __syncthreads();
-
-  for (int kt = 0; kt < nk; ++kt) {
-    char* cur = smem + (kt & 1) * STAGE_BYTES;
-    uint32_t csa[4], csb[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) { csa[i] = sa[i]; csb[i] = sb[i]; }
-    if (kt + 1 < nk) {
-      stage_load(ra, rb, smem + ((kt + 1) & 1) * STAGE_BYTES, wave, lane, row_bytes,
-                 (uint32_t)(kt + 1) * 128u);
-      scale_load(kt + 1);
-    }
-    const uint4* As = reinterpret_cast<const uint4*>(cur);
-    const uint4* Bs = reinterpret_cast<const uint4*>(cur + TILE_BYTES);
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int p_lo = 4 * s + lg, p_hi = 4 * s + 2 + lg;
-      const int shift = 8 * (2 * s + lg);
-      i32x8 b[4];
-      int bsc[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int row = wt + j * 32 + lrow;
-        b[j] = cat8(Bs[swz(row, p_lo)], Bs[swz(row, p_hi)]);
-        bsc[j] = (int)((csb[j] >> shift) & 0xffu);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = wn + i * 32 + lrow;
-        const i32x8 a = cat8(As[swz(row, p_lo)], As[swz(row, p_hi)]);
-        const int asc = (int)((csa[i] >> shift) & 0xffu);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b[j], acc[i][j], 0, 0, 0, asc, 0,
-                                                                     bsc[j]);
-      }
-    }
-    __syncthreads();
-  }
-
-  store_tile(acc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
-}
-
 constexpr int S_ROW = 128;                      // MXFP8 ring: 128-byte slices (two k steps)
 
-// MXFP8 GEMM on the bf16 kernel's ring (K % 256 == 0). A slice is 128
+// MXFP8 GEMM on the bf16 kernel's ring. A slice is 128
 // e4m3 per row, two MFMA k steps ("stages", 16 MFMAs per wave each), so a
 // DMA instruction fetches 8 rows x 128 bytes, 8 whole cache lines. Each
 // operand's slice is a 32 KiB chunk in a ring of five (all 160 KiB of LDS),
@@ -344,23 +218,28 @@ constexpr int S_ROW = 128;                      // MXFP8 ring: 128-byte slices (
 // 4h+2+g of its row and passes the E8M0 byte of k block 2*stage + g. The
 // fragments stream one A row block ahead (two register sets); B and the
 // next stage's first A block are read under a stage's last four MFMAs.
-__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(1, 1)))
+// Slices go in pairs; HALF (K % 256 == 128): one more behind the loop, whose
+// group of scale bytes is half the row's, half the next row's or zeros, unused.
+// NT 4: the 256x256 tile; 2: 128x128, two workgroups on a compute unit.
+template <int NT, bool HALF>
+__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(NT == 4 ? 1 : 2, NT == 4 ? 1 : 2)))
 void gemm_mx_ring_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restrict__ xs, int T, int K,
                          const uint8_t* __restrict__ w, const uint8_t* __restrict__ ws, int N,
                          uint16_t* __restrict__ kv, int tiles_n, int tiles_t, GateEpi ep) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   int tn, tt;
   tile_of(blockIdx.x, tiles_n, tiles_t, tn, tt);
-  const int n0 = tn * BM, t0 = tt * BN;
+  constexpr int TILE = 64 * NT, CH = S_ROW * TILE, NDMA = 2 * NT;   // a chunk in LDS, a wave's DMAs for it
+  const int n0 = tn * TILE, t0 = tt * TILE;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wn = (wave >> 1) * 128, wt = (wave & 1) * 128;
+  const int wn = (wave >> 1) * (32 * NT), wt = (wave & 1) * (32 * NT);
   const uint32_t row_bytes = (uint32_t)K;
-  const rsrc_t ra = make_rsrc(w + (int64_t)n0 * K, (uint32_t)min(BM, N - n0) * row_bytes);
-  const rsrc_t rb = make_rsrc(xq + (int64_t)t0 * K, (uint32_t)min(BN, T - t0) * row_bytes);
-  const uint32_t oob = (uint32_t)BM * row_bytes;   // at or past both ranges
-  const int ns = K / 128;                           // slices, even
-  const int kb = K / 32;                            // scale bytes per row, a multiple of 8
+  const rsrc_t ra = make_rsrc(w + (int64_t)n0 * K, (uint32_t)min(TILE, N - n0) * row_bytes);
+  const rsrc_t rb = make_rsrc(xq + (int64_t)t0 * K, (uint32_t)min(TILE, T - t0) * row_bytes);
+  const uint32_t oob = (uint32_t)TILE * row_bytes;   // at or past both ranges
+  const int ns = K / 128;                           // slices, odd where HALF
+  const int kb = K / 32;                            // scale bytes per row
   const int lrow = lane & 31, lg = lane >> 5;
 
   const dma::Lane dl = dma::lane_of(wave, lane, row_bytes);
@@ -373,16 +252,16 @@ void gemm_mx_ring_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restri
   // range-checked vector loads: a scalar load would be waited for by the
   // next fragment read's lgkmcnt(0). Token rows past T read zeros.
   const rsrc_t rsa = make_rsrc(ws, (uint32_t)(N / 32) * (uint32_t)kb);
-  const rsrc_t rsb = make_rsrc(xs + (int64_t)t0 * kb, (uint32_t)min(BN, T - t0) * (uint32_t)kb);
-  uint32_t arow[4], brow[4];
+  const rsrc_t rsb = make_rsrc(xs + (int64_t)t0 * kb, (uint32_t)min(TILE, T - t0) * (uint32_t)kb);
+  uint32_t arow[NT], brow[NT];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < NT; ++i) {
     arow[i] = (uint32_t)min((n0 + wn + i * 32) / 32, N / 32 - 1) * (uint32_t)kb;
     brow[i] = (uint32_t)(wt + i * 32 + lrow) * (uint32_t)kb;
   }
-  auto scales8 = [&](int s4, u32x2 (&a8)[4], u32x2 (&b8)[4]) {
+  auto scales8 = [&](int s4, u32x2 (&a8)[NT], u32x2 (&b8)[NT]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < NT; ++i) {
       a8[i] = __builtin_amdgcn_raw_buffer_load_b64(rsa, arow[i] + 2u * (uint32_t)s4, 0, 0);
       b8[i] = __builtin_amdgcn_raw_buffer_load_b64(rsb, brow[i] + 2u * (uint32_t)s4, 0, 0);
     }
@@ -399,98 +278,100 @@ void gemm_mx_ring_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restri
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
 
-  f32x16 acc[4][4];
+  f32x16 acc[NT][NT];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-  i32x8 a0, a1, b[4], nb[4];
-  int sa[4], sb[4];
+  i32x8 a0, a1, b[NT], nb[NT];
+  int sa[NT], sb[NT];
   auto mfma_row = [&](const i32x8& a, int i) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < NT; ++j)
       acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b[j], acc[i][j], 0, 0, 0, sa[i], 0,
                                                                  sb[j]);
   };
 
   // prologue: the first group's scale bytes, then A_0 -> slot 0, B_0 -> slot
-  // 1, A_1 -> slot 2; wait for all but A_1's 8 DMAs
-  u32x2 sa8[4], sb8[4], na8[4], nb8[4];
+  // 1, A_1 -> slot 2; wait for all but A_1's DMAs
+  u32x2 sa8[NT], sb8[NT], na8[NT], nb8[NT];
   scales8(0, sa8, sb8);
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int i = 0; i < Q_DMA; ++i) dma(0, 0, 0u, i);
+  for (int i = 0; i < NDMA; ++i) dma(0, 0, 0u, i);
 #pragma unroll
-  for (int i = 0; i < Q_DMA; ++i) dma(Q_CHUNK, 1, 0u, i);
+  for (int i = 0; i < NDMA; ++i) dma(CH, 1, 0u, i);
 #pragma unroll
-  for (int i = 0; i < Q_DMA; ++i) dma(2 * Q_CHUNK, 0, ns > 1 ? (uint32_t)S_ROW : oob, i);
-  wait_vm<Q_DMA>();
+  for (int i = 0; i < NDMA; ++i) dma(2 * CH, 0, ns > 1 ? (uint32_t)S_ROW : oob, i);
+  wait_vm<NDMA>();
   // a use here keeps the first group's scale loads ahead of the DMAs (left
   // to itself, the compiler sinks them to the loop, and the waits it then
   // places at the loop head drain every slice's DMAs)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(sa8[i]), "+v"(sb8[i]));
+  for (int i = 0; i < NT; ++i) asm volatile("" : "+v"(sa8[i]), "+v"(sb8[i]));
   bare_barrier();
 #pragma unroll
-  for (int j = 0; j < 4; ++j) b[j] = frag(Q_CHUNK, 0, wt + j * 32 + lrow);
+  for (int j = 0; j < NT; ++j) b[j] = frag(CH, 0, wt + j * 32 + lrow);
   a0 = frag(0, 0, wn + lrow);
 
   int base = 0;   // (2d) % 5
   // one slice; PAR = d % 2 (the slice's place in its group of two)
   auto slice = [&](int d, auto par) {
     constexpr int PAR = decltype(par)::value;
-    auto slot = [&](int m) { const int v = base + m; return (v >= Q_SLOTS ? v - Q_SLOTS : v) * Q_CHUNK; };
+    auto slot = [&](int m) { const int v = base + m; return (v >= Q_SLOTS ? v - Q_SLOTS : v) * CH; };
     const int s_a = slot(0), s_b = slot(1), s_a1 = slot(2), s_b1 = slot(3), s_a2 = slot(4);
     const uint32_t kb1 = d + 1 < ns ? (uint32_t)(d + 1) * S_ROW : oob;
     const uint32_t ka2 = d + 2 < ns ? (uint32_t)(d + 2) * S_ROW : oob;
-    if (PAR == 0) scales8(min(2 * d + 4, 2 * ns - 4), na8, nb8);   // the last group reloads itself, unused
+    if (PAR == 0) scales8(min(2 * d + 4, 2 * ns - (HALF ? 2 : 4)), na8, nb8);   // the last group reloads itself, unused
     // stage 0: B_{d+1}, two DMAs per quarter
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < NT; ++i) {
       sa[i] = pick(sa8[i], 2 * PAR);
       sb[i] = pick(sb8[i], 2 * PAR);
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < NT; ++q) {
       __builtin_amdgcn_sched_barrier(0);
       dma(s_b1, 1, kb1, 2 * q);
       dma(s_b1, 1, kb1, 2 * q + 1);
-      if (q < 3) {
+      if (q < NT - 1) {
         if (q & 1) a0 = frag(s_a, 0, wn + (q + 1) * 32 + lrow);
         else a1 = frag(s_a, 0, wn + (q + 1) * 32 + lrow);
         mfma_row((q & 1) ? a1 : a0, q);
         SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_DSR, 1); SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_DSR, 1);
-        SGB(SG_MFMA, 2);
+        if (NT == 4) SGB(SG_MFMA, 2);
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) nb[j] = frag(s_b, 1, wt + j * 32 + lrow);
+        for (int j = 0; j < NT; ++j) nb[j] = frag(s_b, 1, wt + j * 32 + lrow);
         a0 = frag(s_a, 1, wn + lrow);
-        mfma_row(a1, 3);
-        SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_DSR, 4); SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_DSR, 3);
-        SGB(SG_MFMA, 1); SGB(SG_DSR, 3); SGB(SG_MFMA, 1);
+        mfma_row(a1, NT - 1);
+        SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_DSR, 4); SGB(SG_MFMA, 1); SGB(SG_VMEM, 1);
+        if (NT == 4) { SGB(SG_DSR, 3); SGB(SG_MFMA, 1); SGB(SG_DSR, 3); SGB(SG_MFMA, 1); }
       }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) b[j] = nb[j];
+    for (int j = 0; j < NT; ++j) b[j] = nb[j];
     // stage 1: A_{d+2}, 3 + 3 + 2 DMAs; the barrier after the third row block
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < NT; ++i) {
       sa[i] = pick(sa8[i], 2 * PAR + 1);
       sb[i] = pick(sb8[i], 2 * PAR + 1);
     }
 #pragma unroll
-    for (int q = 0; q < 3; ++q) {
+    for (int q = 0; q < NT - 1; ++q) {
       __builtin_amdgcn_sched_barrier(0);
-      const int nd = q < 2 ? 3 : 2, d0 = 3 * q;
+      const int nd = NT == 2 ? 4 : q < 2 ? 3 : 2, d0 = 3 * q;
 #pragma unroll
       for (int k = 0; k < nd; ++k) dma(s_a2, 0, ka2, d0 + k);
       if (q & 1) a0 = frag(s_a, 1, wn + (q + 1) * 32 + lrow);
       else a1 = frag(s_a, 1, wn + (q + 1) * 32 + lrow);
       mfma_row((q & 1) ? a1 : a0, q);
-      if (nd == 3) {
+      if (nd == 4) {
+        SGB(SG_MFMA, 1); SGB(SG_VMEM, 2); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_VMEM, 2);
+      } else if (nd == 3) {
         SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_DSR, 1); SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_DSR, 1);
         SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_MFMA, 1);
       } else {
@@ -499,34 +380,48 @@ void gemm_mx_ring_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restri
       }
     }
     __builtin_amdgcn_sched_barrier(0);
-    wait_vm<Q_DMA>();   // all but A_{d+2}'s 8: B_{d+1}, A_{d+1} and the scale loads are in
+    wait_vm<NDMA>();   // all but A_{d+2}'s: B_{d+1}, A_{d+1} and the scale loads are in
     wait_lgkm0();
     bare_barrier();
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) nb[j] = frag(s_b1, 0, wt + j * 32 + lrow);
+    for (int j = 0; j < NT; ++j) nb[j] = frag(s_b1, 0, wt + j * 32 + lrow);
     a0 = frag(s_a1, 0, wn + lrow);
-    mfma_row(a1, 3);
-    SGB(SG_MFMA, 1); SGB(SG_DSR, 4); SGB(SG_MFMA, 1); SGB(SG_DSR, 3); SGB(SG_MFMA, 1); SGB(SG_DSR, 3);
-    SGB(SG_MFMA, 1);
+    mfma_row(a1, NT - 1);
+    SGB(SG_MFMA, 1); SGB(SG_DSR, 4); SGB(SG_MFMA, 1);
+    if (NT == 4) { SGB(SG_DSR, 3); SGB(SG_MFMA, 1); SGB(SG_DSR, 3); SGB(SG_MFMA, 1); }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) b[j] = nb[j];
+    for (int j = 0; j < NT; ++j) b[j] = nb[j];
     if (PAR == 1) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < NT; ++i) {
         sa8[i] = na8[i];
         sb8[i] = nb8[i];
       }
     }
     base = base + 2 >= Q_SLOTS ? base + 2 - Q_SLOTS : base + 2;
   };
-  for (int d = 0; d < ns; d += 2) {
+  for (int d = 0; d < (HALF ? ns - 1 : ns); d += 2) {
     slice(d, std::integral_constant<int, 0>{});
     slice(d + 1, std::integral_constant<int, 1>{});
   }
+  if constexpr (HALF) slice(ns - 1, std::integral_constant<int, 0>{});
   __builtin_amdgcn_sched_barrier(0);
   wait_vm<0>();   // the zero-fill DMAs of the last slices land before LDS is reused
-  store_tile(acc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
+  store_tile<NT>(acc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
+}
+
+template <int NT, bool HALF>
+hipError_t launch_mx_ring(const uint8_t* xq, const uint8_t* xs, int T, int K, const uint8_t* w, const uint8_t* ws,
+                          int N, uint16_t* kv, hipStream_t s, const GateEpi& ep) {
+  const int tiles_n = (N + 64 * NT - 1) / (64 * NT), tiles_t = (T + 64 * NT - 1) / (64 * NT);
+  constexpr int lds = Q_LDS * NT / 4;
+  const auto fn = gemm_mx_ring_kernel<NT, HALF>;
+  const hipError_t e = set_lds((const void*)fn, lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(fn, dim3(tiles_n * tiles_t), dim3(THREADS), lds, s, xq, xs, T, K, w, ws, N, kv, tiles_n,
+                     tiles_t, ep);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -549,22 +444,20 @@ hipError_t launch_gemm_bf16(const void* x, int64_t T, int K, const void* w, int 
   return hipGetLastError();
 }
 
+// Measured in us, 256x256 / 128x128 tiles: N 20480, K 2048: T 128 25.6 / 13.8, T
+// 300 27 / 19, T 515 29.5 / 35.6, T 1000 57 / 48, T 8192 310 / 369; T 383, N 7808,
+// K 384 12.0 / 5.2; T 6968, N 10112, K 640 76 / 68.
+// The gate's epilogue has the 256x256 tile only. kv is the same bit for bit
+// whatever the tile.
 hipError_t launch_gemm_mxfp8(const uint8_t* xq, const uint8_t* xs, int64_t T, int K, const uint8_t* w,
                              const uint8_t* ws, int N, void* kv, hipStream_t s, const GateEpi& ep) {
-  const int tiles_n = (N + BM - 1) / BM;
-  const int tiles_t = (int)((T + BN - 1) / BN);
-  if (K % 256 == 0 && N % 32 == 0) {
-    hipError_t e = set_lds((const void*)gemm_mx_ring_kernel, Q_LDS);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(gemm_mx_ring_kernel, dim3(tiles_n * tiles_t), dim3(THREADS), Q_LDS, s, xq, xs, (int)T,
-                       K, w, ws, N, (uint16_t*)kv, tiles_n, tiles_t, ep);
-    return hipGetLastError();
-  }
-  hipError_t e = set_lds((const void*)gemm_mxfp8_kernel, LDS_BYTES);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(gemm_mxfp8_kernel, dim3(tiles_n * tiles_t), dim3(THREADS), LDS_BYTES, s, xq, xs,
-                     (int)T, K, w, ws, N, (uint16_t*)kv, tiles_n, tiles_t, ep);
-  return hipGetLastError();
+  uint16_t* out = (uint16_t*)kv;
+  const bool small = !ep.hidden && small_tiles(T, N, K, {8000, 1400, 3200, 950, 3200, 660});
+  if (K % 256)
+    return small ? launch_mx_ring<2, true>(xq, xs, (int)T, K, w, ws, N, out, s, ep)
+                 : launch_mx_ring<4, true>(xq, xs, (int)T, K, w, ws, N, out, s, ep);
+  return small ? launch_mx_ring<2, false>(xq, xs, (int)T, K, w, ws, N, out, s, ep)
+               : launch_mx_ring<4, false>(xq, xs, (int)T, K, w, ws, N, out, s, ep);
 }
 
 }  // namespace engram

@@ -35,38 +35,33 @@ namespace engram {
 namespace {
 
 constexpr int kWSlots = 2, kXSlots = 3;
-// A block is 64 * NI W rows x 64 * NJ tokens: 256 x 256, 256 x 128, or 128 x
-// 128 with two workgroups on a compute unit (launch_gemm_mxfp4).
-constexpr int op_slot(int n) { return 64 * n * Q_ROW; }       // an operand's chunk or slice in LDS
-constexpr int op_dma(int n) { return 2 * n; }                 // a wave's DMAs for it
-constexpr int fp4_lds(int ni, int nj) {
-  const int ring = kWSlots * op_slot(ni) + kXSlots * op_slot(nj), epi = 64 * nj * 128 * ni;
-  return ring > epi ? ring : epi;
-}
-static_assert(fp4_lds(4, 4) == Q_LDS && 2 * fp4_lds(2, 2) <= Q_LDS, "LDS budget");
+// A block is 64 * NT W rows x 64 * NT tokens: 256 x 256, or 128 x 128 with two
+// workgroups on a compute unit (launch_gemm_mxfp4).
+constexpr int fp4_lds(int nt) { return (kWSlots + kXSlots) * 64 * nt * Q_ROW; }
+static_assert(fp4_lds(4) == Q_LDS && 2 * fp4_lds(2) <= Q_LDS, "LDS budget");
 constexpr int SG_VALU = 0x002;
 
 template <int V> using Int = std::integral_constant<int, V>;
 
-template <int NI, int NJ, bool HALF>
-__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(NI == 4 ? 1 : 2, NI == 4 ? 1 : 2)))
+template <int NT, bool HALF>
+__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(NT == 4 ? 1 : 2, NT == 4 ? 1 : 2)))
 void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const uint8_t* __restrict__ w,
                           const uint8_t* __restrict__ ws, int N, uint16_t* __restrict__ kv, int tiles_n,
                           int tiles_t, GateEpi ep) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   int tn, tt;
   tile_of(blockIdx.x, tiles_n, tiles_t, tn, tt);
-  constexpr int TM = 64 * NI, TN = 64 * NJ, WCH = op_slot(NI), XCH = op_slot(NJ), WD = op_dma(NI), XD = op_dma(NJ);
-  constexpr int XBASE = kWSlots * WCH;
-  const int n0 = tn * TM, t0 = tt * TN;
+  constexpr int TILE = 64 * NT, CH = TILE * Q_ROW, NDMA = 2 * NT;   // a chunk or slice in LDS, a wave's DMAs for it
+  constexpr int XBASE = kWSlots * CH;
+  const int n0 = tn * TILE, t0 = tt * TILE;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wn = (wave >> 1) * (32 * NI), wt = (wave & 1) * (32 * NJ);
+  const int wn = (wave >> 1) * (32 * NT), wt = (wave & 1) * (32 * NT);
   const uint32_t wpitch = (uint32_t)K / 2u, xpitch = (uint32_t)K * 2u, kb = (uint32_t)K / 32u;
-  const rsrc_t ra = make_rsrc(w + (int64_t)n0 * wpitch, (uint32_t)min(TM, N - n0) * wpitch);
-  const rsrc_t rb = make_rsrc(x + (int64_t)t0 * K, (uint32_t)min(TN, T - t0) * xpitch);
-  const rsrc_t rs = make_rsrc(ws + (int64_t)n0 * kb, (uint32_t)min(TM, N - n0) * kb);
-  const uint32_t ooba = (uint32_t)TM * wpitch, oobb = (uint32_t)TN * xpitch;   // at or past the ranges
+  const rsrc_t ra = make_rsrc(w + (int64_t)n0 * wpitch, (uint32_t)min(TILE, N - n0) * wpitch);
+  const rsrc_t rb = make_rsrc(x + (int64_t)t0 * K, (uint32_t)min(TILE, T - t0) * xpitch);
+  const rsrc_t rs = make_rsrc(ws + (int64_t)n0 * kb, (uint32_t)min(TILE, N - n0) * kb);
+  const uint32_t ooba = (uint32_t)TILE * wpitch, oobb = (uint32_t)TILE * xpitch;   // at or past the ranges
   const int nk = K / 64, nc = K / 256 + HALF;   // x slices (even), W chunks
 
   const dma::Lane la = dma::lane_of(wave, lane, wpitch), lb = dma::lane_of(wave, lane, xpitch);
@@ -83,12 +78,12 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
   const int fsw = (lrow >> 1) & 7;
   // the 8 scale bytes of a chunk (256 k) of this lane's four rows; byte
   // 2*PAR + h is slice PAR's
-  uint32_t srow[NI];
+  uint32_t srow[NT];
 #pragma unroll
-  for (int i = 0; i < NI; ++i) srow[i] = (uint32_t)(wn + i * 32 + lrow) * kb;
-  auto scales8 = [&](int c, u32x2 (&s8)[NI]) {
+  for (int i = 0; i < NT; ++i) srow[i] = (uint32_t)(wn + i * 32 + lrow) * kb;
+  auto scales8 = [&](int c, u32x2 (&s8)[NT]) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i) s8[i] = __builtin_amdgcn_raw_buffer_load_b64(rs, srow[i] + 8u * (uint32_t)c, 0, 0);
+    for (int i = 0; i < NT; ++i) s8[i] = __builtin_amdgcn_raw_buffer_load_b64(rs, srow[i] + 8u * (uint32_t)c, 0, 0);
   };
   // byte 2*par + h in the exponent field of an fp32 (the conversion reads no
   // other bits of its scale)
@@ -97,17 +92,17 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
     return __uint_as_float(((par < 2 ? v.x : v.y) >> ((uint32_t)(16 * (par & 1)) + lsh)) << 23);
   };
 
-  f32x16 acc[NI][NJ];
+  f32x16 acc[NT][NT];
 #pragma unroll
-  for (int i = 0; i < NI; ++i)
+  for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-  bf16x8_t a[2][NI], b[2][NJ];
-  i32x4 raw[NI];
-  float sc[NI];
+  bf16x8_t a[2][NT], b[2][NT];
+  i32x4 raw[NT];
+  float sc[NT];
   auto read_raw = [&](int slot, int par, int i) {
     raw[i] = *reinterpret_cast<const i32x4*>(smem + slot + (wn + i * 32 + lrow) * Q_ROW +
                                              (((2 * par + lhalf) ^ fsw) << 4));
@@ -124,35 +119,35 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
   };
   auto mfma_row = [&](int c, int i) {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
+    for (int j = 0; j < NT; ++j)
       acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[c][i], b[c][j], acc[i][j], 0, 0, 0);
   };
-  auto wslot = [](int c) { return (c & 1) * WCH; };
+  auto wslot = [](int c) { return (c & 1) * CH; };
 
   // prologue: W chunk 0, x slices 0 and 1; all but x slice 1's DMAs waited for
-  u32x2 s8[NI], n8[NI];
+  u32x2 s8[NT], n8[NT];
   scales8(0, s8);
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int i = 0; i < WD; ++i) dma_w(0, 0u, i);
+  for (int i = 0; i < NDMA; ++i) dma_w(0, 0u, i);
 #pragma unroll
-  for (int i = 0; i < XD; ++i) dma_x(XBASE, 0u, i);
+  for (int i = 0; i < NDMA; ++i) dma_x(XBASE, 0u, i);
 #pragma unroll
-  for (int i = 0; i < XD; ++i) dma_x(XBASE + XCH, (uint32_t)Q_ROW, i);
-  wait_vm<XD>();
+  for (int i = 0; i < NDMA; ++i) dma_x(XBASE + CH, (uint32_t)Q_ROW, i);
+  wait_vm<NDMA>();
   // a use here keeps the scale loads ahead of the DMAs
 #pragma unroll
-  for (int i = 0; i < NI; ++i) asm volatile("" : "+v"(s8[i]));
+  for (int i = 0; i < NT; ++i) asm volatile("" : "+v"(s8[i]));
   bare_barrier();
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
+  for (int i = 0; i < NT; ++i) {
     read_raw(0, 0, i);
     sc[i] = pick(s8[i], 0);
   }
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) read_x(XBASE, 0, 0, j);
+  for (int j = 0; j < NT; ++j) read_x(XBASE, 0, 0, j);
 #pragma unroll
-  for (int i = 0; i < NI; ++i) convert(0, 0, i);
+  for (int i = 0; i < NT; ++i) convert(0, 0, i);
 
   int xb = 0;   // d % 3
   // slice d (64 k), par = d % 4: x of slice d+2 and, in the chunk's first
@@ -161,7 +156,7 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
   auto slice = [&](int d, auto par) {
     constexpr int PAR = decltype(par)::value;
     const int c = d >> 2;
-    auto xslot = [&](int m) { const int v = xb + m; return XBASE + (v >= 3 ? v - 3 : v) * XCH; };
+    auto xslot = [&](int m) { const int v = xb + m; return XBASE + (v >= 3 ? v - 3 : v) * CH; };
     const int sb = xslot(0), sb1 = xslot(1), sb2 = xslot(2);
     const uint32_t kx = d + 2 < nk ? (uint32_t)(d + 2) * Q_ROW : oobb;
     const uint32_t kw = c + 1 < nc ? (uint32_t)(c + 1) * Q_ROW : ooba;
@@ -170,70 +165,70 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
 #pragma unroll
     for (int kk = 0; kk < 3; ++kk) {
 #pragma unroll
-      for (int q = 0; q < NI; ++q) {
+      for (int q = 0; q < NT; ++q) {
         __builtin_amdgcn_sched_barrier(0);
         // W: 3 + 3 + 2 (2 + 1 + 1) DMAs over a chunk's first three slices
-        constexpr int w0 = NI == 4 ? 3 * PAR : PAR + (PAR > 0), wd = NI == 4 ? (PAR == 2 ? 2 : 3) : (PAR ? 1 : 2);
+        constexpr int w0 = NT == 4 ? 3 * PAR : PAR + (PAR > 0), wd = NT == 4 ? (PAR == 2 ? 2 : 3) : (PAR ? 1 : 2);
         const bool dw = PAR < 3 && kk == 0 && q < wd;
         if (dw) dma_w(wslot(c + 1), kw, w0 + q);
-        const int x0 = kk * NI + q - (NI == 4);   // x: one each from (kk 0, q 1 or 0) on
-        const bool dx = x0 >= 0 && x0 < XD;
+        const int x0 = kk * NT + q - (NT == 4);   // x: one each from (kk 0, q 1 or 0) on
+        const bool dx = x0 >= 0 && x0 < NDMA;
         if (dx) dma_x(sb2, kx, x0);
-        if (q < NJ) read_x(sb, kk + 1, (kk + 1) & 1, q);
+        if (q < NT) read_x(sb, kk + 1, (kk + 1) & 1, q);
         convert(kk + 1, (kk + 1) & 1, q);
         mfma_row(kk & 1, q);
         SGB(SG_MFMA, 1);
         if (dw) SGB(SG_VMEM, 1);
         if (dx) SGB(SG_VMEM, 1);
-        if (NJ == 4) { SGB(SG_MFMA, 1); SGB(SG_DSR, 1); SGB(SG_MFMA, 1); SGB(SG_VALU, 4); SGB(SG_MFMA, 1); }
-        else { if (q < NJ) SGB(SG_DSR, 1); SGB(SG_VALU, 4); SGB(SG_MFMA, 1); }
+        if (NT == 4) { SGB(SG_MFMA, 1); SGB(SG_DSR, 1); SGB(SG_MFMA, 1); SGB(SG_VALU, 4); SGB(SG_MFMA, 1); }
+        else { if (q < NT) SGB(SG_DSR, 1); SGB(SG_VALU, 4); SGB(SG_MFMA, 1); }
       }
     }
     __builtin_amdgcn_sched_barrier(0);
     mfma_row(1, 0);
     __builtin_amdgcn_sched_barrier(0);
-    wait_vm<XD>();   // only x of slice d+2 may still fly
+    wait_vm<NDMA>();   // only x of slice d+2 may still fly
     wait_lgkm0();
     bare_barrier();
     // the rest of sub-step 3: slice d+1's W words, first x fragments, conversions
     const int sw1 = wslot(PAR == 3 ? c + 1 : c);
     auto next_w = [&]() {
 #pragma unroll
-      for (int i = 0; i < NI; ++i) read_raw(sw1, (PAR + 1) & 3, i);
+      for (int i = 0; i < NT; ++i) read_raw(sw1, (PAR + 1) & 3, i);
     };
     auto next_x = [&]() {
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) read_x(sb1, 0, 0, j);
+      for (int j = 0; j < NT; ++j) read_x(sb1, 0, 0, j);
 #pragma unroll
-      for (int i = 0; i < NI; ++i) sc[i] = PAR == 3 ? pick(n8[i], 0) : pick(s8[i], (PAR + 1) & 3);
+      for (int i = 0; i < NT; ++i) sc[i] = PAR == 3 ? pick(n8[i], 0) : pick(s8[i], (PAR + 1) & 3);
     };
     __builtin_amdgcn_sched_barrier(0);
     next_w();
-    if constexpr (NI == 4) {
+    if constexpr (NT == 4) {
       mfma_row(1, 1);
-      if (NJ == 4) { SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 2); }
+      if (NT == 4) { SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 2); }
       else { SGB(SG_MFMA, 1); SGB(SG_DSR, 4); SGB(SG_MFMA, 1); }
       __builtin_amdgcn_sched_barrier(0);
       next_x();
       mfma_row(1, 2);
-      if (NJ == 4) { SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 2); }
+      if (NT == 4) { SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 2); }
       else { SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); }
       __builtin_amdgcn_sched_barrier(0);
     } else {
       next_x();
     }
 #pragma unroll
-    for (int i = 0; i < NI; ++i) convert(0, 0, i);
-    mfma_row(1, NI - 1);
-    if (NJ == 4) {
+    for (int i = 0; i < NT; ++i) convert(0, 0, i);
+    mfma_row(1, NT - 1);
+    if (NT == 4) {
       SGB(SG_MFMA, 1); SGB(SG_VALU, 5); SGB(SG_MFMA, 1); SGB(SG_VALU, 5); SGB(SG_MFMA, 1); SGB(SG_VALU, 5);
       SGB(SG_MFMA, 1);
-    } else if (NI == 4) {
+    } else if (NT == 4) {
       SGB(SG_MFMA, 1); SGB(SG_VALU, 8); SGB(SG_MFMA, 1);
     }
     if (PAR == 3) {
 #pragma unroll
-      for (int i = 0; i < NI; ++i) s8[i] = n8[i];
+      for (int i = 0; i < NT; ++i) s8[i] = n8[i];
     }
     xb = xb + 1 >= 3 ? 0 : xb + 1;
   };
@@ -249,29 +244,29 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
   }
   __builtin_amdgcn_sched_barrier(0);
   wait_vm<0>();   // the zero-fill DMAs of the last slices land before LDS is reused
-  store_tile<NI, NJ>(acc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
+  store_tile<NT>(acc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
 }
 
-template <int NI, int NJ, bool HALF>
-__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(NI == 4 ? 1 : 2, NI == 4 ? 1 : 2)))
+template <int NT, bool HALF>
+__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(NT == 4 ? 1 : 2, NT == 4 ? 1 : 2)))
 void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restrict__ xs, int T, int K,
                         const uint8_t* __restrict__ w, const uint8_t* __restrict__ ws, int N,
                         uint16_t* __restrict__ kv, int tiles_n, int tiles_t, GateEpi ep) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   int tn, tt;
   tile_of(blockIdx.x, tiles_n, tiles_t, tn, tt);
-  constexpr int TM = 64 * NI, TN = 64 * NJ, WCH = op_slot(NI), XCH = op_slot(NJ), WD = op_dma(NI), XD = op_dma(NJ);
-  constexpr int XBASE = kWSlots * WCH;
-  const int n0 = tn * TM, t0 = tt * TN;
+  constexpr int TILE = 64 * NT, CH = TILE * Q_ROW, NDMA = 2 * NT;   // a chunk or slice in LDS, a wave's DMAs for it
+  constexpr int XBASE = kWSlots * CH;
+  const int n0 = tn * TILE, t0 = tt * TILE;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wn = (wave >> 1) * (32 * NI), wt = (wave & 1) * (32 * NJ);
+  const int wn = (wave >> 1) * (32 * NT), wt = (wave & 1) * (32 * NT);
   const uint32_t wpitch = (uint32_t)K / 2u, xpitch = (uint32_t)K, kb = (uint32_t)K / 32u;
-  const rsrc_t ra = make_rsrc(w + (int64_t)n0 * wpitch, (uint32_t)min(TM, N - n0) * wpitch);
-  const rsrc_t rb = make_rsrc(xq + (int64_t)t0 * xpitch, (uint32_t)min(TN, T - t0) * xpitch);
-  const rsrc_t rsa = make_rsrc(ws + (int64_t)n0 * kb, (uint32_t)min(TM, N - n0) * kb);
-  const rsrc_t rsb = make_rsrc(xs + (int64_t)t0 * kb, (uint32_t)min(TN, T - t0) * kb);
-  const uint32_t ooba = (uint32_t)TM * wpitch, oobb = (uint32_t)TN * xpitch;
+  const rsrc_t ra = make_rsrc(w + (int64_t)n0 * wpitch, (uint32_t)min(TILE, N - n0) * wpitch);
+  const rsrc_t rb = make_rsrc(xq + (int64_t)t0 * xpitch, (uint32_t)min(TILE, T - t0) * xpitch);
+  const rsrc_t rsa = make_rsrc(ws + (int64_t)n0 * kb, (uint32_t)min(TILE, N - n0) * kb);
+  const rsrc_t rsb = make_rsrc(xs + (int64_t)t0 * kb, (uint32_t)min(TILE, T - t0) * kb);
+  const uint32_t ooba = (uint32_t)TILE * wpitch, oobb = (uint32_t)TILE * xpitch;
   const int ns = K / 128, nc = K / 256 + HALF;   // x slices, W chunks
 
   const dma::Lane la = dma::lane_of(wave, lane, wpitch), lb = dma::lane_of(wave, lane, xpitch);
@@ -288,16 +283,16 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
   const int fsw = (lrow >> 1) & 7;
   // the 8 scale bytes of a chunk (four stages of 64 k) of this lane's W and
   // token rows; lane group g takes byte 2*stage + g
-  uint32_t arow[NI], brow[NJ];
+  uint32_t arow[NT], brow[NT];
 #pragma unroll
-  for (int i = 0; i < NI; ++i) arow[i] = (uint32_t)(wn + i * 32 + lrow) * kb;
+  for (int i = 0; i < NT; ++i) arow[i] = (uint32_t)(wn + i * 32 + lrow) * kb;
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) brow[j] = (uint32_t)(wt + j * 32 + lrow) * kb;
-  auto scales8 = [&](int c, u32x2 (&a8)[NI], u32x2 (&b8)[NJ]) {
+  for (int j = 0; j < NT; ++j) brow[j] = (uint32_t)(wt + j * 32 + lrow) * kb;
+  auto scales8 = [&](int c, u32x2 (&a8)[NT], u32x2 (&b8)[NT]) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
+    for (int i = 0; i < NT; ++i) {
       a8[i] = __builtin_amdgcn_raw_buffer_load_b64(rsa, arow[i] + 8u * (uint32_t)c, 0, 0);
-      if (i < NJ) b8[i] = __builtin_amdgcn_raw_buffer_load_b64(rsb, brow[i] + 8u * (uint32_t)c, 0, 0);
+      if (i < NT) b8[i] = __builtin_amdgcn_raw_buffer_load_b64(rsb, brow[i] + 8u * (uint32_t)c, 0, 0);
     }
   };
   const uint32_t lsh = (uint32_t)lg * 8u;
@@ -315,45 +310,45 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
 
-  f32x16 acc[NI][NJ];
+  f32x16 acc[NT][NT];
 #pragma unroll
-  for (int i = 0; i < NI; ++i)
+  for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-  i32x4 a[NI], na[NI];
-  i32x8 b[NJ], nb[NJ];
-  int sa[NI], sb[NJ];
+  i32x4 a[NT], na[NT];
+  i32x8 b[NT], nb[NT];
+  int sa[NT], sb[NT];
   auto mfma_row = [&](int i) {
     const i32x8 wa = __builtin_shufflevector(a[i], a[i], 0, 1, 2, 3, 0, 1, 2, 3);   // fp4: the first four words
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
+    for (int j = 0; j < NT; ++j)
       acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wa, b[j], acc[i][j], 4, 0, 0, sa[i], 0, sb[j]);
   };
-  auto wslot = [](int c) { return (c & 1) * WCH; };
+  auto wslot = [](int c) { return (c & 1) * CH; };
 
-  u32x2 sa8[NI], sb8[NJ], na8[NI], nb8[NJ];
+  u32x2 sa8[NT], sb8[NT], na8[NT], nb8[NT];
   scales8(0, sa8, sb8);
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int i = 0; i < WD; ++i) dma_w(0, 0u, i);
+  for (int i = 0; i < NDMA; ++i) dma_w(0, 0u, i);
 #pragma unroll
-  for (int i = 0; i < XD; ++i) dma_x(XBASE, 0u, i);
+  for (int i = 0; i < NDMA; ++i) dma_x(XBASE, 0u, i);
 #pragma unroll
-  for (int i = 0; i < XD; ++i) dma_x(XBASE + XCH, (uint32_t)Q_ROW, i);
-  wait_vm<XD>();
+  for (int i = 0; i < NDMA; ++i) dma_x(XBASE + CH, (uint32_t)Q_ROW, i);
+  wait_vm<NDMA>();
 #pragma unroll
-  for (int i = 0; i < NI; ++i) asm volatile("" : "+v"(sa8[i]));
+  for (int i = 0; i < NT; ++i) asm volatile("" : "+v"(sa8[i]));
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) asm volatile("" : "+v"(sb8[j]));
+  for (int j = 0; j < NT; ++j) asm volatile("" : "+v"(sb8[j]));
   bare_barrier();
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
+  for (int i = 0; i < NT; ++i) {
     a[i] = wfrag(0, 0, i);
     sa[i] = pick(sa8[i], 0);
-    if (i < NJ) {
+    if (i < NT) {
       b[i] = xfrag(XBASE, 0, i);
       sb[i] = pick(sb8[i], 0);
     }
@@ -365,26 +360,26 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
   auto slice = [&](int d, auto par) {
     constexpr int PAR = decltype(par)::value;
     const int c = d >> 1;
-    auto xslot = [&](int m) { const int v = xb + m; return XBASE + (v >= 3 ? v - 3 : v) * XCH; };
+    auto xslot = [&](int m) { const int v = xb + m; return XBASE + (v >= 3 ? v - 3 : v) * CH; };
     const int s_x = xslot(0), s_x1 = xslot(1), s_x2 = xslot(2);
     const uint32_t kx = d + 2 < ns ? (uint32_t)(d + 2) * Q_ROW : oobb;
     const uint32_t kw = c + 1 < nc ? (uint32_t)(c + 1) * Q_ROW : ooba;
     if (PAR == 0) scales8(min(c + 1, nc - 1), na8, nb8);   // the last chunk reloads itself, unused
     // stage 0; stage 1's fragments are read ahead
 #pragma unroll
-    for (int q = 0; q < NI; ++q) {
+    for (int q = 0; q < NT; ++q) {
       __builtin_amdgcn_sched_barrier(0);
       if (PAR == 0) {
         dma_w(wslot(c + 1), kw, 2 * q);
         dma_w(wslot(c + 1), kw, 2 * q + 1);
       } else {
 #pragma unroll
-        for (int k = 0; k < XD / NI; ++k) dma_x(s_x2, kx, XD / NI * q + k);
+        for (int k = 0; k < NDMA / NT; ++k) dma_x(s_x2, kx, NDMA / NT * q + k);
       }
       na[q] = wfrag(wslot(c), 2 * PAR + 1, q);
-      if (q < NJ) nb[q] = xfrag(s_x, 1, q);
+      if (q < NT) nb[q] = xfrag(s_x, 1, q);
       mfma_row(q);
-      if (NJ == 4) {
+      if (NT == 4) {
         SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_DSR, 1); SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_DSR, 1);
         SGB(SG_MFMA, 1); SGB(SG_DSR, 1); SGB(SG_MFMA, 1);
       } else {
@@ -392,47 +387,47 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
       }
     }
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
+    for (int i = 0; i < NT; ++i) {
       a[i] = na[i];
       sa[i] = pick(sa8[i], 2 * PAR + 1);
-      if (i < NJ) {
+      if (i < NT) {
         b[i] = nb[i];
         sb[i] = pick(sb8[i], 2 * PAR + 1);
       }
     }
     // stage 1; the barrier that publishes slice d+1 after half its row blocks
 #pragma unroll
-    for (int q = 0; q < NI / 2; ++q) {
+    for (int q = 0; q < NT / 2; ++q) {
       __builtin_amdgcn_sched_barrier(0);
       if (PAR == 0) {
 #pragma unroll
-        for (int k = 0; k < 2 * XD / NI; ++k) dma_x(s_x2, kx, 2 * XD / NI * q + k);
+        for (int k = 0; k < 2 * NDMA / NT; ++k) dma_x(s_x2, kx, 2 * NDMA / NT * q + k);
       }
       mfma_row(q);
       if (PAR == 0) {
         SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_MFMA, 1); SGB(SG_VMEM, 1);
-        if (NJ == 4) { SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); }
+        if (NT == 4) { SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); }
       }
     }
     __builtin_amdgcn_sched_barrier(0);
     // in flight may be x of slice d+2 and, in an even slice, the W chunk
     // after this slice's (not needed before the next slice's end)
-    if (PAR == 0) wait_vm<WD + XD>();
-    else wait_vm<XD>();
+    if (PAR == 0) wait_vm<NDMA + NDMA>();
+    else wait_vm<NDMA>();
     wait_lgkm0();
     bare_barrier();
     const int sw1 = wslot(PAR == 1 ? c + 1 : c);
     constexpr int u1 = PAR == 1 ? 0 : 2;
 #pragma unroll
-    for (int q = NI / 2; q < NI; ++q) {
+    for (int q = NT / 2; q < NT; ++q) {
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 2 * q - NI; i < 2 * q - NI + 2; ++i) {
+      for (int i = 2 * q - NT; i < 2 * q - NT + 2; ++i) {
         na[i] = wfrag(sw1, u1, i);
-        if (i < NJ) nb[i] = xfrag(s_x1, 0, i);
+        if (i < NT) nb[i] = xfrag(s_x1, 0, i);
       }
       mfma_row(q);
-      if (NJ == 4) {
+      if (NT == 4) {
         SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2);
         SGB(SG_MFMA, 1);
       } else {
@@ -440,11 +435,11 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
       }
     }
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
+    for (int i = 0; i < NT; ++i) {
       a[i] = na[i];
       if (PAR == 1) sa8[i] = na8[i];
       sa[i] = pick(sa8[i], u1);
-      if (i < NJ) {
+      if (i < NT) {
         b[i] = nb[i];
         if (PAR == 1) sb8[i] = nb8[i];
         sb[i] = pick(sb8[i], u1);
@@ -459,22 +454,22 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
   if constexpr (HALF) slice(ns - 1, Int<0>{});
   __builtin_amdgcn_sched_barrier(0);
   wait_vm<0>();   // the zero-fill DMAs of the last slices land before LDS is reused
-  store_tile<NI, NJ>(acc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
+  store_tile<NT>(acc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
 }
 
-template <int NI, int NJ, bool HALF>
+template <int NT, bool HALF>
 hipError_t launch_half(const void* x, const uint8_t* xs, int T, int K, const uint8_t* w, const uint8_t* ws, int N,
                        uint16_t* kv, hipStream_t s, const GateEpi& ep) {
-  const int tiles_n = (N + 64 * NI - 1) / (64 * NI), tiles_t = (T + 64 * NJ - 1) / (64 * NJ);
+  const int tiles_n = (N + 64 * NT - 1) / (64 * NT), tiles_t = (T + 64 * NT - 1) / (64 * NT);
   const dim3 grid(tiles_n * tiles_t), block(THREADS);
-  constexpr int lds = fp4_lds(NI, NJ);
+  constexpr int lds = fp4_lds(NT);
   hipError_t e;
   if (xs) {
-    const auto fn = gemm_fp4_mx_kernel<NI, NJ, HALF>;
+    const auto fn = gemm_fp4_mx_kernel<NT, HALF>;
     if ((e = set_lds((const void*)fn, lds)) != hipSuccess) return e;
     hipLaunchKernelGGL(fn, grid, block, lds, s, (const uint8_t*)x, xs, T, K, w, ws, N, kv, tiles_n, tiles_t, ep);
   } else {
-    const auto fn = gemm_fp4_bf16_kernel<NI, NJ, HALF>;
+    const auto fn = gemm_fp4_bf16_kernel<NT, HALF>;
     if ((e = set_lds((const void*)fn, lds)) != hipSuccess) return e;
     hipLaunchKernelGGL(fn, grid, block, lds, s, (const uint16_t*)x, T, K, w, ws, N, kv, tiles_n, tiles_t, ep);
   }
@@ -483,40 +478,30 @@ hipError_t launch_half(const void* x, const uint8_t* xs, int T, int K, const uin
 
 // The half chunk at the end is code of its own behind the loop: one that the
 // loop leaves early for cost the accumulators' registers (1000 spilled).
-template <int NI, int NJ>
+template <int NT>
 hipError_t launch_tile(const void* x, const uint8_t* xs, int T, int K, const uint8_t* w, const uint8_t* ws, int N,
                        uint16_t* kv, hipStream_t s, const GateEpi& ep) {
-  return K % 256 ? launch_half<NI, NJ, true>(x, xs, T, K, w, ws, N, kv, s, ep)
-                 : launch_half<NI, NJ, false>(x, xs, T, K, w, ws, N, kv, s, ep);
+  return K % 256 ? launch_half<NT, true>(x, xs, T, K, w, ws, N, kv, s, ep)
+                 : launch_half<NT, false>(x, xs, T, K, w, ws, N, kv, s, ep);
 }
 
 }  // namespace
 
-// The tile by what its rounds cost, a full round of 256x256 tiles being 100.
-// Larger tiles move fewer bytes a flop; smaller ones fill the compute units
-// where there are few, and end sooner. Measured at K 2048, bf16 x: a round of
-// 256x128 tiles costs 60 of that, one of 128x128 tiles 60 as well with two
-// workgroups on a compute unit and 42 with one (N 20480: T 128 in 40 / 24 / 18
-// us for 256x256 / 256x128 / 128x128, T 515 50 / 53 / 52, T 1000 90 / 83 / 74, T
-// 8192 490 / 540 / 550).
-MxFp4Tile gemm_mxfp4_tile(int64_t T, int N) {
-  const int64_t cus = dev_info().num_cus;
-  auto tiles = [&](int tm, int tt) { return ((int64_t)N + tm - 1) / tm * ((T + tt - 1) / tt); };
-  auto rounds = [&](int64_t n) { return (n + cus - 1) / cus; };
-  const int64_t n22 = tiles(128, 128), last = n22 % (2 * cus);
-  const int64_t c44 = 100 * rounds(tiles(256, 256)), c42 = 60 * rounds(tiles(256, 128));
-  const int64_t c22 = 60 * (n22 / (2 * cus)) + (last > cus ? 60 : last > 0 ? 42 : 0);
-  return c44 <= c42 && c44 <= c22 ? MxFp4Tile::k256x256 : c42 <= c22 ? MxFp4Tile::k256x128 : MxFp4Tile::k128x128;
+// Measured in us, 256x256 / 128x128 tiles: bf16 x, N 20480, K 2048: T 128 40 /
+// 18, T 515 47 / 53, T 1000 91 / 73, T 8192 500 / 550; T 6164, N 10656, K 512 89
+// / 76; MXFP8 x: T 128 25 / 11, T 515 29 / 32, T 8192 300 / 327, K 512 67 / 52.
+// 256x128 tiles came within 2% of the better of the two at best, and went.
+bool gemm_mxfp4_small_tiles(int64_t T, int N, int K, bool x_mxfp8) {
+  return small_tiles(T, N, K, x_mxfp8 ? TileTimes{8000, 1370, 3100, 830, 2000, 585}
+                                      : TileTimes{7000, 2700, 3000, 1540, 2200, 970});
 }
 
 // The gate's epilogue has the 256x256 tile only.
 hipError_t launch_gemm_mxfp4(const void* x, const uint8_t* xs, int64_t T, int K, const uint8_t* w,
                              const uint8_t* ws, int N, void* kv, hipStream_t s, const GateEpi& ep) {
-  switch (ep.hidden ? MxFp4Tile::k256x256 : gemm_mxfp4_tile(T, N)) {
-    case MxFp4Tile::k256x256: return launch_tile<4, 4>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep);
-    case MxFp4Tile::k256x128: return launch_tile<4, 2>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep);
-    default: return launch_tile<2, 2>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep);
-  }
+  return !ep.hidden && gemm_mxfp4_small_tiles(T, N, K, xs != nullptr)
+             ? launch_tile<2>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep)
+             : launch_tile<4>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep);
 }
 
 }  // namespace engram

@@ -87,21 +87,21 @@ __device__ __forceinline__ void store_nt(uint16_t* dst, const uint4& v) {
 //    bf16-rounded keys ("vllm.models.deepseek_v41.amd.engram",
 //    _engram_gate_partials_kernel, at tile granularity), into
 //    ep.part[(h*T + t) * (dim/256) + tile].
-// NI, NJ: 32-row and 32-token blocks of a wave (4, 4: the 256x256 tile;
-// smaller ones have the plain store only).
-template <int NI = 4, int NJ = 4>
-__device__ __forceinline__ void store_tile(f32x16 (&acc)[NI][NJ], char* smem, uint16_t* __restrict__ kv,
+// NT: 32-row and 32-token blocks of a wave (4: the 256x256 tile; 2: 128x128,
+// the plain store only).
+template <int NT = 4>
+__device__ __forceinline__ void store_tile(f32x16 (&acc)[NT][NT], char* smem, uint16_t* __restrict__ kv,
                                            int T, int N, int t0, int n0, int wn, int wt, int lane,
                                            int wave, const GateEpi& ep) {
-  constexpr int RB = 128 * NI, CPR = 8 * NI;   // bytes and 16-byte chunks of a staged row
+  constexpr int RB = 128 * NT, CPR = 8 * NT;   // bytes and 16-byte chunks of a staged row
   const int lrow = lane & 31, lhalf = lane >> 5;
   wait_lgkm0();
   bare_barrier();
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) {
+  for (int j = 0; j < NT; ++j) {
     const int t = wt + j * 32 + lrow;
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         // accumulator r of lane l: n = 8*(r/4) + 4*(l/32) + r%4, token = l%32
@@ -118,11 +118,11 @@ __device__ __forceinline__ void store_tile(f32x16 (&acc)[NI][NJ], char* smem, ui
   auto lds_row = [&](int t) {
     return *reinterpret_cast<const uint4*>(smem + t * RB + ((c ^ (t & (CPR - 1))) << 4));
   };
-  if (NI < 4 || NJ < 4 || !ep.hidden) {
+  if (NT < 4 || !ep.hidden) {
     const int n = n0 + c * 8;
 #pragma unroll 4
-    for (int it = 0; it < 2 * NI * NJ; ++it) {
-      const int t = wave * (16 * NJ) + it * (64 / CPR) + lane / CPR;
+    for (int it = 0; it < 2 * NT * NT; ++it) {
+      const int t = wave * (16 * NT) + it * (64 / CPR) + lane / CPR;
       const uint4 v = lds_row(t);
       if (t0 + t < T) {
         uint16_t* dst = kv + (int64_t)(t0 + t) * N + n;
@@ -226,6 +226,25 @@ __device__ __forceinline__ void store_tile(f32x16 (&acc)[NI][NJ], char* smem, ui
   }
   const int t = wave * 64 + 4 * c16 + g;
   if (t0 + t < T) ep.part[((int64_t)h * T + t0 + t) * tiles + tile] = make_float2(dts[0], kss[0]);
+}
+
+// Whether 128x128 tiles store kv sooner than 256x256 ones: by the rounds that
+// each needs and a round's time, an offset (launch, first DMAs, epilogue) and so
+// much a 128-k slice. With two 128x128 workgroups on a compute unit one's
+// epilogue runs beside the other's loop. The times (ns) are fitted to T 65-8192,
+// N 96-35840, K 128-4096 for each kernel; kv is the same bit for bit either way.
+struct TileTimes {
+  int big, big_k;     // a round of 256x256 tiles
+  int full, full_k;   // a round of 128x128 tiles, two on a compute unit
+  int half, half_k;   // the same, one on a compute unit
+};
+
+inline bool small_tiles(int64_t T, int64_t N, int K, const TileTimes& t) {
+  const int64_t cus = dev_info().num_cus, ks = K / 128;
+  const int64_t big = ((N + 255) / 256) * ((T + 255) / 256), small = ((N + 127) / 128) * ((T + 127) / 128);
+  const int64_t last = small % (2 * cus), full = t.full + t.full_k * ks, half = t.half + t.half_k * ks;
+  return small / (2 * cus) * full + (last > cus ? full : last > 0 ? half : 0) <
+         (big + cus - 1) / cus * (t.big + t.big_k * ks);
 }
 
 inline hipError_t set_lds(const void* fn, int bytes) {

@@ -400,7 +400,7 @@ typedef struct engram_forward_args {
  *   stored whole and the plain gate kernel reads it back (the composition of
  *   engram_wkv and engram_gate). With ENGRAM_W_MXFP4
  *   the epilogue is used only where T and N fill the compute
- *   units with 256x256 tiles. Elsewhere the option has no effect. The two
+ *   units with 256x256 tiles or kv is larger than 128 MiB. Elsewhere the option has no effect. The two
  *   routes agree to the rounding of the gate's sums (the same bf16 keys
  *   summed in another order).
  */

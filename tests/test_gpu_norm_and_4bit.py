@@ -406,7 +406,7 @@ def test_forward_mxfp4(T, dim, hc, C, fp8_table):
         assert torch.equal(a, outs[0])
 
 
-@pytest.mark.parametrize("C", [4, 6])
+@pytest.mark.parametrize("C", [8, 6])
 def test_forward_mxfp4_gate_epilogue(C):
     """Enough tokens that the forward's default is the GEMM's gate epilogue (6
     x 80 tiles of 256x256 on 256 compute units), and the route that stores kv:
@@ -578,12 +578,11 @@ class _FakeOther:
 @pytest.mark.parametrize("op", ["wkv", "wkv_mx"])
 @pytest.mark.parametrize("T,K,N", [(1500, 256, 20480), (1500, 512, 20476), (300, 768, 20480), (515, 256, 10236),
                                    (4096, 512, 5116), (1500, 384, 20476), (1500, 128, 20480), (300, 640, 20480),
-                                   (515, 128, 10236), (4096, 384, 5116)])
+                                   (515, 128, 10236), (4096, 384, 5116), (515, 1024, 20480), (515, 1152, 20476)])
 def test_mxfp4_many_tiles(op, T, K, N):
-    """Enough tiles that the GEMM's larger ones run (256x256 in the first two,
-    256x128 in the next two, 128x128 in the fifth, on 256 compute units; then
-    the same with a half chunk at K's end), ragged in T and N; a token from
-    every tile and some more."""
+    """Many tiles, ragged in T and N, with and without a half chunk at K's end:
+    128x128, on 256 compute units 256x256 in the last two (and the second with
+    bf16 x); a token from every tile and some more."""
     E = _E()
     rng = np.random.default_rng(K)
     wq, ws = mxfp4_weight(rng, N, K)
@@ -600,6 +599,26 @@ def test_mxfp4_many_tiles(op, T, K, N):
         kv = E.wkv_mx(torch.from_numpy(xq).to(DEV), torch.from_numpy(xs).to(DEV), wd, sd)
     ref, tol = product_tolerance(xa[toks], wa, scaled=op == "wkv_mx")
     _inside(bf16_values(bits(kv[torch.from_numpy(toks).to(DEV)])), ref, tol, op)
+
+
+@pytest.mark.parametrize("T,K,N", [(65, 128, 32), (70, 384, 96), (130, 256, 160), (257, 2048, 2080), (300, 640, 1280),
+                                   (515, 512, 20480), (515, 896, 20480), (700, 4224, 20448)])
+def test_wkv_mx_mxfp8_weight_tiles(T, K, N):
+    """MXFP8 weights past the GEMV: 128x128 tiles in the first five, 256x256 in
+    the others (on 256 compute units), with and without a half pair of slices at
+    K's end, ragged in T and N."""
+    E = _E()
+    rng = np.random.default_rng(T + K)
+    w = torch.from_numpy(rng.standard_normal((N, K)).astype(np.float32)).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    s = rng.integers(119, 128, size=(N // 32, K // 32), dtype=np.uint8)
+    xq, xs = mxfp8_rows(rng, T, K)
+    guard = torch.full((T * N + 512,), 55, dtype=torch.bfloat16, device=DEV)
+    kv = guard[:T * N].view(T, N)
+    E.wkv_mx(*(torch.from_numpy(t).to(DEV) for t in (xq, xs, w, s)), kv=kv)
+    assert bool((guard[T * N:] == 55).all())
+    toks = sample_tokens(T, 48, seed=1, tile=128)
+    ref, tol = product_tolerance(o.mx_dequantize_activations(xq[toks], xs[toks]), o.mx_dequantize_weight(w, s), scaled=True)
+    _inside(bf16_values(bits(kv[torch.from_numpy(toks).to(DEV)])), ref, tol, "wkv_mx mxfp8")
 
 
 @pytest.mark.parametrize("op", ["wkv", "wkv_mx"])
