@@ -6,7 +6,8 @@
 // W stays e2m1 all the way into LDS: a 128-byte LDS row of W holds 256 k, so a
 // 32 KiB chunk of W serves four bf16 slices of x (64 k) or two MXFP8 slices
 // (128 k), and a slice moves 40 (48) KiB from L2 instead of 64, which is what
-// bounds those kernels. LDS: two slots for W chunks, a ring of three for x.
+// bounds those kernels. LDS: two slots for W chunks, a ring of three or
+// four for x.
 // Where K % 256 == 128 the last chunk is half: its rows' second 64 bytes are
 // the next row's (zeros past the tile), as the second half of its scale bytes
 // is, and the loop ends before the slices that would use them.
@@ -34,16 +35,20 @@ namespace engram {
 
 namespace {
 
-constexpr int kWSlots = 2, kXSlots = 3;
+constexpr int kWSlots = 2;
 // A block is 64 * NT W rows x 64 * NT tokens: 256 x 256, or 128 x 128 with two
-// workgroups on a compute unit (launch_gemm_mxfp4).
-constexpr int fp4_lds(int nt) { return (kWSlots + kXSlots) * 64 * nt * Q_ROW; }
-static_assert(fp4_lds(4) == Q_LDS && 2 * fp4_lds(2) <= Q_LDS, "LDS budget");
+// workgroups on a compute unit (launch_gemm_mxfp4). x is fetched LA slices
+// ahead, into a ring of LA + 1: two fill LDS; three where there is one 128 x
+// 128 workgroup for a compute unit and no other to cover a late slice (N 20480,
+// T 128, bf16 / MXFP8 x: K 2048 18.6 -> 15.5 / 11.5 -> 10.5 us, K 4096 33.4 ->
+// 26.9 / 20.6 -> 20.1; four, or a third slot for W, gave no more).
+constexpr int fp4_lds(int nt, int la) { return (kWSlots + la + 1) * 64 * nt * Q_ROW; }
+static_assert(fp4_lds(4, 2) == Q_LDS && 2 * fp4_lds(2, 2) <= Q_LDS, "LDS budget");
 constexpr int SG_VALU = 0x002;
 
 template <int V> using Int = std::integral_constant<int, V>;
 
-template <int NT, bool HALF>
+template <int NT, bool HALF, int LA>
 __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(NT == 4 ? 1 : 2, NT == 4 ? 1 : 2)))
 void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const uint8_t* __restrict__ w,
                           const uint8_t* __restrict__ ws, int N, uint16_t* __restrict__ kv, int tiles_n,
@@ -124,7 +129,7 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
   };
   auto wslot = [](int c) { return (c & 1) * CH; };
 
-  // prologue: W chunk 0, x slices 0 and 1; all but x slice 1's DMAs waited for
+  // prologue: W chunk 0, x slices 0 .. LA - 1; W and x slice 0 waited for
   u32x2 s8[NT], n8[NT];
   scales8(0, s8);
   __builtin_amdgcn_sched_barrier(0);
@@ -133,8 +138,10 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
 #pragma unroll
   for (int i = 0; i < NDMA; ++i) dma_x(XBASE, 0u, i);
 #pragma unroll
-  for (int i = 0; i < NDMA; ++i) dma_x(XBASE + CH, (uint32_t)Q_ROW, i);
-  wait_vm<NDMA>();
+  for (int m = 1; m < LA; ++m)
+#pragma unroll
+    for (int i = 0; i < NDMA; ++i) dma_x(XBASE + m * CH, m < 2 || m < nk ? (uint32_t)(m * Q_ROW) : oobb, i);
+  wait_vm<(LA - 1) * NDMA>();
   // a use here keeps the scale loads ahead of the DMAs
 #pragma unroll
   for (int i = 0; i < NT; ++i) asm volatile("" : "+v"(s8[i]));
@@ -149,16 +156,16 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
 #pragma unroll
   for (int i = 0; i < NT; ++i) convert(0, 0, i);
 
-  int xb = 0;   // d % 3
-  // slice d (64 k), par = d % 4: x of slice d+2 and, in the chunk's first
+  int xb = 0;   // d % (LA + 1)
+  // slice d (64 k), par = d % 4: x of slice d+LA and, in the chunk's first
   // three slices, W of the next chunk are fetched; the barrier that publishes
   // slice d+1 sits after the first 4 of the last 16 MFMAs.
   auto slice = [&](int d, auto par) {
     constexpr int PAR = decltype(par)::value;
     const int c = d >> 2;
-    auto xslot = [&](int m) { const int v = xb + m; return XBASE + (v >= 3 ? v - 3 : v) * CH; };
-    const int sb = xslot(0), sb1 = xslot(1), sb2 = xslot(2);
-    const uint32_t kx = d + 2 < nk ? (uint32_t)(d + 2) * Q_ROW : oobb;
+    auto xslot = [&](int m) { const int v = xb + m; return XBASE + (v > LA ? v - LA - 1 : v) * CH; };
+    const int sb = xslot(0), sb1 = xslot(1), sb2 = xslot(LA);
+    const uint32_t kx = d + LA < nk ? (uint32_t)(d + LA) * Q_ROW : oobb;
     const uint32_t kw = c + 1 < nc ? (uint32_t)(c + 1) * Q_ROW : ooba;
     if (PAR == 0) scales8(min(c + 1, nc - 1), n8);   // the last chunk reloads itself, unused
     // sub-steps 0..2: MFMAs of sub-step kk, fragments of kk+1
@@ -187,7 +194,9 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
     __builtin_amdgcn_sched_barrier(0);
     mfma_row(1, 0);
     __builtin_amdgcn_sched_barrier(0);
-    wait_vm<NDMA>();   // only x of slice d+2 may still fly
+    // only the last LA - 1 slices' x DMAs may still fly; the next chunk's last W
+    // DMA went out beside the first of slice d-1's, in whichever order
+    wait_vm<(LA - 1) * NDMA - (LA > 2 && PAR == 3)>();
     wait_lgkm0();
     bare_barrier();
     // the rest of sub-step 3: slice d+1's W words, first x fragments, conversions
@@ -230,7 +239,7 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
 #pragma unroll
       for (int i = 0; i < NT; ++i) s8[i] = n8[i];
     }
-    xb = xb + 1 >= 3 ? 0 : xb + 1;
+    xb = xb + 1 > LA ? 0 : xb + 1;
   };
   for (int d = 0; d < (HALF ? nk - 2 : nk); d += 4) {
     slice(d, Int<0>{});
@@ -247,7 +256,7 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
   store_tile<NT>(acc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
 }
 
-template <int NT, bool HALF>
+template <int NT, bool HALF, int LA>
 __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(NT == 4 ? 1 : 2, NT == 4 ? 1 : 2)))
 void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restrict__ xs, int T, int K,
                         const uint8_t* __restrict__ w, const uint8_t* __restrict__ ws, int N,
@@ -337,8 +346,10 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
 #pragma unroll
   for (int i = 0; i < NDMA; ++i) dma_x(XBASE, 0u, i);
 #pragma unroll
-  for (int i = 0; i < NDMA; ++i) dma_x(XBASE + CH, (uint32_t)Q_ROW, i);
-  wait_vm<NDMA>();
+  for (int m = 1; m < LA; ++m)
+#pragma unroll
+    for (int i = 0; i < NDMA; ++i) dma_x(XBASE + m * CH, m < 2 || m < ns ? (uint32_t)(m * Q_ROW) : oobb, i);
+  wait_vm<(LA - 1) * NDMA>();
 #pragma unroll
   for (int i = 0; i < NT; ++i) asm volatile("" : "+v"(sa8[i]));
 #pragma unroll
@@ -354,15 +365,15 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
     }
   }
 
-  int xb = 0;   // d % 3
-  // slice d (two stages of 64 k), par = d % 2: x of slice d+2 goes out in the
+  int xb = 0;   // d % (LA + 1)
+  // slice d (two stages of 64 k), par = d % 2: x of slice d+LA goes out in the
   // last six quarters, W of the next chunk in the first four of an even slice
   auto slice = [&](int d, auto par) {
     constexpr int PAR = decltype(par)::value;
     const int c = d >> 1;
-    auto xslot = [&](int m) { const int v = xb + m; return XBASE + (v >= 3 ? v - 3 : v) * CH; };
-    const int s_x = xslot(0), s_x1 = xslot(1), s_x2 = xslot(2);
-    const uint32_t kx = d + 2 < ns ? (uint32_t)(d + 2) * Q_ROW : oobb;
+    auto xslot = [&](int m) { const int v = xb + m; return XBASE + (v > LA ? v - LA - 1 : v) * CH; };
+    const int s_x = xslot(0), s_x1 = xslot(1), s_x2 = xslot(LA);
+    const uint32_t kx = d + LA < ns ? (uint32_t)(d + LA) * Q_ROW : oobb;
     const uint32_t kw = c + 1 < nc ? (uint32_t)(c + 1) * Q_ROW : ooba;
     if (PAR == 0) scales8(min(c + 1, nc - 1), na8, nb8);   // the last chunk reloads itself, unused
     // stage 0; stage 1's fragments are read ahead
@@ -410,10 +421,10 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
       }
     }
     __builtin_amdgcn_sched_barrier(0);
-    // in flight may be x of slice d+2 and, in an even slice, the W chunk
-    // after this slice's (not needed before the next slice's end)
-    if (PAR == 0) wait_vm<NDMA + NDMA>();
-    else wait_vm<NDMA>();
+    // in flight may be x of slices d+2 .. d+LA and, in an even slice, the W
+    // chunk after this slice's (not needed before the next slice's end)
+    if (PAR == 0) wait_vm<LA * NDMA>();
+    else wait_vm<(LA - 1) * NDMA>();
     wait_lgkm0();
     bare_barrier();
     const int sw1 = wslot(PAR == 1 ? c + 1 : c);
@@ -445,7 +456,7 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
         sb[i] = pick(sb8[i], u1);
       }
     }
-    xb = xb + 1 >= 3 ? 0 : xb + 1;
+    xb = xb + 1 > LA ? 0 : xb + 1;
   };
   for (int d = 0; d < (HALF ? ns - 1 : ns); d += 2) {
     slice(d, Int<0>{});
@@ -457,19 +468,19 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
   store_tile<NT>(acc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
 }
 
-template <int NT, bool HALF>
+template <int NT, bool HALF, int LA>
 hipError_t launch_half(const void* x, const uint8_t* xs, int T, int K, const uint8_t* w, const uint8_t* ws, int N,
                        uint16_t* kv, hipStream_t s, const GateEpi& ep) {
   const int tiles_n = (N + 64 * NT - 1) / (64 * NT), tiles_t = (T + 64 * NT - 1) / (64 * NT);
   const dim3 grid(tiles_n * tiles_t), block(THREADS);
-  constexpr int lds = fp4_lds(NT);
+  constexpr int lds = fp4_lds(NT, LA);
   hipError_t e;
   if (xs) {
-    const auto fn = gemm_fp4_mx_kernel<NT, HALF>;
+    const auto fn = gemm_fp4_mx_kernel<NT, HALF, LA>;
     if ((e = set_lds((const void*)fn, lds)) != hipSuccess) return e;
     hipLaunchKernelGGL(fn, grid, block, lds, s, (const uint8_t*)x, xs, T, K, w, ws, N, kv, tiles_n, tiles_t, ep);
   } else {
-    const auto fn = gemm_fp4_bf16_kernel<NT, HALF>;
+    const auto fn = gemm_fp4_bf16_kernel<NT, HALF, LA>;
     if ((e = set_lds((const void*)fn, lds)) != hipSuccess) return e;
     hipLaunchKernelGGL(fn, grid, block, lds, s, (const uint16_t*)x, T, K, w, ws, N, kv, tiles_n, tiles_t, ep);
   }
@@ -478,30 +489,32 @@ hipError_t launch_half(const void* x, const uint8_t* xs, int T, int K, const uin
 
 // The half chunk at the end is code of its own behind the loop: one that the
 // loop leaves early for cost the accumulators' registers (1000 spilled).
-template <int NT>
+template <int NT, int LA>
 hipError_t launch_tile(const void* x, const uint8_t* xs, int T, int K, const uint8_t* w, const uint8_t* ws, int N,
                        uint16_t* kv, hipStream_t s, const GateEpi& ep) {
-  return K % 256 ? launch_half<NT, true>(x, xs, T, K, w, ws, N, kv, s, ep)
-                 : launch_half<NT, false>(x, xs, T, K, w, ws, N, kv, s, ep);
+  return K % 256 ? launch_half<NT, true, LA>(x, xs, T, K, w, ws, N, kv, s, ep)
+                 : launch_half<NT, false, LA>(x, xs, T, K, w, ws, N, kv, s, ep);
 }
 
 }  // namespace
 
 // Measured in us, 256x256 / 128x128 tiles: bf16 x, N 20480, K 2048: T 128 40 /
-// 18, T 515 47 / 53, T 1000 91 / 73, T 8192 500 / 550; T 6164, N 10656, K 512 89
-// / 76; MXFP8 x: T 128 25 / 11, T 515 29 / 32, T 8192 300 / 327, K 512 67 / 52.
+// 15.5, T 515 47 / 53, T 1000 91 / 73, T 8192 500 / 550; T 6164, N 10656, K 512 89
+// / 76; MXFP8 x: T 128 25 / 10.5, T 515 29 / 32, T 8192 300 / 327, K 512 67 / 52.
 // 256x128 tiles came within 2% of the better of the two at best, and went.
 bool gemm_mxfp4_small_tiles(int64_t T, int N, int K, bool x_mxfp8) {
-  return small_tiles(T, N, K, x_mxfp8 ? TileTimes{8000, 1370, 3100, 830, 2000, 585}
-                                      : TileTimes{7000, 2700, 3000, 1540, 2200, 970});
+  return small_tiles(T, N, K, x_mxfp8 ? TileTimes{8000, 1370, 3100, 830, 1500, 570}
+                                      : TileTimes{7000, 2700, 3000, 1540, 3400, 750});
 }
 
 // The gate's epilogue has the 256x256 tile only.
 hipError_t launch_gemm_mxfp4(const void* x, const uint8_t* xs, int64_t T, int K, const uint8_t* w,
                              const uint8_t* ws, int N, void* kv, hipStream_t s, const GateEpi& ep) {
-  return !ep.hidden && gemm_mxfp4_small_tiles(T, N, K, xs != nullptr)
-             ? launch_tile<2>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep)
-             : launch_tile<4>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep);
+  if (ep.hidden || !gemm_mxfp4_small_tiles(T, N, K, xs != nullptr))
+    return launch_tile<4, 2>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep);
+  return ((int64_t)N + 127) / 128 * ((T + 127) / 128) <= dev_info().num_cus
+             ? launch_tile<2, 3>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep)
+             : launch_tile<2, 2>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep);
 }
 
 }  // namespace engram

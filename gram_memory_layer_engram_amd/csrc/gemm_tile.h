@@ -17,7 +17,7 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 constexpr int BM = 256;      // W rows per block
 constexpr int BN = 256;      // tokens per block
 constexpr int THREADS = 256;
-constexpr int LDS_BYTES = 128 * 1024;            // two-stage MXFP8; the epilogue's staging tile (rings: Q_LDS)
+constexpr int LDS_BYTES = 128 * 1024;            // the epilogue's staging tile (rings: Q_LDS)
 static_assert(BN * 512 == LDS_BYTES, "epilogue staging tile");
 // rings: 64-element bf16 (128-element MXFP8) k slices (128-byte LDS rows of 8 pieces, piece p of row
 // r at p ^ ((r >> 1) & 7)); each operand's slice is a 32 KiB chunk in a ring
