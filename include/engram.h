@@ -177,7 +177,7 @@ int engram_mx_quantize(const void* x, int64_t T, int32_t K, uint8_t* xq,
  *              or packed codes [N, K/2] (ENGRAM_W_MXFP4).
  *   w_scales   uint8 [N/32, K/32] for MXFP8 (4-byte aligned), [N, K/32] for
  *              MXFP4 (16-byte aligned), NULL for bf16.
- *   kv         bf16 [T, N].
+ *   kv         bf16 [T, N]; on no operand (MXFP4: ENGRAM_EINVAL).
  *   workspace  device scratch of at least engram_wkv_workspace_size() bytes
  *              (NULL allowed when that size is 0). For MXFP8 it holds x's
  *              MXFP8 codes and scales. 256-byte aligned.
@@ -212,7 +212,7 @@ int engram_wkv(const void* x, int64_t T, int32_t K, const void* w,
  *               16-byte aligned.
  *   w, w_scales, w_format   ENGRAM_W_MXFP8 or ENGRAM_W_MXFP4 as engram_wkv;
  *               ENGRAM_W_BF16 returns ENGRAM_EUNSUPPORTED.
- *   kv          bf16 [T, N].
+ *   kv          bf16 [T, N]; on an operand: ENGRAM_EINVAL.
  *   Shapes and errors: as engram_wkv for the format.
  */
 int engram_wkv_mx(const uint8_t* xq, const uint8_t* xs, int64_t T, int32_t K, const void* w,

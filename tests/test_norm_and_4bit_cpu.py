@@ -81,12 +81,16 @@ def test_mxfp4_projection_refusals(lib):
     F4, F8, BF = 2, 1, 0
     big = 1 << 40
 
-    def wkv(T=4, K=256, N=64, x=P, w=P, s=P, kv=P, ws=P, nbytes=big):
+    X, W, S, V, Y = (i << 24 for i in range(1, 6))     # apart: x, w, its scales, kv, x's scales
+
+    def wkv(T=4, K=256, N=64, x=X, w=W, s=S, kv=V, ws=P, nbytes=big):
         return lib.engram_wkv(x, T, K, w, s, F4, N, kv, ws, nbytes, None)
 
     assert wkv(T=0, x=None, w=None, s=None, kv=None, ws=None, nbytes=0) == OK
     for bad in (dict(T=-1), dict(K=0), dict(N=0), dict(x=None), dict(w=None), dict(s=None), dict(kv=None),
-                dict(x=P + 2), dict(w=P + 8), dict(s=P + 1), dict(s=P + 4)):
+                dict(x=X + 2), dict(w=W + 8), dict(s=S + 1), dict(s=S + 4), dict(kv=V + 2),
+                # kv (512 bytes) on x (2048), w (8192) or its scales (512)
+                dict(kv=X), dict(kv=X + 2032), dict(kv=X - 496), dict(kv=W + 8176), dict(kv=S + 496), dict(kv=S - 496)):
         assert wkv(**bad) == INV, bad
     for bad in (dict(K=192), dict(K=1 << 21), dict(N=66), dict(N=(1 << 28) + 4)):
         assert wkv(**bad) == UNS, bad
@@ -94,13 +98,15 @@ def test_mxfp4_projection_refusals(lib):
     for T, K in ((0, 256), (64, 384), (300, 256), (300, 384)):
         assert lib.engram_wkv_workspace_size(T, K, 64, F4) == 0
 
-    def mx(T=4, K=256, N=64, xq=P, xs=P, w=P, s=P, f=F4, kv=P):
+    def mx(T=4, K=256, N=64, xq=X, xs=Y, w=W, s=S, f=F4, kv=V):
         return lib.engram_wkv_mx(xq, xs, T, K, w, s, f, N, kv, None)
 
     for f in (F4, F8):
         assert mx(f=f, T=0, xq=None, xs=None, w=None, s=None, kv=None) == OK
         for bad in (dict(T=-1), dict(K=0), dict(N=0), dict(xq=None), dict(xs=None), dict(w=None), dict(s=None),
-                    dict(kv=None), dict(xq=P + 8), dict(xs=P + 4), dict(w=P + 8), dict(s=P + 1), dict(kv=P + 2)):
+                    dict(kv=None), dict(xq=X + 8), dict(xs=Y + 4), dict(w=W + 8), dict(s=S + 1), dict(kv=V + 2),
+                    # kv on the codes (1024 bytes), x's scales (32), w (8192 at least), its scales (16 at least)
+                    dict(kv=X + 1008), dict(kv=Y + 16), dict(kv=Y - 496), dict(kv=W + 8176), dict(kv=S)):
             assert mx(f=f, **bad) == INV, (f, bad)
         assert mx(f=f, K=192) == UNS and mx(f=f, N=66) == UNS
     assert mx(f=F8, N=36) == UNS
