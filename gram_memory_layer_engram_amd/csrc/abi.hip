@@ -456,7 +456,7 @@ static int run_forward(const engram_forward_args* a, int32_t K, int32_t N, uint8
   // dim 4096, epilogue / kv stored: K 2048, T 300 59 / 43 us, T 1000 118 / 100, T
   // 4096 340 / 358; K 256, T 1000 51 / 42, T 4096 139 / 155).
   const bool epi = !(a->options & ENGRAM_FORWARD_STORE_KV) && tiled && a->dim % 256 == 0 &&
-                   (a->w_format != ENGRAM_W_MXFP4 || !gemm_mxfp4_small_tiles(a->T, N, K, false) ||
+                   (a->w_format != ENGRAM_W_MXFP4 || gemm_mxfp4_big_tiles(a->T, N, K) ||
                     a->T * (int64_t)N * 2 > (128 << 20));
   uint16_t* value = (uint16_t*)kv;
   float2* part = (float2*)((uint8_t*)kv + round_up((size_t)a->T * a->dim * 2));

@@ -133,9 +133,9 @@ hipError_t launch_gemv_mxfp8(const uint8_t* xq, const uint8_t* xs, int64_t T,
                              int K, const uint8_t* w, const uint8_t* ws, int N,
                              void* kv, hipStream_t s);
 
-// Whether the MXFP4 GEMM stores kv with 128x128 tiles for (T, N, K), not with
-// the 256x256 ones that the gate's epilogue has.
-bool gemm_mxfp4_small_tiles(int64_t T, int N, int K, bool x_mxfp8);
+// Whether the MXFP4 GEMM with bf16 x stores kv with the 256x256 tiles that the
+// gate's epilogue has, all of it.
+bool gemm_mxfp4_big_tiles(int64_t T, int N, int K);
 
 // Tiled GEMM with MXFP4 weights (K % 128 == 0, N % 4 == 0): x bf16, or MXFP8
 // codes when xs is not null.

@@ -225,12 +225,12 @@ template <int NT, bool HALF>
 __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(NT == 4 ? 1 : 2, NT == 4 ? 1 : 2)))
 void gemm_mx_ring_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restrict__ xs, int T, int K,
                          const uint8_t* __restrict__ w, const uint8_t* __restrict__ ws, int N,
-                         uint16_t* __restrict__ kv, int tiles_n, int tiles_t, GateEpi ep) {
+                         uint16_t* __restrict__ kv, int tn0, int tiles_n, int tiles_t, GateEpi ep) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   int tn, tt;
   tile_of(blockIdx.x, tiles_n, tiles_t, tn, tt);
   constexpr int TILE = 64 * NT, CH = S_ROW * TILE, NDMA = 2 * NT;   // a chunk in LDS, a wave's DMAs for it
-  const int n0 = tn * TILE, t0 = tt * TILE;
+  const int n0 = (tn0 + tn) * TILE, t0 = tt * TILE;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = (wave >> 1) * (32 * NT), wt = (wave & 1) * (32 * NT);
@@ -411,15 +411,15 @@ void gemm_mx_ring_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restri
   store_tile<NT>(acc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
 }
 
-template <int NT, bool HALF>
+template <int NT>
 hipError_t launch_mx_ring(const uint8_t* xq, const uint8_t* xs, int T, int K, const uint8_t* w, const uint8_t* ws,
-                          int N, uint16_t* kv, hipStream_t s, const GateEpi& ep) {
-  const int tiles_n = (N + 64 * NT - 1) / (64 * NT), tiles_t = (T + 64 * NT - 1) / (64 * NT);
+                          int N, uint16_t* kv, int tn0, int tiles_n, hipStream_t s, const GateEpi& ep) {
+  const int tiles_t = (T + 64 * NT - 1) / (64 * NT);
   constexpr int lds = Q_LDS * NT / 4;
-  const auto fn = gemm_mx_ring_kernel<NT, HALF>;
+  const auto fn = K % 256 ? gemm_mx_ring_kernel<NT, true> : gemm_mx_ring_kernel<NT, false>;
   const hipError_t e = set_lds((const void*)fn, lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(fn, dim3(tiles_n * tiles_t), dim3(THREADS), lds, s, xq, xs, T, K, w, ws, N, kv, tiles_n,
+  hipLaunchKernelGGL(fn, dim3(tiles_n * tiles_t), dim3(THREADS), lds, s, xq, xs, T, K, w, ws, N, kv, tn0, tiles_n,
                      tiles_t, ep);
   return hipGetLastError();
 }
@@ -447,17 +447,16 @@ hipError_t launch_gemm_bf16(const void* x, int64_t T, int K, const void* w, int 
 // Measured in us, 256x256 / 128x128 tiles: N 20480, K 2048: T 128 25.6 / 13.8, T
 // 300 27 / 19, T 515 29.5 / 35.6, T 1000 57 / 48, T 8192 310 / 369; T 383, N 7808,
 // K 384 12.0 / 5.2; T 6968, N 10112, K 640 76 / 68.
-// The gate's epilogue has the 256x256 tile only. kv is the same bit for bit
-// whatever the tile.
+// The gate's epilogue has the 256x256 tile only.
 hipError_t launch_gemm_mxfp8(const uint8_t* xq, const uint8_t* xs, int64_t T, int K, const uint8_t* w,
                              const uint8_t* ws, int N, void* kv, hipStream_t s, const GateEpi& ep) {
   uint16_t* out = (uint16_t*)kv;
-  const bool small = !ep.hidden && small_tiles(T, N, K, {8000, 1400, 3200, 950, 3200, 660});
-  if (K % 256)
-    return small ? launch_mx_ring<2, true>(xq, xs, (int)T, K, w, ws, N, out, s, ep)
-                 : launch_mx_ring<4, true>(xq, xs, (int)T, K, w, ws, N, out, s, ep);
-  return small ? launch_mx_ring<2, false>(xq, xs, (int)T, K, w, ws, N, out, s, ep)
-               : launch_mx_ring<4, false>(xq, xs, (int)T, K, w, ws, N, out, s, ep);
+  const int big = ep.hidden ? (N + 255) / 256 : big_columns(T, N, K, {8000, 1400, 3200, 950, 3200, 660});
+  if (big) {
+    const hipError_t e = launch_mx_ring<4>(xq, xs, (int)T, K, w, ws, N, out, 0, big, s, ep);
+    if (e != hipSuccess || 256 * (int64_t)big >= N) return e;
+  }
+  return launch_mx_ring<2>(xq, xs, (int)T, K, w, ws, N, out, 2 * big, (N + 127) / 128 - 2 * big, s, ep);
 }
 
 }  // namespace engram

@@ -51,14 +51,14 @@ template <int V> using Int = std::integral_constant<int, V>;
 template <int NT, bool HALF, int LA>
 __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(NT == 4 ? 1 : 2, NT == 4 ? 1 : 2)))
 void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const uint8_t* __restrict__ w,
-                          const uint8_t* __restrict__ ws, int N, uint16_t* __restrict__ kv, int tiles_n,
+                          const uint8_t* __restrict__ ws, int N, uint16_t* __restrict__ kv, int tn0, int tiles_n,
                           int tiles_t, GateEpi ep) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   int tn, tt;
   tile_of(blockIdx.x, tiles_n, tiles_t, tn, tt);
   constexpr int TILE = 64 * NT, CH = TILE * Q_ROW, NDMA = 2 * NT;   // a chunk or slice in LDS, a wave's DMAs for it
   constexpr int XBASE = kWSlots * CH;
-  const int n0 = tn * TILE, t0 = tt * TILE;
+  const int n0 = (tn0 + tn) * TILE, t0 = tt * TILE;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = (wave >> 1) * (32 * NT), wt = (wave & 1) * (32 * NT);
@@ -260,13 +260,13 @@ template <int NT, bool HALF, int LA>
 __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(NT == 4 ? 1 : 2, NT == 4 ? 1 : 2)))
 void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restrict__ xs, int T, int K,
                         const uint8_t* __restrict__ w, const uint8_t* __restrict__ ws, int N,
-                        uint16_t* __restrict__ kv, int tiles_n, int tiles_t, GateEpi ep) {
+                        uint16_t* __restrict__ kv, int tn0, int tiles_n, int tiles_t, GateEpi ep) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   int tn, tt;
   tile_of(blockIdx.x, tiles_n, tiles_t, tn, tt);
   constexpr int TILE = 64 * NT, CH = TILE * Q_ROW, NDMA = 2 * NT;   // a chunk or slice in LDS, a wave's DMAs for it
   constexpr int XBASE = kWSlots * CH;
-  const int n0 = tn * TILE, t0 = tt * TILE;
+  const int n0 = (tn0 + tn) * TILE, t0 = tt * TILE;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = (wave >> 1) * (32 * NT), wt = (wave & 1) * (32 * NT);
@@ -470,19 +470,19 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
 
 template <int NT, bool HALF, int LA>
 hipError_t launch_half(const void* x, const uint8_t* xs, int T, int K, const uint8_t* w, const uint8_t* ws, int N,
-                       uint16_t* kv, hipStream_t s, const GateEpi& ep) {
-  const int tiles_n = (N + 64 * NT - 1) / (64 * NT), tiles_t = (T + 64 * NT - 1) / (64 * NT);
+                       uint16_t* kv, int tn0, int tiles_n, hipStream_t s, const GateEpi& ep) {
+  const int tiles_t = (T + 64 * NT - 1) / (64 * NT);
   const dim3 grid(tiles_n * tiles_t), block(THREADS);
   constexpr int lds = fp4_lds(NT, LA);
   hipError_t e;
   if (xs) {
     const auto fn = gemm_fp4_mx_kernel<NT, HALF, LA>;
     if ((e = set_lds((const void*)fn, lds)) != hipSuccess) return e;
-    hipLaunchKernelGGL(fn, grid, block, lds, s, (const uint8_t*)x, xs, T, K, w, ws, N, kv, tiles_n, tiles_t, ep);
+    hipLaunchKernelGGL(fn, grid, block, lds, s, (const uint8_t*)x, xs, T, K, w, ws, N, kv, tn0, tiles_n, tiles_t, ep);
   } else {
     const auto fn = gemm_fp4_bf16_kernel<NT, HALF, LA>;
     if ((e = set_lds((const void*)fn, lds)) != hipSuccess) return e;
-    hipLaunchKernelGGL(fn, grid, block, lds, s, (const uint16_t*)x, T, K, w, ws, N, kv, tiles_n, tiles_t, ep);
+    hipLaunchKernelGGL(fn, grid, block, lds, s, (const uint16_t*)x, T, K, w, ws, N, kv, tn0, tiles_n, tiles_t, ep);
   }
   return hipGetLastError();
 }
@@ -491,9 +491,9 @@ hipError_t launch_half(const void* x, const uint8_t* xs, int T, int K, const uin
 // loop leaves early for cost the accumulators' registers (1000 spilled).
 template <int NT, int LA>
 hipError_t launch_tile(const void* x, const uint8_t* xs, int T, int K, const uint8_t* w, const uint8_t* ws, int N,
-                       uint16_t* kv, hipStream_t s, const GateEpi& ep) {
-  return K % 256 ? launch_half<NT, true, LA>(x, xs, T, K, w, ws, N, kv, s, ep)
-                 : launch_half<NT, false, LA>(x, xs, T, K, w, ws, N, kv, s, ep);
+                       uint16_t* kv, int tn0, int tiles_n, hipStream_t s, const GateEpi& ep) {
+  return K % 256 ? launch_half<NT, true, LA>(x, xs, T, K, w, ws, N, kv, tn0, tiles_n, s, ep)
+                 : launch_half<NT, false, LA>(x, xs, T, K, w, ws, N, kv, tn0, tiles_n, s, ep);
 }
 
 }  // namespace
@@ -502,19 +502,25 @@ hipError_t launch_tile(const void* x, const uint8_t* xs, int T, int K, const uin
 // 15.5, T 515 47 / 53, T 1000 91 / 73, T 8192 500 / 550; T 6164, N 10656, K 512 89
 // / 76; MXFP8 x: T 128 25 / 10.5, T 515 29 / 32, T 8192 300 / 327, K 512 67 / 52.
 // 256x128 tiles came within 2% of the better of the two at best, and went.
-bool gemm_mxfp4_small_tiles(int64_t T, int N, int K, bool x_mxfp8) {
-  return small_tiles(T, N, K, x_mxfp8 ? TileTimes{8000, 1370, 3100, 830, 1500, 570}
+static int fp4_big_columns(int64_t T, int N, int K, bool x_mxfp8) {
+  return big_columns(T, N, K, x_mxfp8 ? TileTimes{8000, 1370, 3100, 830, 1500, 570}
                                       : TileTimes{7000, 2700, 3000, 1540, 3400, 750});
 }
+
+bool gemm_mxfp4_big_tiles(int64_t T, int N, int K) { return fp4_big_columns(T, N, K, false) == (N + 255) / 256; }
 
 // The gate's epilogue has the 256x256 tile only.
 hipError_t launch_gemm_mxfp4(const void* x, const uint8_t* xs, int64_t T, int K, const uint8_t* w,
                              const uint8_t* ws, int N, void* kv, hipStream_t s, const GateEpi& ep) {
-  if (ep.hidden || !gemm_mxfp4_small_tiles(T, N, K, xs != nullptr))
-    return launch_tile<4, 2>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep);
-  return ((int64_t)N + 127) / 128 * ((T + 127) / 128) <= dev_info().num_cus
-             ? launch_tile<2, 3>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep)
-             : launch_tile<2, 2>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, s, ep);
+  const int big = ep.hidden ? (N + 255) / 256 : fp4_big_columns(T, N, K, xs != nullptr);
+  if (big) {
+    const hipError_t e = launch_tile<4, 2>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, 0, big, s, ep);
+    if (e != hipSuccess || 256 * (int64_t)big >= N) return e;
+  }
+  const int tn0 = 2 * big, tiles_n = (N + 127) / 128 - tn0;
+  return tiles_n * ((T + 127) / 128) <= dev_info().num_cus
+             ? launch_tile<2, 3>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, tn0, tiles_n, s, ep)
+             : launch_tile<2, 2>(x, xs, (int)T, K, w, ws, N, (uint16_t*)kv, tn0, tiles_n, s, ep);
 }
 
 }  // namespace engram

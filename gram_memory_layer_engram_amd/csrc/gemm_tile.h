@@ -228,23 +228,34 @@ __device__ __forceinline__ void store_tile(f32x16 (&acc)[NT][NT], char* smem, ui
   if (t0 + t < T) ep.part[((int64_t)h * T + t0 + t) * tiles + tile] = make_float2(dts[0], kss[0]);
 }
 
-// Whether 128x128 tiles store kv sooner than 256x256 ones: by the rounds that
-// each needs and a round's time, an offset (launch, first DMAs, epilogue) and so
-// much a 128-k slice. With two 128x128 workgroups on a compute unit one's
-// epilogue runs beside the other's loop. The times (ns) are fitted to T 65-8192,
-// N 96-35840, K 128-4096 for each kernel; kv is the same bit for bit either way.
+// How many columns of 256 W rows are stored by 256x256 tiles, the rest by
+// 128x128 ones (a second launch): by the rounds that each needs and a round's
+// time, an offset (launch, first DMAs, epilogue) and so much a 128-k slice. All,
+// none, or as many as fill whole rounds of 256x256 tiles (N 20480, K 4096, T
+// 1000, the 64 of 80, us all / none / split: MXFP4 and bf16 x 167 / 139 / 130,
+// MXFP8 x 101 / 93 / 80, MXFP8 weights 98 / 97 / 84). With two 128x128
+// workgroups on a compute unit one's epilogue runs beside the other's loop. The
+// times (ns) are fitted to T 65-8192, N 96-35840, K 128-4096 for each kernel; kv
+// is the same bit for bit whatever the tile.
 struct TileTimes {
   int big, big_k;     // a round of 256x256 tiles
   int full, full_k;   // a round of 128x128 tiles, two on a compute unit
   int half, half_k;   // the same, one on a compute unit
 };
 
-inline bool small_tiles(int64_t T, int64_t N, int K, const TileTimes& t) {
+inline int big_columns(int64_t T, int64_t N, int K, const TileTimes& t) {
   const int64_t cus = dev_info().num_cus, ks = K / 128;
-  const int64_t big = ((N + 255) / 256) * ((T + 255) / 256), small = ((N + 127) / 128) * ((T + 127) / 128);
-  const int64_t last = small % (2 * cus), full = t.full + t.full_k * ks, half = t.half + t.half_k * ks;
-  return small / (2 * cus) * full + (last > cus ? full : last > 0 ? half : 0) <
-         (big + cus - 1) / cus * (t.big + t.big_k * ks);
+  const int64_t tt = (T + 255) / 256, tn = (N + 255) / 256, rounds = tn * tt / cus;
+  const int64_t big = t.big + t.big_k * ks, full = t.full + t.full_k * ks, half = t.half + t.half_k * ks;
+  auto small = [&](int64_t rows) {
+    const int64_t n = ((rows + 127) / 128) * ((T + 127) / 128), last = n % (2 * cus);
+    return n / (2 * cus) * full + (last > cus ? full : last > 0 ? half : 0);
+  };
+  int64_t best = (tn * tt + cus - 1) / cus * big, cols = tn;
+  if (small(N) < best) best = small(N), cols = 0;
+  const int64_t part = rounds * cus / tt, second_launch = 3500;
+  if (rounds > 0 && part < tn && rounds * big + small(N - 256 * part) + second_launch < best) cols = part;
+  return (int)cols;
 }
 
 inline hipError_t set_lds(const void* fn, int bytes) {

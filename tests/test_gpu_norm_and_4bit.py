@@ -578,11 +578,12 @@ class _FakeOther:
 @pytest.mark.parametrize("op", ["wkv", "wkv_mx"])
 @pytest.mark.parametrize("T,K,N", [(1500, 256, 20480), (1500, 512, 20476), (300, 768, 20480), (515, 256, 10236),
                                    (4096, 512, 5116), (1500, 384, 20476), (1500, 128, 20480), (300, 640, 20480),
-                                   (515, 128, 10236), (4096, 384, 5116), (515, 1024, 20480), (515, 1152, 20476)])
+                                   (515, 128, 10236), (4096, 384, 5116), (515, 1024, 20480), (515, 1152, 20476),
+                                   (4000, 4096, 5116), (4000, 4224, 5120)])
 def test_mxfp4_many_tiles(op, T, K, N):
     """Many tiles, ragged in T and N, with and without a half chunk at K's end:
-    128x128, on 256 compute units 256x256 in the last two (and the second with
-    bf16 x); a token from every tile and some more."""
+    128x128, on 256 compute units 256x256 in those of 515 tokens and K past 1000
+    (and the second with bf16 x), both in the last two; a token from every tile and some more."""
     E = _E()
     rng = np.random.default_rng(K)
     wq, ws = mxfp4_weight(rng, N, K)
@@ -602,10 +603,10 @@ def test_mxfp4_many_tiles(op, T, K, N):
 
 
 @pytest.mark.parametrize("T,K,N", [(65, 128, 32), (70, 384, 96), (130, 256, 160), (257, 2048, 2080), (300, 640, 1280),
-                                   (515, 512, 20480), (515, 896, 20480), (700, 4224, 20448)])
+                                   (515, 512, 20480), (515, 896, 20480), (700, 4224, 20448), (4000, 4224, 5088)])
 def test_wkv_mx_mxfp8_weight_tiles(T, K, N):
     """MXFP8 weights past the GEMV: 128x128 tiles in the first five, 256x256 in
-    the others (on 256 compute units), with and without a half pair of slices at
+    the next three, both in the last (on 256 compute units), with and without a half pair of slices at
     K's end, ragged in T and N."""
     E = _E()
     rng = np.random.default_rng(T + K)
