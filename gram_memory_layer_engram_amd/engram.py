@@ -27,6 +27,12 @@ _i64 = ctypes.c_int64
 _f32 = ctypes.c_float
 _sz = ctypes.c_size_t
 
+# names of the calls that count in single tokens, looked up once
+_BF16, _U8 = torch.bfloat16, torch.uint8
+_empty_strided = torch.empty_strided
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
 
 class ForwardArgs(ctypes.Structure):
     """Mirror of ``engram_forward_args``."""
@@ -174,7 +180,7 @@ def _format(w: torch.Tensor, w_scales, K: int) -> int:
 
 
 def _check_mxfp4(w: torch.Tensor, w_scales: torch.Tensor, N: int, K: int) -> None:
-    if (w.dtype != torch.uint8 or w_scales.dtype != torch.uint8 or w_scales.shape != (N, K // 32)
+    if (w.dtype != _U8 or w_scales.dtype != _U8 or w_scales.shape != (N, K // 32)
             or not w_scales.is_contiguous()):
         raise ValueError("MXFP4 wkv needs uint8 codes [N, K/2] and contiguous uint8 scales [N, K/32]")
 
@@ -264,17 +270,25 @@ def wkv(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor | None = None,
     """kv = bf16(x . W^T). ``w_scales`` given: MXFP8 (w = uint8 codes [N, K],
     scales [N/32, K/32]) or MXFP4 (w = uint8 packed codes [N, K/2], scales
     [N, K/32]), told apart by w's shape."""
-    L = load_library()
+    L = _lib or load_library()
     if not x.is_contiguous() or not w.is_contiguous():
         raise ValueError("x and w must be contiguous")
     T, K = x.shape
-    N = w.shape[0]
-    if w_scales is not None and w.dim() == 2 and 2 * w.shape[1] == K:
+    wshape = w.shape
+    N = wshape[0]
+    if w_scales is not None and len(wshape) == 2 and 2 * wshape[1] == K:
         _check_mxfp4(w, w_scales, N, K)
-        if x.dtype != torch.bfloat16:
+        if x.dtype != _BF16:
             raise ValueError("MXFP4 wkv needs bf16 x (wkv_mx takes MXFP8 activations)")
+        dev = x.get_device()
+        kv = _product_out(dev, w, w_scales, T, N, kv)
         # no workspace in this format
-        return _product(L.engram_wkv, (x.data_ptr(),), x.get_device(), T, K, w, w_scales, W_MXFP4, N, kv, (None, 0))
+        args = (x.data_ptr(), T, K, w.data_ptr(), w_scales.data_ptr(), W_MXFP4, N, kv.data_ptr(), None, 0)
+        if dev != _current_device():
+            _run_on(dev, L.engram_wkv, *args)
+        elif status := L.engram_wkv(*args, _raw_stream(dev)):
+            _check(status)
+        return kv
     fmt = W_BF16 if w_scales is None else W_MXFP8
     if w.dim() != 2 or w.shape[1] != K:
         raise ValueError(f"w must be [N, {K}], got {tuple(w.shape)}")
@@ -295,25 +309,16 @@ def wkv(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor | None = None,
     return kv
 
 
-def _product(fn, xp, dev, T, K, w, w_scales, fmt, N, kv, tail=()):
-    """Output and call of a projection whose operands are checked; xp: x's
-    address, or those of its codes and scales; dev: its device; tail: arguments
-    past kv."""
+def _product_out(dev, w, w_scales, T, N, kv):
+    """kv of a projection, allocated if not given; all on x's device dev."""
     if w.get_device() != dev or w_scales.get_device() != dev or dev < 0:
         _device_of(w, w_scales)
         raise ValueError("x and w are on different devices")
     if kv is None:
         # empty_strided is the cheapest allocation by half a microsecond
-        kv = torch.empty_strided((T, N), (N, 1), dtype=torch.bfloat16, device=w.device)
-    elif kv.shape != (T, N) or kv.dtype != torch.bfloat16 or not kv.is_contiguous() or kv.get_device() != dev:
+        return _empty_strided((T, N), (N, 1), dtype=_BF16, device=w.device)
+    if kv.shape != (T, N) or kv.dtype != _BF16 or not kv.is_contiguous() or kv.get_device() != dev:
         raise ValueError(f"kv must be bf16 [{T}, {N}], contiguous, on x's device")
-    if dev == torch._C._cuda_getDevice():
-        status = fn(*xp, T, K, w.data_ptr(), w_scales.data_ptr(), fmt, N, kv.data_ptr(), *tail,
-                    torch._C._cuda_getCurrentRawStream(dev))
-        if status:
-            _check(status)
-    else:
-        _run_on(dev, fn, *xp, T, K, w.data_ptr(), w_scales.data_ptr(), fmt, N, kv.data_ptr(), *tail)
     return kv
 
 
@@ -322,11 +327,9 @@ def wkv_mx(xq: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, w_scales: torch.
     """kv = bf16(deq(xq, xs) . deq(W)^T): the projection from MXFP8 activations
     (uint8 codes [T, K], E8M0 bytes [T, K/32], as mx_quantize or add_rms_norm
     give them), W in MXFP8 or MXFP4 as in ``wkv``."""
-    L = load_library()
-    u8 = torch.uint8
-    if not (xq.dtype == u8 and xs.dtype == u8 and w.dtype == u8 and w_scales.dtype == u8 and xq.is_contiguous()
-            and xs.is_contiguous() and w.is_contiguous() and w_scales.is_contiguous() and xq.dim() == 2
-            and w.dim() == 2):
+    L = _lib or load_library()
+    if not (xq.dtype == xs.dtype == w.dtype == w_scales.dtype == _U8 and xq.is_contiguous() and xs.is_contiguous()
+            and w.is_contiguous() and w_scales.is_contiguous()):
         raise ValueError("xq, xs, w and w_scales must be contiguous uint8 matrices")
     T, K = xq.shape
     N, KW = w.shape
@@ -339,9 +342,16 @@ def wkv_mx(xq: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, w_scales: torch.
     else:
         raise ValueError(f"w must be [N, {K}] with scales [N/32, {K // 32}] (MXFP8) or [N, {K // 2}] with "
                          f"[N, {K // 32}] (MXFP4)")
-    if xq.get_device() != xs.get_device():
+    dev = xq.get_device()
+    if dev != xs.get_device():
         raise ValueError("xq and xs are on different devices")
-    return _product(L.engram_wkv_mx, (xq.data_ptr(), xs.data_ptr()), xq.get_device(), T, K, w, w_scales, fmt, N, kv)
+    kv = _product_out(dev, w, w_scales, T, N, kv)
+    args = (xq.data_ptr(), xs.data_ptr(), T, K, w.data_ptr(), w_scales.data_ptr(), fmt, N, kv.data_ptr())
+    if dev != _current_device():
+        _run_on(dev, L.engram_wkv_mx, *args)
+    elif status := L.engram_wkv_mx(*args, _raw_stream(dev)):
+        _check(status)
+    return kv
 
 
 def add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None = None, weight: torch.Tensor | None = None,
@@ -358,7 +368,7 @@ def add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None = None, weight: 
     dimension). weight: bf16 [dim], or [hc, dim] with one row per copy. The
     outputs may be given (contiguous); residual_out may be residual itself and
     out may be x itself."""
-    L = load_library()
+    L = _lib or load_library()
     shape = x.shape
     if len(shape) == 3:
         T, hc, dim = shape
@@ -371,7 +381,7 @@ def add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None = None, weight: 
     dev = x.get_device()
     if dev < 0:
         raise ValueError("libengram takes device tensors only")
-    bf16, u8, device = torch.bfloat16, torch.uint8, x.device
+    bf16, u8, device = _BF16, _U8, x.device
     dense = (hc * dim, dim, 1) if len(shape) == 3 else (dim, 1)
     if x.dtype != bf16 or (xsd != 1 and dim > 1):
         raise ValueError("x must be bf16, contiguous in its last dimension")
@@ -390,7 +400,7 @@ def add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None = None, weight: 
             _device_of(x, residual)
         rp, rst, rsh = residual.data_ptr(), rstride[0], rstride[1] if len(shape) == 3 else 0
         if residual_out is None:
-            residual_out = torch.empty_strided(shape, dense, dtype=bf16, device=device)
+            residual_out = _empty_strided(shape, dense, dtype=bf16, device=device)
             rop = residual_out.data_ptr()
         else:
             rop = given(residual_out, "residual_out", bf16, shape)
@@ -412,7 +422,7 @@ def add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None = None, weight: 
         if out_format != "bf16" and out_format != "both":
             raise ValueError('out_format must be "bf16", "mxfp8" or "both"')
         if out is None:
-            out = torch.empty_strided(shape, dense, dtype=bf16, device=device)
+            out = _empty_strided(shape, dense, dtype=bf16, device=device)
             op = out.data_ptr()
         else:
             op = given(out, "out", bf16, shape)
@@ -420,14 +430,14 @@ def add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None = None, weight: 
         raise ValueError('out is not written with out_format "mxfp8"')
     if out_format != "bf16":
         if xq is None:
-            xq = torch.empty_strided(shape, dense, dtype=u8, device=device)
+            xq = _empty_strided(shape, dense, dtype=u8, device=device)
             qp = xq.data_ptr()
         else:
             qp = given(xq, "xq", u8, shape)
         nb = dim // 32
         scales = (T, hc, nb) if len(shape) == 3 else (T, nb)
         if xs is None:
-            xs = torch.empty_strided(scales, (hc * nb, nb, 1) if len(shape) == 3 else (nb, 1), dtype=u8, device=device)
+            xs = _empty_strided(scales, (hc * nb, nb, 1) if len(shape) == 3 else (nb, 1), dtype=u8, device=device)
             sp = xs.data_ptr()
         else:
             sp = given(xs, "xs", u8, scales)
@@ -438,14 +448,11 @@ def add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None = None, weight: 
         xst = rst = 0
     if hc <= 1:
         xsh = rsh = 0
-    if dev == torch._C._cuda_getDevice():
-        status = L.engram_add_rms_norm(x.data_ptr(), xst, xsh, rp, rst, rsh, wp, whc, T, hc, dim, eps, rop, op, qp, sp,
-                                       torch._C._cuda_getCurrentRawStream(dev))
-        if status:
-            _check(status)
-    else:
-        _run_on(dev, L.engram_add_rms_norm, x.data_ptr(), xst, xsh, rp, rst, rsh, wp, whc, T, hc, dim, eps, rop, op,
-                qp, sp)
+    args = (x.data_ptr(), xst, xsh, rp, rst, rsh, wp, whc, T, hc, dim, eps, rop, op, qp, sp)
+    if dev != _current_device():
+        _run_on(dev, L.engram_add_rms_norm, *args)
+    elif status := L.engram_add_rms_norm(*args, _raw_stream(dev)):
+        _check(status)
     return residual_out, out, xq, xs
 
 
