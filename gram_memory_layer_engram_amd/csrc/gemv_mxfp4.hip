@@ -34,11 +34,12 @@
 // wave: it waits for its own DMAs only, no barrier in the loop.
 //
 // Measured (N 20480, K 2048, 22.3 MB of weight; graph replay, about 2.5 us of
-// it an empty kernel's): x bf16, T 1 / 16 / 32 / 61 in 7.0 / 7.3 / 9.0 / 12.2 us
-// (fragments straight from memory: 9.0 / 10.5 / 12.9 / 17), x MXFP8 6.2 / 6.4 /
-// 7.7 / 9.8 us. Up to 16 tokens the weight's stream bounds it (5 TB/s past the
-// launch); beyond 32, x: 256 workgroups read its 250 KB (bf16, T 61) each from
-// L2, three times the weight's bytes.
+// it an empty kernel's): x bf16, T 1 / 16 / 32 / 48 / 61 in 7.0 / 7.3 / 9.0 /
+// 10.8 / 12.2 us (fragments straight from memory, T 1 / 16 / 32 / 61: 9.0 /
+// 10.5 / 12.9 / 17), x MXFP8 6.2 / 6.4 / 7.7 / 8.8 / 9.8 us. Up to 16 tokens the
+// weight's stream bounds it (5 TB/s past the launch); beyond 32, x: 256
+// workgroups read its 250 KB (bf16, T 61) each from L2, three times the
+// weight's bytes.
 #include <algorithm>
 
 #include "common.h"
@@ -72,8 +73,9 @@ struct Gemv4Args {
   int T, K, N;
 };
 
-// x moves in units of JG token tiles of one k step, UPS units a step.
-constexpr int f4_jg(bool a8, int nt) { return a8 || nt < 2 ? nt : 2; }
+// x moves in units of JG token tiles of one k step, UPS units a step (four bf16
+// tiles, 16 KB, would leave LDS for 7 waves at most).
+constexpr int f4_jg(bool a8, int nt) { return !a8 && nt == 4 ? 2 : nt; }
 constexpr int f4_ups(bool a8, int nt) { return nt / f4_jg(a8, nt); }
 // W steps in the ring when XS units of x are (two units a step: one at a time)
 constexpr int f4_dw(bool a8, int nt, int xs) { return f4_ups(a8, nt) == 1 ? xs : 1; }
@@ -325,8 +327,14 @@ bool gemv_mxfp4_supported(int64_t T, int K, bool x_mxfp8) {
 hipError_t launch_gemv_mxfp4(const void* x, const uint8_t* xs, int64_t T, int K, const void* w, const uint8_t* ws,
                              int N, void* kv, hipStream_t s) {
   const Gemv4Args a{x, xs, (const uint8_t*)w, ws, (uint16_t*)kv, (int)T, K, N};
-  if (xs) return T <= 16 ? f4_small<true, 1>(a, s) : T <= 32 ? f4_small<true, 2>(a, s) : f4_large<true, 4, 4, 2>(a, s);
-  return T <= 16 ? f4_small<false, 1>(a, s) : T <= 32 ? f4_large<false, 2, 8, 1>(a, s) : f4_large<false, 4, 8, 1>(a, s);
+  if (xs)
+    return T <= 16 ? f4_small<true, 1>(a, s) : T <= 32 ? f4_small<true, 2>(a, s)
+         : T <= 48 ? f4_large<true, 3, 4, 2>(a, s) : f4_large<true, 4, 4, 2>(a, s);
+  if (T <= 16) return f4_small<false, 1>(a, s);
+  if (T <= 32) return f4_large<false, 2, 8, 1>(a, s);
+  // three tiles in one unit a step: T 48 12.2 -> 10.8 us (MXFP8 x 9.3 -> 8.8)
+  if (T <= 48 && f4_lds(false, 1, 3, 8, 1, K / 32) <= kLds) return f4_large<false, 3, 8, 1>(a, s);
+  return f4_large<false, 4, 8, 1>(a, s);
 }
 
 }  // namespace engram

@@ -234,11 +234,12 @@ def test_norm_codes_match_the_quantizer_where_y_is_bf16():
     assert (a == b)[keep].mean() > 0.95
 
 
-KN = [(128, 4), (256, 64), (384, 100), (4096, 36), (8192, 20), (2048, 272), (4224, 96), (1024, 20480 // 8), (640, 1284), (2560, 5 * 16 * 3 + 36)]
+KN = [(128, 4), (256, 64), (384, 100), (4096, 36), (8192, 20), (2048, 272), (4224, 96), (1024, 20480 // 8), (640, 1284),
+      (2560, 5 * 16 * 3 + 36), (512, 20476), (384, 10236)]
 
 
 @pytest.mark.parametrize("K,N", KN)
-@pytest.mark.parametrize("T", [1, 2, 7, 16, 17, 33, 50, 64, 65, 130, 300])
+@pytest.mark.parametrize("T", [1, 2, 7, 16, 17, 33, 48, 50, 64, 65, 130, 300])
 def test_mxfp4_products(T, K, N):
     E = _E()
     _say(f"mxfp4 products T {T} K {K} N {N}")
