@@ -171,12 +171,22 @@ def _stream() -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
-def _format(w: torch.Tensor, w_scales, K: int) -> int:
-    """The wkv weight format by its tensors: bf16 [N, K] without scales,
-    MXFP8 codes [N, K], or MXFP4 codes [N, K/2]."""
+def _format(w: torch.Tensor, w_scales, N: int, K: int) -> int:
+    """The wkv weight format by its tensors: bf16 [N, K] without scales, MXFP8
+    codes [N, K] with scales [N/32, K/32], or MXFP4 codes [N, K/2] with scales
+    [N, K/32]. The kernels read all of them: anything else is refused."""
+    shape = w.shape
+    if w_scales is not None and shape == (N, K // 2):
+        _check_mxfp4(w, w_scales, N, K)
+        return W_MXFP4
+    if shape != (N, K) or w.element_size() != (2 if w_scales is None else 1):
+        raise ValueError(f"w must be bf16 [{N}, {K}], codes [{N}, {K}] with scales [{N // 32}, {K // 32}] (MXFP8) or "
+                         f"[{N}, {K // 2}] with [{N}, {K // 32}] (MXFP4), got {w.dtype} {tuple(shape)}")
     if w_scales is None:
         return W_BF16
-    return W_MXFP4 if w.dim() == 2 and 2 * w.shape[1] == K else W_MXFP8
+    if w_scales.shape != (N // 32, K // 32) or w_scales.element_size() != 1 or not w_scales.is_contiguous():
+        raise ValueError(f"MXFP8 wkv needs contiguous scales [{N // 32}, {K // 32}], one byte each")
+    return W_MXFP8
 
 
 def _check_mxfp4(w: torch.Tensor, w_scales: torch.Tensor, N: int, K: int) -> None:
@@ -469,13 +479,7 @@ def wkv_gate_partials(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor |
     T, K = x.shape
     _, hc, dim = hidden.shape
     N = (hc + 1) * dim
-    fmt = _format(w, w_scales, K)
-    if tuple(w.shape) != (N, K // 2 if fmt == W_MXFP4 else K):
-        raise ValueError(f"w must be [{N}, {K}] (MXFP4: [{N}, {K // 2}]), got {tuple(w.shape)}")
-    if fmt == W_MXFP4:
-        _check_mxfp4(w, w_scales, N, K)
-    if fmt == W_MXFP8:
-        _dense(w_scales, "w_scales")
+    fmt = _format(w, w_scales, N, K)
     if value is None:
         value = torch.empty((T, dim), dtype=torch.bfloat16, device=x.device)
     if partials is None:
@@ -539,9 +543,7 @@ def forward_args(table, hash_ids, w, w_scales, hidden, q_weight, k_weight, token
     a.ids_stride_t = hash_ids.stride(0); a.ids_stride_c = hash_ids.stride(1)
     a.w = _ptr(w); a.w_scales = _ptr(w_scales)
     K = hash_ids.shape[1] * table.shape[1]
-    a.w_format = _format(w, w_scales, K)
-    if a.w_format == W_MXFP4:
-        _check_mxfp4(w, w_scales, (hc + 1) * dim, K)
+    a.w_format = _format(w, w_scales, (hc + 1) * dim, K)
     a.hidden = _ptr(hidden); a.q_weight = _ptr(q_weight); a.k_weight = _ptr(k_weight)
     a.token_mask = _ptr(token_mask)
     a.T = T; a.hc = hc; a.dim = dim
