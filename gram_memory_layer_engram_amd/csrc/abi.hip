@@ -94,10 +94,10 @@ inline bool meet(const Span& a, const Span& b) {
   return x && y && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
 }
 
-// Whether kv lies on an operand (the tiles that come later would read it).
-bool kv_on_operand(const void* kv, int64_t T, int64_t K, int64_t N, const void* x, int64_t x_bytes, const uint8_t* xs,
-                   const void* w, const uint8_t* w_scales, int32_t w_format) {
-  const Span o{kv, 2 * T * N};
+// Whether an output lies on an operand of a product (the tiles that come later
+// would read it).
+bool on_operand(const Span& o, int64_t T, int64_t K, int64_t N, const void* x, int64_t x_bytes, const uint8_t* xs,
+                const void* w, const uint8_t* w_scales, int32_t w_format) {
   const bool f4 = w_format == ENGRAM_W_MXFP4;
   return meet(o, {x, x_bytes}) || meet(o, {xs, T * K / 32}) || meet(o, {w, f4 ? N * K / 2 : N * K}) ||
          meet(o, {w_scales, f4 ? N * K / 32 : N * K / 1024});
@@ -285,6 +285,15 @@ int engram_wkv_gate_partials(const void* x, int64_t T, int32_t K, const void* w,
   if (st != ENGRAM_OK) return st;
   if (T == 0) return ENGRAM_OK;
   if (!partials || ((uintptr_t)partials & 7u)) return ENGRAM_EINVAL;
+  if (w_format == ENGRAM_W_MXFP4) {
+    const int64_t n = T * hc * dim;
+    const Span outs[2] = {{value, 2 * T * dim}, {partials, n / 256 * 8}};
+    if (meet(outs[0], outs[1])) return ENGRAM_EINVAL;
+    for (const Span& o : outs)
+      if (on_operand(o, T, K, N, x, 2 * T * K, nullptr, w, w_scales, w_format) || meet(o, {hidden, 2 * n}) ||
+          meet(o, {q_weight, (int64_t)2 * hc * dim}) || meet(o, {k_weight, (int64_t)2 * hc * dim}))
+        return ENGRAM_EINVAL;
+  }
   const size_t need = engram_wkv_workspace_size(T, K, N, w_format);
   if (workspace_bytes < need || (need && (!workspace || ((uintptr_t)workspace % kAlign))))
     return ENGRAM_EINVAL;
@@ -298,7 +307,7 @@ int engram_wkv(const void* x, int64_t T, int32_t K, const void* w,
                void* workspace, size_t workspace_bytes, void* stream) {
   int st = check_wkv(x, T, K, w, w_scales, w_format, N, kv);
   if (st != ENGRAM_OK || T == 0) return st;
-  if (w_format == ENGRAM_W_MXFP4 && kv_on_operand(kv, T, K, N, x, 2 * T * K, nullptr, w, w_scales, w_format))
+  if (w_format == ENGRAM_W_MXFP4 && on_operand({kv, 2 * T * N}, T, K, N, x, 2 * T * K, nullptr, w, w_scales, w_format))
     return ENGRAM_EINVAL;
   const size_t need = engram_wkv_workspace_size(T, K, N, w_format);
   if (workspace_bytes < need || (need && (!workspace || ((uintptr_t)workspace % kAlign))))
@@ -313,7 +322,7 @@ int engram_wkv_mx(const uint8_t* xq, const uint8_t* xs, int64_t T, int32_t K, co
   if (w_format == ENGRAM_W_BF16) return ENGRAM_EUNSUPPORTED;
   if (T == 0) return ENGRAM_OK;
   if (!xs || !aligned16(xs)) return ENGRAM_EINVAL;
-  if (kv_on_operand(kv, T, K, N, xq, T * K, xs, w, w_scales, w_format)) return ENGRAM_EINVAL;
+  if (on_operand({kv, 2 * T * N}, T, K, N, xq, T * K, xs, w, w_scales, w_format)) return ENGRAM_EINVAL;
   hipStream_t s = (hipStream_t)stream;
   if (w_format == ENGRAM_W_MXFP8)
     return hip_status(run_mx_projection(xq, xs, T, K, w, w_scales, N, kv, s, kPlainStore));

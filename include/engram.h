@@ -277,7 +277,8 @@ int engram_add_rms_norm(const void* x, int64_t x_stride_t, int64_t x_stride_h, c
  *   partials    fp32 [hc, T, dim/256, 2], 8-byte aligned
  *   workspace   engram_wkv_workspace_size(T, K, (hc+1)*dim, w_format) bytes
  *   Errors: ENGRAM_EINVAL for hc or dim <= 0, a NULL or misaligned pointer,
- *   or a short workspace; T = 0 is a no-op. Asynchronous on `stream`.
+ *   or a short workspace; with MXFP4 weights, value or partials on an operand
+ *   or on each other; T = 0 is a no-op. Asynchronous on `stream`.
  *   Shapes: as engram_wkv, plus dim % 256 == 0 and 1 <= hc <= 8; other
  *   shapes return ENGRAM_EUNSUPPORTED. This always runs the tiled GEMM
  *   (engram_wkv may take a GEMV for T <= 64).
