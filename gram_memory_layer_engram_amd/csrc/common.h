@@ -51,6 +51,12 @@ __device__ __forceinline__ uint32_t fp4_pair_to_bf16(uint32_t codes, float scale
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, B));
 }
 
+// LDS of a compute unit. A kernel that may need more than the default 64 KiB of
+// dynamic LDS has its limit set to all of it, whatever the call needs: the limit
+// is the kernel's, so one that followed a call could be lowered by another
+// thread's smaller call between that and the launch.
+constexpr int kLds = 160 * 1024;
+
 // Device properties the launchers need (cached per device by the ABI layer).
 struct DevInfo {
   int num_cus;

@@ -264,8 +264,6 @@ __global__ __launch_bounds__(WAVES * 64) void gemv_mxfp4_kernel(
   }
 }
 
-constexpr int kLds = 160 * 1024;
-
 template <bool A8, int RT, int NT, int WAVES, int XS>
 hipError_t f4_launch(const Gemv4Args& a, hipStream_t s) {
   const int lds = f4_lds(A8, RT, NT, WAVES, XS, a.K / 32);
@@ -274,7 +272,7 @@ hipError_t f4_launch(const Gemv4Args& a, hipStream_t s) {
   const bool swap = !A8 && a.K % 4096 == 0;
   const auto fn = swap ? gemv_mxfp4_kernel<A8, RT, NT, WAVES, XS, !A8> : gemv_mxfp4_kernel<A8, RT, NT, WAVES, XS, false>;
   if (lds > 64 * 1024) {   // above the default limit
-    const hipError_t e = hipFuncSetAttribute((const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    const hipError_t e = hipFuncSetAttribute((const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL(fn, dim3((a.N + 16 * RT - 1) / (16 * RT)), dim3(WAVES * 64), lds, s, (const uint8_t*)a.x, a.xs,

@@ -287,7 +287,7 @@ hipError_t gemv_xlds(const uint8_t* xq, const uint8_t* xs, int T, int K, const u
 #define GX_CASE(S)                                                                                     \
   case S:                                                                                              \
     e = hipFuncSetAttribute((const void*)gemv_mxfp8_xlds_kernel<RT, NT, S>,                            \
-                            hipFuncAttributeMaxDynamicSharedMemorySize, lds);                          \
+                            hipFuncAttributeMaxDynamicSharedMemorySize, kLds);                         \
     if (e != hipSuccess) return e;                                                                     \
     hipLaunchKernelGGL((gemv_mxfp8_xlds_kernel<RT, NT, S>), grid, block, lds, s, xq, xs, T, K, w, ws, N, \
                        (uint16_t*)kv);                                                                 \
@@ -328,7 +328,7 @@ hipError_t gemv_nt(const uint8_t* xq, const uint8_t* xs, int T, int K,
   // two or more token tiles: x in LDS when it fits (K % 256 == 0 for the
   // swizzle, at most 2 k steps per wave)
   if constexpr (NT >= 2) {
-    if (tiles % 5 == 0 && K % 256 == 0 && K / 128 <= 2 * GV_WAVES && xlds_bytes<5, NT>(K) <= 160 * 1024)
+    if (tiles % 5 == 0 && K % 256 == 0 && K / 128 <= 2 * GV_WAVES && xlds_bytes<5, NT>(K) <= kLds)
       return gemv_xlds<5, NT>(xq, xs, T, K, w, ws, N, kv, s);
   }
   if constexpr (5 * NT <= 8)
