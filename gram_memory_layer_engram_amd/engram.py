@@ -214,7 +214,15 @@ def _run_on(dev: int, fn, *args) -> None:
     themselves where it is current, with the raw stream number: a Stream object
     costs 2.7 us, a third of a decode call.)"""
     with torch.cuda.device(dev):
-        _check(fn(*args, torch._C._cuda_getCurrentRawStream(dev)))
+        _check(fn(*args, _raw_stream(dev)))
+
+
+def _run(dev: int, fn, *args) -> None:
+    """fn(*args, stream) on device dev's current stream."""
+    if dev != _current_device():
+        _run_on(dev, fn, *args)
+    else:
+        _check(fn(*args, _raw_stream(dev)))
 
 
 def lookup(table, hash_ids: torch.Tensor, rows_out: torch.Tensor | None = None,
@@ -494,9 +502,9 @@ def wkv_gate_partials(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor |
     if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     ws_bytes = 0 if workspace is None else workspace.numel()
-    _check(L.engram_wkv_gate_partials(_ptr(x), T, K, _ptr(w), _ptr(w_scales), fmt, hc, dim, _ptr(hidden),
-                                      _ptr(q_weight), _ptr(k_weight), _ptr(value), _ptr(partials),
-                                      _ptr(workspace), ws_bytes, _stream()))
+    dev = _device_of(x, w, w_scales, hidden, q_weight, k_weight, value, partials, workspace)
+    _run(dev, L.engram_wkv_gate_partials, _ptr(x), T, K, _ptr(w), _ptr(w_scales), fmt, hc, dim, _ptr(hidden),
+         _ptr(q_weight), _ptr(k_weight), _ptr(value), _ptr(partials), _ptr(workspace), ws_bytes)
     return value, partials
 
 
@@ -559,6 +567,12 @@ def forward_args(table, hash_ids, w, w_scales, hidden, q_weight, k_weight, token
     return a
 
 
+def _forward_device(hidden, *tensors) -> int:
+    """The device a forward runs on: that of all its tensors (a host table is
+    mapped into every device)."""
+    return _device_of(hidden, *(t for t in tensors if not isinstance(t, HostTable)))
+
+
 def forward_workspace_size(args: ForwardArgs) -> int:
     return load_library().engram_forward_workspace_size(ctypes.byref(args))
 
@@ -586,7 +600,9 @@ def forward(table, hash_ids, w, w_scales, hidden, q_weight, k_weight, token_mask
         workspace = new_forward_workspace(need, hidden.device)
     ws_bytes = 0 if workspace is None else workspace.numel()
     fn = L.engram_forward_single_launch if single_launch else L.engram_forward
-    _check(fn(ctypes.byref(args), _ptr(workspace), ws_bytes, _stream()))
+    dev = _forward_device(hidden, table, hash_ids, w, w_scales, q_weight, k_weight, token_mask, out, gate_out, err_flag,
+                          workspace, table_scales)
+    _run(dev, fn, ctypes.byref(args), _ptr(workspace), ws_bytes)
     return out
 
 
@@ -605,7 +621,9 @@ def forward_noalloc(table, hash_ids, w, w_scales, hidden, q_weight, k_weight, to
         out = torch.empty_like(hidden)
     args = forward_args(table, hash_ids, w, w_scales, hidden, q_weight, k_weight, token_mask,
                         eps, clamp, out, gate_out, err_flag, table_scales, store_kv)
-    _check(L.engram_forward_noalloc(ctypes.byref(args), _stream()))
+    dev = _forward_device(hidden, table, hash_ids, w, w_scales, q_weight, k_weight, token_mask, out, gate_out, err_flag,
+                          table_scales)
+    _run(dev, L.engram_forward_noalloc, ctypes.byref(args))
     return out
 
 
@@ -640,14 +658,19 @@ class ForwardPlan:
         if workspace is None and need:
             workspace = new_forward_workspace(need, hidden.device)
         self.workspace = workspace
+        self._dev = _forward_device(hidden, *self._keep, out, workspace)
         self._ws = _ptr(workspace)
         self._ws_bytes = 0 if workspace is None else workspace.numel()
         self._argp = ctypes.byref(self.args)
         self._fn = L.engram_forward_single_launch if single_launch else L.engram_forward
-        self._stream = (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+        self._stream = (torch.cuda.current_stream(self._dev) if stream is None else stream).cuda_stream
 
     def run(self):
-        status = self._fn(self._argp, self._ws, self._ws_bytes, self._stream)
+        if self._dev != _current_device():
+            with torch.cuda.device(self._dev):
+                status = self._fn(self._argp, self._ws, self._ws_bytes, self._stream)
+        else:
+            status = self._fn(self._argp, self._ws, self._ws_bytes, self._stream)
         if status:
             _check(status)
         return self.out
