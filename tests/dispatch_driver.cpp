@@ -52,6 +52,7 @@ std::string plain_name(const char* mangled) {
   if (at != std::string::npos) s = s.substr(at + head.size());
   s = s.substr(0, s.find('('));
   for (size_t i; (i = s.find(", ")) != std::string::npos;) s.erase(i + 1, 1);
+  for (char& c : s) c = c == ' ' ? '_' : c;
   return s;
 }
 
