@@ -181,14 +181,14 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
         const int x0 = kk * NT + q - (NT == 4);   // x: one each from (kk 0, q 1 or 0) on
         const bool dx = x0 >= 0 && x0 < NDMA;
         if (dx) dma_x(sb2, kx, x0);
-        if (q < NT) read_x(sb, kk + 1, (kk + 1) & 1, q);
+        read_x(sb, kk + 1, (kk + 1) & 1, q);
         convert(kk + 1, (kk + 1) & 1, q);
         mfma_row(kk & 1, q);
         SGB(SG_MFMA, 1);
         if (dw) SGB(SG_VMEM, 1);
         if (dx) SGB(SG_VMEM, 1);
         if (NT == 4) { SGB(SG_MFMA, 1); SGB(SG_DSR, 1); SGB(SG_MFMA, 1); SGB(SG_VALU, 4); SGB(SG_MFMA, 1); }
-        else { if (q < NT) SGB(SG_DSR, 1); SGB(SG_VALU, 4); SGB(SG_MFMA, 1); }
+        else { SGB(SG_DSR, 1); SGB(SG_VALU, 4); SGB(SG_MFMA, 1); }
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -215,13 +215,11 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
     next_w();
     if constexpr (NT == 4) {
       mfma_row(1, 1);
-      if (NT == 4) { SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 2); }
-      else { SGB(SG_MFMA, 1); SGB(SG_DSR, 4); SGB(SG_MFMA, 1); }
+      SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 2);
       __builtin_amdgcn_sched_barrier(0);
       next_x();
       mfma_row(1, 2);
-      if (NT == 4) { SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 2); }
-      else { SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); }
+      SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 2);
       __builtin_amdgcn_sched_barrier(0);
     } else {
       next_x();
@@ -232,8 +230,6 @@ void gemm_fp4_bf16_kernel(const uint16_t* __restrict__ x, int T, int K, const ui
     if (NT == 4) {
       SGB(SG_MFMA, 1); SGB(SG_VALU, 5); SGB(SG_MFMA, 1); SGB(SG_VALU, 5); SGB(SG_MFMA, 1); SGB(SG_VALU, 5);
       SGB(SG_MFMA, 1);
-    } else if (NT == 4) {
-      SGB(SG_MFMA, 1); SGB(SG_VALU, 8); SGB(SG_MFMA, 1);
     }
     if (PAR == 3) {
 #pragma unroll
@@ -301,7 +297,7 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       a8[i] = __builtin_amdgcn_raw_buffer_load_b64(rsa, arow[i] + 8u * (uint32_t)c, 0, 0);
-      if (i < NT) b8[i] = __builtin_amdgcn_raw_buffer_load_b64(rsb, brow[i] + 8u * (uint32_t)c, 0, 0);
+      b8[i] = __builtin_amdgcn_raw_buffer_load_b64(rsb, brow[i] + 8u * (uint32_t)c, 0, 0);
     }
   };
   const uint32_t lsh = (uint32_t)lg * 8u;
@@ -359,10 +355,8 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
   for (int i = 0; i < NT; ++i) {
     a[i] = wfrag(0, 0, i);
     sa[i] = pick(sa8[i], 0);
-    if (i < NT) {
-      b[i] = xfrag(XBASE, 0, i);
-      sb[i] = pick(sb8[i], 0);
-    }
+    b[i] = xfrag(XBASE, 0, i);
+    sb[i] = pick(sb8[i], 0);
   }
 
   int xb = 0;   // d % (LA + 1)
@@ -388,7 +382,7 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
         for (int k = 0; k < NDMA / NT; ++k) dma_x(s_x2, kx, NDMA / NT * q + k);
       }
       na[q] = wfrag(wslot(c), 2 * PAR + 1, q);
-      if (q < NT) nb[q] = xfrag(s_x, 1, q);
+      nb[q] = xfrag(s_x, 1, q);
       mfma_row(q);
       if (NT == 4) {
         SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_DSR, 1); SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_DSR, 1);
@@ -401,10 +395,8 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
     for (int i = 0; i < NT; ++i) {
       a[i] = na[i];
       sa[i] = pick(sa8[i], 2 * PAR + 1);
-      if (i < NT) {
-        b[i] = nb[i];
-        sb[i] = pick(sb8[i], 2 * PAR + 1);
-      }
+      b[i] = nb[i];
+      sb[i] = pick(sb8[i], 2 * PAR + 1);
     }
     // stage 1; the barrier that publishes slice d+1 after half its row blocks
 #pragma unroll
@@ -435,7 +427,7 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
 #pragma unroll
       for (int i = 2 * q - NT; i < 2 * q - NT + 2; ++i) {
         na[i] = wfrag(sw1, u1, i);
-        if (i < NT) nb[i] = xfrag(s_x1, 0, i);
+        nb[i] = xfrag(s_x1, 0, i);
       }
       mfma_row(q);
       if (NT == 4) {
@@ -450,11 +442,9 @@ void gemm_fp4_mx_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restric
       a[i] = na[i];
       if (PAR == 1) sa8[i] = na8[i];
       sa[i] = pick(sa8[i], u1);
-      if (i < NT) {
-        b[i] = nb[i];
-        if (PAR == 1) sb8[i] = nb8[i];
-        sb[i] = pick(sb8[i], u1);
-      }
+      b[i] = nb[i];
+      if (PAR == 1) sb8[i] = nb8[i];
+      sb[i] = pick(sb8[i], u1);
     }
     xb = xb + 1 > LA ? 0 : xb + 1;
   };
