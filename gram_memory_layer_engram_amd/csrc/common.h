@@ -157,7 +157,7 @@ bool gemv_bf16_supported(int64_t T, int K, int N);
 hipError_t launch_gemv_bf16(const void* x, int64_t T, int K, const void* w, int N, void* kv, hipStream_t s);
 
 // Small-batch projection with MXFP4 weights: whether it takes (T, K) (T <=
-// kGemvMaxT, and a tile's scale bytes fit LDS: K up to 36000 at least), and
+// kGemvMaxT, and a tile's scale bytes fit LDS: K up to 35840 at least), and
 // its launch (K % 128 == 0, N % 4 == 0): x bf16, or MXFP8 codes when xs (E8M0
 // [T, K/32]) is not null.
 bool gemv_mxfp4_supported(int64_t T, int K, bool x_mxfp8);

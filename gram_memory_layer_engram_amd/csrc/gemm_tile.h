@@ -232,8 +232,8 @@ __device__ __forceinline__ void store_tile(f32x16 (&acc)[NT][NT], char* smem, ui
 // 128x128 ones (a second launch): by the rounds that each needs and a round's
 // time, an offset (launch, first DMAs, epilogue) and so much a 128-k slice. All,
 // none, or as many as fill whole rounds of 256x256 tiles (N 20480, K 4096, T
-// 1000, the 64 of 80, us all / none / split: MXFP4 and bf16 x 167 / 139 / 130,
-// MXFP8 x 101 / 93 / 80, MXFP8 weights 98 / 97 / 84). With two 128x128
+// 1000, the 64 of 80, us all / none / split: MXFP4 and bf16 x 171 / 144 / 134,
+// MXFP8 x 103 / 93 / 82, MXFP8 weights 101 / 97 / 85). With two 128x128
 // workgroups on a compute unit one's epilogue runs beside the other's loop. The
 // times (ns) are fitted to T 65-8192, N 96-35840, K 128-4096 for each kernel; kv
 // is the same bit for bit whatever the tile.

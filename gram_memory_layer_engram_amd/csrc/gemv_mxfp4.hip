@@ -1,5 +1,5 @@
 // Projection with MXFP4 weights for small batches (T <= 64): kv[T, N] =
-// bf16(x . deq(W)^T), x bf16 or MXFP8, fp32 accumulation.
+// bf16(x . deq(W)^T), x bf16 (fp32 sums) or MXFP8 (fp32 but for runs of 8 k).
 //
 // W is e2m1 codes [N, K/2] with one E8M0 byte per row and 32 k [N, K/32] (OCP
 // MX v1.0 MXFP4). With few tokens the product is a stream of the weight
@@ -37,9 +37,10 @@
 // it an empty kernel's): x bf16, T 1 / 16 / 32 / 48 / 61 in 7.0 / 7.3 / 9.0 /
 // 10.8 / 12.2 us (fragments straight from memory, T 1 / 16 / 32 / 61: 9.0 /
 // 10.5 / 12.9 / 17), x MXFP8 6.2 / 6.4 / 7.7 / 8.8 / 9.8 us. Up to 16 tokens the
-// weight's stream bounds it (5 TB/s past the launch); beyond 32, x: 256
-// workgroups read its 250 KB (bf16, T 61) each from L2, three times the
-// weight's bytes.
+// weight's stream bounds it (5 TB/s past the launch). Beyond 32 two things are
+// not told apart: 256 workgroups read x's 250 KB (bf16, T 61) each from L2, three
+// times the weight's bytes, and a wave has one unit of x in flight (bf16: at K
+// 2048 four trips to memory, one after the other).
 #include <algorithm>
 
 #include "common.h"

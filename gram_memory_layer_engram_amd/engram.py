@@ -344,7 +344,8 @@ def wkv_mx(xq: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, w_scales: torch.
            kv: torch.Tensor | None = None) -> torch.Tensor:
     """kv = bf16(deq(xq, xs) . deq(W)^T): the projection from MXFP8 activations
     (uint8 codes [T, K], E8M0 bytes [T, K/32], as mx_quantize or add_rms_norm
-    give them), W in MXFP8 or MXFP4 as in ``wkv``."""
+    give them), W in MXFP8 or MXFP4 as in ``wkv``. Sums are fp32 but for runs of 8
+    k, which the 8-bit matrix instructions add 14 bits deep (include/engram.h)."""
     L = _lib or load_library()
     if not (xq.dtype == xs.dtype == w.dtype == w_scales.dtype == _U8 and xq.is_contiguous() and xs.is_contiguous()
             and w.is_contiguous() and w_scales.is_contiguous()):
