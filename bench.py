@@ -49,20 +49,27 @@ TRAFFIC_FILE = os.path.join(ROOT, "profiles", "traffic.json")
 DECODE_COPIES = 16
 
 
-def _source_sha(rel: str) -> str:
-    with open(os.path.join(ROOT, rel), "rb") as f:
-        return hashlib.sha256(f.read()).hexdigest()[:16]
+# the bf16 GEMM's loop and loads, the epilogue that stores its tiles, its DMA offsets
+GEMM_SOURCES = tuple(f"gram_memory_layer_engram_amd/csrc/{f}" for f in ("gemm.hip", "gemm_tile.h", "gemm_dma.h"))
 
 
-def _traffic(kernel: str, src: str):
+def _source_sha(sources) -> str:
+    h = hashlib.sha256()
+    for rel in sources:
+        with open(os.path.join(ROOT, rel), "rb") as f:
+            h.update(f.read())
+    return h.hexdigest()[:16]
+
+
+def _traffic(kernel: str, sources):
     """HBM bytes per launch from committed rocprofv3 counter runs, if they
-    were taken on the current kernel source; else None."""
+    were taken on the current kernel sources; else None."""
     try:
         with open(TRAFFIC_FILE) as f:
             rec = json.load(f).get(kernel)
     except (OSError, ValueError):
         return None
-    if not rec or rec.get("source_sha") != _source_sha(src):
+    if not rec or rec.get("source_sha") != _source_sha(sources):
         return None
     return rec.get("hbm_bytes_per_launch")
 
@@ -576,7 +583,7 @@ def main():
                   "2048), timed between the forward's lookup and finish launches",
         "bound": "mfma", "achieved": round(achieved, 1), "peak": BF16_PEAK_TFLOPS,
         "unit": "TFLOP/s", "frac": round(achieved / BF16_PEAK_TFLOPS, 4),
-        "traffic": _traffic("gemm_bf16_kernel_gate_epilogue", "gram_memory_layer_engram_amd/csrc/gemm.hip"),
+        "traffic": _traffic("gemm_bf16_kernel_gate_epilogue", GEMM_SOURCES),
         "traffic_unit": "bytes per launch past L2 (rocprofv3 FETCH_SIZE + WRITE_SIZE, each copy-calibrated)",
     }
     # the HBM-bound kernels of the same step, against 8 TB/s
