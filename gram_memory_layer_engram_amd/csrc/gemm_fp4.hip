@@ -23,10 +23,10 @@
 //    the fp8 operand k 16g.. and 32+16g.., and its E8M0 bytes scale k block
 //    [32g, 32g+32) of its own row.
 //
-// Measured at N 20480, K 2048, T 8192: bf16 x 485-510 us (1.35-1.42 PFLOP/s;
+// Measured at N 20480, K 2048, T 8192: bf16 x 485-527 us (1.30-1.42 PFLOP/s;
 // matrix cores busy 68% of the cycles, at the 1.9 GHz that the chip sustains
 // with them busy), against 517 us for the weight expanded to bf16 and
-// multiplied by the bf16 kernel; MXFP8 x 282 us (2.4 PFLOP/s).
+// multiplied by the bf16 kernel; MXFP8 x 282-302 us (2.3-2.4 PFLOP/s).
 #include <type_traits>
 
 #include "gemm_tile.h"
