@@ -316,7 +316,9 @@ hipError_t f4_large(const Gemv4Args& a, hipStream_t s) {
 
 bool gemv_mxfp4_supported(int64_t T, int K, bool x_mxfp8) {
   if (T < 1 || T > kGemvMaxT) return false;
-  const int kb = std::min(K, 1 << 20) / 32;   // the smallest instantiation's LDS
+  // the smallest instantiation's LDS (past 32 tokens of MXFP8 x the four-tile one's,
+  // though up to 48 run three tiles, which K 53248 would fit)
+  const int kb = std::min(K, 1 << 20) / 32;
   if (x_mxfp8) return (T <= 16 ? f4_lds(true, 1, 1, 4, 1, kb) : T <= 32 ? f4_lds(true, 1, 2, 4, 1, kb)
                                                                         : f4_lds(true, 1, 4, 4, 2, kb)) <= kLds;
   return (T <= 16 ? f4_lds(false, 1, 1, 4, 1, kb) : T <= 32 ? f4_lds(false, 1, 2, 8, 1, kb)

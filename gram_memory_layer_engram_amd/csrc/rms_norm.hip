@@ -17,11 +17,11 @@
 // 1 + 1/32 of codes and scale; the weight row comes from L2. 8192 tokens of
 // four streams of 4096 with a residual: MXFP8 output 131-134 us (742 MB, 5.6
 // TB/s; leaving out the quantizer's arithmetic or the scale bytes changes it
-// by 1%), bf16 output 177 us (1.07 GB, 6.1 TB/s). One token: 3.0 us, a launch
-// and one trip to memory. Without profit: workgroups regrouped so that a
-// token's copies share an XCD's L2 (the same time), non-temporal loads of the
-// residual (3% faster on these 268 MB, 17% slower where it lies in the
-// Infinity Cache).
+// by 1%), bf16 output 177 us (1.07 GB, 6.1 TB/s), both 203 us (1.21 GB, 6.0
+// TB/s). One token: 3.0 us, a launch and one trip to memory. Without profit:
+// workgroups regrouped so that a token's copies share an XCD's L2 (the same
+// time), non-temporal loads of the residual (3% faster on these 268 MB, 17%
+// slower where it lies in the Infinity Cache).
 //
 // Layout: a row is owned by TPR threads. Each of its waves takes a contiguous
 // run of P * 64 pieces of 8 elements, lane l the pieces l, 64 + l, .. of the

@@ -148,3 +148,80 @@ def test_norm_codes_at_ties_are_the_quantizers(rows, dim):
     assert torch.equal(s.view(rows, -1), s2) and torch.equal(q.view(rows, dim), q2)
     codes, scale = o.mx_quantize(bits(x.view(rows, dim)))
     assert np.array_equal(u8(s).reshape(rows, -1), scale) and np.array_equal(u8(q).reshape(rows, dim), codes)
+
+
+@pytest.mark.parametrize("T", [3, 40, 70])
+@pytest.mark.parametrize("weights", ["mxfp4", "mxfp8"])
+def test_a_nan_scale_makes_a_block_of_zero_codes_nan(T, weights):
+    """OCP MX: byte 255 makes its whole block NaN, zero codes too, in a weight's
+    scale and in a token's."""
+    E = _E()
+    K, N = 256, 96
+    gen = X.generator(T, DEV)
+    w, s = X.mxfp4_weight(N, K, gen) if weights == "mxfp4" else X.mxfp8_weight(N, K, gen)
+    xq, xs = X.mxfp8_rows(T, K, gen)
+    if weights == "mxfp4":
+        w[9, 32:48], s[9, 2] = 0, 255                # k 64 .. 95 of row 9
+        rows = torch.zeros(N, dtype=torch.bool, device=DEV)
+        rows[9] = True
+        got = E.wkv(X.bf16_rows(T, K, gen), w, s)
+        assert torch.equal(torch.isnan(got), rows.expand(T, N))
+    else:
+        w[32:64, 64:96], s[1, 2] = 0, 255
+        rows = (torch.arange(N, device=DEV) // 32) == 1
+    assert torch.equal(torch.isnan(E.wkv_mx(xq, xs, w, s)), rows.expand(T, N))
+    xq[1, 128:160], xs[1, 4] = 0, 255
+    want = rows.expand(T, N).clone()
+    want[1] = True
+    assert torch.equal(torch.isnan(E.wkv_mx(xq, xs, w, s)), want)
+
+
+@pytest.mark.parametrize("T", [3, 40, 70])
+def test_subnormal_bf16_activations_count(T):
+    """x of 2^-133 .. 2^-127 against weights near fp32's top: nothing is flushed."""
+    E = _E()
+    K, N = 256, 64
+    gen = X.generator(T, DEV)
+    w, s = X.mxfp4_weight(N, K, gen)
+    s.fill_(250)
+    x = torch.zeros((T, K), dtype=torch.bfloat16, device=DEV)
+    x[:, ::16] = (torch.randint(1, 128, (T, K // 16), generator=gen, device=DEV).double() * 2.0 ** -133).to(torch.bfloat16)
+    ref = X.product(x.double(), X.mxfp4_values(w, s))
+    assert torch.equal(E.wkv(x, w, s), ref)
+
+
+def test_two_threads_with_different_k_at_once():
+    """Calls of two host threads, each on its own stream, with K that need
+    different LDS from the same kernels: every result is the serial one."""
+    import threading
+
+    E = _E()
+    T, N = 40, 2048
+    jobs = []
+    for i, K in enumerate((512, 16384)):
+        gen = X.generator(i, DEV)
+        w, s = X.mxfp4_weight(N, K, gen)
+        x, (xq, xs) = X.bf16_rows(T, K, gen), X.mxfp8_rows(T, K, gen)
+        wv = X.mxfp4_values(w, s)
+        refs = X.product(x.double(), wv), X.product(X.mxfp8_row_values(xq, xs), wv)
+        jobs.append((x, xq, xs, w, s, refs, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    start, failed = threading.Barrier(2), []
+
+    def work(x, xq, xs, w, s, refs, stream):
+        try:
+            with torch.cuda.stream(stream):
+                start.wait(30)
+                got = [(E.wkv(x, w, s), E.wkv_mx(xq, xs, w, s)) for _ in range(100)]
+                stream.synchronize()
+                for a, b in got:
+                    assert torch.equal(a, refs[0]) and torch.equal(b, refs[1])
+        except BaseException as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not failed, failed
