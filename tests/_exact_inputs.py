@@ -17,7 +17,7 @@ import torch
 # scale bytes for, both sides of that, and a wide N where fewer row tiles fit
 LONG_K = [(1, 32768, 36), (20, 32768, 36), (50, 36864, 20), (40, 131072, 32), (3, 163840, 8), (64, 131072 + 128, 4),
           (40, 35840, 36), (40, 35968, 36), (64, 35840, 20), (64, 35968, 20), (16, 65536, 52), (90, 32896, 132),
-          (20, 24576, 20476), (48, 30720, 16380), (64, 32768, 20476), (33, 8192, 12292)]
+          (20, 24576, 20476), (48, 30592, 16380), (64, 32768, 20476), (33, 8192, 12292)]
 # row tiles of a workgroup: 1 to 5 on 256 compute units, a part tile at the end
 WIDE_N = [4100, 6148, 8188, 10236, 12292, 16380, 20476]
 WIDE_K = [512, 4096]     # 4096: the swapped scale pieces
