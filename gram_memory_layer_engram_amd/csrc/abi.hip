@@ -48,10 +48,20 @@ size_t mx_stage_bytes(int64_t T, int32_t K) {
   return round_up((size_t)T * K) + round_up((size_t)T * (K / 32));
 }
 
-// Scratch of a projection from bf16 x besides kv: MXFP8 staging of x.
-size_t wkv_scratch_bytes(int64_t T, int64_t K, int32_t w_format) {
-  return w_format == ENGRAM_W_MXFP8 ? mx_stage_bytes(T, (int32_t)K) : 0;
+// Int8 activation staging: codes [T, K] then one fp32 scale a row.
+size_t int8_stage_bytes(int64_t T, int64_t K) { return round_up((size_t)T * K) + round_up((size_t)T * 4); }
+inline float* int8_stage_scales(void* stage, int64_t T, int64_t K) {
+  return (float*)((uint8_t*)stage + round_up((size_t)T * K));
 }
+
+// Scratch of a projection from bf16 x besides kv: 8-bit staging of x.
+size_t wkv_scratch_bytes(int64_t T, int64_t K, int32_t w_format) {
+  return w_format == ENGRAM_W_MXFP8  ? mx_stage_bytes(T, (int32_t)K)
+         : w_format == ENGRAM_W_INT8 ? int8_stage_bytes(T, K)
+                                     : 0;
+}
+
+constexpr int32_t kInt8MaxK = (1 << 17) - 16;   // sums of K products up to 2^14 fit 32 bits
 
 int check_wkv(const void* x, int64_t T, int32_t K, const void* w,
               const uint8_t* w_scales, int32_t w_format, int32_t N, void* kv) {
@@ -67,6 +77,9 @@ int check_wkv(const void* x, int64_t T, int32_t K, const void* w,
   } else if (w_format == ENGRAM_W_MXFP4) {
     if (T > 0 && (!w_scales || !aligned16(w_scales))) return ENGRAM_EINVAL;
     if (K % 128 != 0 || N % 4 != 0 || N > (1 << 28)) return ENGRAM_EUNSUPPORTED;
+  } else if (w_format == ENGRAM_W_INT8) {
+    if (T > 0 && (!w_scales || !aligned16(w_scales))) return ENGRAM_EINVAL;
+    if (K % 16 != 0 || K > kInt8MaxK || N % 4 != 0 || N > (1 << 28)) return ENGRAM_EUNSUPPORTED;
   } else {
     return ENGRAM_EINVAL;
   }
@@ -98,12 +111,31 @@ inline bool meet(const Span& a, const Span& b) {
 // would read it).
 bool on_operand(const Span& o, int64_t T, int64_t K, int64_t N, const void* x, int64_t x_bytes, const uint8_t* xs,
                 const void* w, const uint8_t* w_scales, int32_t w_format) {
+  if (w_format == ENGRAM_W_INT8)
+    return meet(o, {x, x_bytes}) || meet(o, {xs, 4 * T}) || meet(o, {w, N * K}) || meet(o, {w_scales, 4 * N});
   const bool f4 = w_format == ENGRAM_W_MXFP4;
   return meet(o, {x, x_bytes}) || meet(o, {xs, T * K / 32}) || meet(o, {w, f4 ? N * K / 2 : N * K}) ||
          meet(o, {w_scales, f4 ? N * K / 32 : N * K / 1024});
 }
 
+// Whether the staging of int8 activations lies on a tensor of its call.
+bool stage_meets(const void* stage, size_t bytes, int64_t T, int64_t K, int64_t N, const void* x, const void* w,
+                 const uint8_t* w_scales, const Span& out) {
+  const Span s{stage, (int64_t)bytes};
+  return meet(s, out) || on_operand(s, T, K, N, x, 2 * T * K, nullptr, w, w_scales, ENGRAM_W_INT8);
+}
+
 constexpr GateEpi kPlainStore{nullptr, nullptr, nullptr, nullptr, nullptr, 0, 0};
+
+// The projection from int8 activations.
+hipError_t run_int8_projection(const uint8_t* xq, const float* xs, int64_t T, int32_t K, const void* w,
+                               const uint8_t* w_scales, int32_t N, void* kv, hipStream_t s, const GateEpi& ep) {
+  return launch_gemm_int8(xq, xs, T, K, (const uint8_t*)w, (const float*)w_scales, N, kv, s, ep);
+}
+
+// Whether a format's outputs are checked against its operands (the formats that
+// came first leave that to the caller).
+inline bool checks_overlap(int32_t w_format) { return w_format == ENGRAM_W_MXFP4 || w_format == ENGRAM_W_INT8; }
 
 // Enqueue the projection given a workspace already checked to be large enough.
 int run_wkv(const void* x, int64_t T, int32_t K, const void* w,
@@ -119,14 +151,19 @@ int run_wkv(const void* x, int64_t T, int32_t K, const void* w,
     return hip_status(launch_gemm_mxfp4(x, nullptr, T, K, (const uint8_t*)w, w_scales, N, kv, s, ep));
   }
   uint8_t* xq = (uint8_t*)workspace;
+  if (w_format == ENGRAM_W_INT8) {
+    float* xs8 = int8_stage_scales(workspace, T, K);
+    if (launch_int8_quantize(x, T, K, xq, xs8, s) != hipSuccess) return ENGRAM_EHIP;
+    return hip_status(run_int8_projection(xq, xs8, T, K, w, w_scales, N, kv, s, ep));
+  }
   uint8_t* xs = xq + round_up((size_t)T * K);
   hipError_t e = launch_mx_quantize(x, T, K, xq, xs, s);
   if (e != hipSuccess) return ENGRAM_EHIP;
   return hip_status(run_mx_projection(xq, xs, T, K, w, w_scales, N, kv, s, ep));
 }
 
-// MXFP8 quantize + tiled scaled-MFMA GEMM whatever T is (the gate epilogue
-// lives in the tiled GEMM only).
+// Quantize where the format needs it + tiled GEMM whatever T is (the gate
+// epilogue lives in the tiled GEMM only).
 int run_wkv_tiled(const void* x, int64_t T, int32_t K, const void* w, const uint8_t* w_scales,
                   int32_t w_format, int32_t N, void* kv, void* workspace, hipStream_t s, const GateEpi& ep) {
   if (T == 0) return ENGRAM_OK;
@@ -134,6 +171,11 @@ int run_wkv_tiled(const void* x, int64_t T, int32_t K, const void* w, const uint
   if (w_format == ENGRAM_W_MXFP4)
     return hip_status(launch_gemm_mxfp4(x, nullptr, T, K, (const uint8_t*)w, w_scales, N, kv, s, ep));
   uint8_t* xq = (uint8_t*)workspace;
+  if (w_format == ENGRAM_W_INT8) {
+    float* xs8 = int8_stage_scales(workspace, T, K);
+    if (launch_int8_quantize(x, T, K, xq, xs8, s) != hipSuccess) return ENGRAM_EHIP;
+    return hip_status(launch_gemm_int8(xq, xs8, T, K, (const uint8_t*)w, (const float*)w_scales, N, kv, s, ep));
+  }
   uint8_t* xs = xq + round_up((size_t)T * K);
   if (launch_mx_quantize(x, T, K, xq, xs, s) != hipSuccess) return ENGRAM_EHIP;
   return hip_status(launch_gemm_mxfp8(xq, xs, T, K, (const uint8_t*)w, w_scales, N, kv, s, ep));
@@ -263,6 +305,16 @@ int engram_mx_quantize(const void* x, int64_t T, int32_t K, uint8_t* xq,
   return hip_status(launch_mx_quantize(x, T, K, xq, xs, (hipStream_t)stream));
 }
 
+int engram_int8_quantize(const void* x, int64_t T, int32_t K, int8_t* xq, float* xs, void* stream) {
+  if (T < 0 || K <= 0) return ENGRAM_EINVAL;
+  if (K % 16 != 0 || K > kInt8MaxK || T > INT32_MAX) return ENGRAM_EUNSUPPORTED;
+  if (T == 0) return ENGRAM_OK;
+  if (!x || !xq || !xs || !aligned16(x) || !aligned16(xq) || ((uintptr_t)xs & 3u)) return ENGRAM_EINVAL;
+  const Span sx{x, 2 * T * K}, sq{xq, T * K}, ss{xs, 4 * T};
+  if (meet(sq, sx) || meet(ss, sx) || meet(sq, ss)) return ENGRAM_EINVAL;
+  return hip_status(launch_int8_quantize(x, T, K, (uint8_t*)xq, xs, (hipStream_t)stream));
+}
+
 size_t engram_wkv_workspace_size(int64_t T, int32_t K, int32_t N,
                                  int32_t w_format) {
   (void)N;
@@ -285,7 +337,7 @@ int engram_wkv_gate_partials(const void* x, int64_t T, int32_t K, const void* w,
   if (st != ENGRAM_OK) return st;
   if (T == 0) return ENGRAM_OK;
   if (!partials || ((uintptr_t)partials & 7u)) return ENGRAM_EINVAL;
-  if (w_format == ENGRAM_W_MXFP4) {
+  if (checks_overlap(w_format)) {
     const int64_t n = T * hc * dim;
     const Span outs[2] = {{value, 2 * T * dim}, {partials, n / 256 * 8}};
     if (meet(outs[0], outs[1])) return ENGRAM_EINVAL;
@@ -297,6 +349,13 @@ int engram_wkv_gate_partials(const void* x, int64_t T, int32_t K, const void* w,
   const size_t need = engram_wkv_workspace_size(T, K, N, w_format);
   if (workspace_bytes < need || (need && (!workspace || ((uintptr_t)workspace % kAlign))))
     return ENGRAM_EINVAL;
+  if (w_format == ENGRAM_W_INT8) {
+    const Span ws{workspace, (int64_t)need}, hid{hidden, 2 * T * hc * dim}, part{partials, T * hc * dim / 256 * 8};
+    const int64_t wb = (int64_t)2 * hc * dim;
+    if (stage_meets(workspace, need, T, K, N, x, w, w_scales, {value, 2 * T * dim}) || meet(ws, hid) || meet(ws, part) ||
+        meet(ws, {q_weight, wb}) || meet(ws, {k_weight, wb}))
+      return ENGRAM_EINVAL;
+  }
   const GateEpi ep{(const uint16_t*)hidden, (const uint16_t*)q_weight, (const uint16_t*)k_weight,
                    (uint16_t*)value, (float2*)partials, hc, dim};
   return run_wkv_tiled(x, T, K, w, w_scales, w_format, N, value, workspace, (hipStream_t)stream, ep);
@@ -307,11 +366,12 @@ int engram_wkv(const void* x, int64_t T, int32_t K, const void* w,
                void* workspace, size_t workspace_bytes, void* stream) {
   int st = check_wkv(x, T, K, w, w_scales, w_format, N, kv);
   if (st != ENGRAM_OK || T == 0) return st;
-  if (w_format == ENGRAM_W_MXFP4 && on_operand({kv, 2 * T * N}, T, K, N, x, 2 * T * K, nullptr, w, w_scales, w_format))
+  if (checks_overlap(w_format) && on_operand({kv, 2 * T * N}, T, K, N, x, 2 * T * K, nullptr, w, w_scales, w_format))
     return ENGRAM_EINVAL;
   const size_t need = engram_wkv_workspace_size(T, K, N, w_format);
   if (workspace_bytes < need || (need && (!workspace || ((uintptr_t)workspace % kAlign))))
     return ENGRAM_EINVAL;
+  if (w_format == ENGRAM_W_INT8 && stage_meets(workspace, need, T, K, N, x, w, w_scales, {kv, 2 * T * N})) return ENGRAM_EINVAL;
   return run_wkv(x, T, K, w, w_scales, w_format, N, kv, workspace, (hipStream_t)stream);
 }
 
@@ -328,6 +388,74 @@ int engram_wkv_mx(const uint8_t* xq, const uint8_t* xs, int64_t T, int32_t K, co
     return hip_status(run_mx_projection(xq, xs, T, K, w, w_scales, N, kv, s, kPlainStore));
   if (gemv_mxfp4_supported(T, K, true)) return hip_status(launch_gemv_mxfp4(xq, xs, T, K, w, w_scales, N, kv, s));
   return hip_status(launch_gemm_mxfp4(xq, xs, T, K, (const uint8_t*)w, w_scales, N, kv, s, kPlainStore));
+}
+
+int engram_wkv_int8(const int8_t* xq, const float* xs, int64_t T, int32_t K, const int8_t* w, const float* w_scales,
+                    int32_t N, void* kv, void* stream) {
+  const uint8_t* wsb = (const uint8_t*)w_scales;
+  int st = check_wkv(xq, T, K, w, wsb, ENGRAM_W_INT8, N, kv);
+  if (st != ENGRAM_OK || T == 0) return st;
+  if (!xs || ((uintptr_t)xs & 3u)) return ENGRAM_EINVAL;
+  if (on_operand({kv, 2 * T * N}, T, K, N, xq, T * K, (const uint8_t*)xs, w, wsb, ENGRAM_W_INT8)) return ENGRAM_EINVAL;
+  return hip_status(run_int8_projection((const uint8_t*)xq, xs, T, K, w, wsb, N, kv, (hipStream_t)stream, kPlainStore));
+}
+
+int engram_post_pre_norm(const engram_post_pre_norm_args* p, void* stream) {
+  if (!p) return ENGRAM_EINVAL;
+  const engram_post_pre_norm_args& a = *p;
+  const int64_t T = a.T, hc = a.hc, dim = a.dim;
+  if (T < 0 || hc <= 0 || dim <= 0 || !(a.eps >= 0.0f) || !(a.post_eps >= 0.0f)) return ENGRAM_EINVAL;
+  if (a.x_stride_t < 0 || a.x_stride_h < 0 || a.residual_stride_t < 0 || a.residual_stride_h < 0 ||
+      a.gate_stride_t < 0 || a.gate_stride_h < 0)
+    return ENGRAM_EINVAL;
+  if (a.gate_format < ENGRAM_GATE_NONE || a.gate_format > ENGRAM_GATE_CHANNEL || (a.gate_sigmoid & ~1) ||
+      (a.post_norm & ~1))
+    return ENGRAM_EINVAL;
+  if ((a.gate_format == ENGRAM_GATE_NONE) != (a.gate == nullptr) && T > 0) return ENGRAM_EINVAL;
+  if (a.q_format < ENGRAM_Q_NONE || a.q_format > ENGRAM_Q_INT8) return ENGRAM_EINVAL;
+  const bool q = a.q_format != ENGRAM_Q_NONE;
+  if (T > 0 && (q != (a.xq != nullptr) || q != (a.xs != nullptr))) return ENGRAM_EINVAL;
+  if (a.post_weight && a.post_weight_hc != 1 && a.post_weight_hc != hc) return ENGRAM_EINVAL;
+  if (a.pre_weight && a.pre_weight_hc != 1 && a.pre_weight_hc != hc) return ENGRAM_EINVAL;
+  if (dim % 8 != 0 || dim > 16384 || (a.q_format == ENGRAM_Q_MXFP8 && dim % 32 != 0)) return ENGRAM_EUNSUPPORTED;
+  const bool channel = a.gate_format == ENGRAM_GATE_CHANNEL;
+  if ((a.x_stride_t | a.x_stride_h | a.residual_stride_t | a.residual_stride_h |
+       (channel ? a.gate_stride_t | a.gate_stride_h : 0)) & 7)
+    return ENGRAM_EUNSUPPORTED;
+  if (T > INT32_MAX / hc) return ENGRAM_EUNSUPPORTED;
+  if (T == 0) return ENGRAM_OK;
+  if (!a.x || (!a.residual_out && !a.out && !q)) return ENGRAM_EINVAL;
+  for (const void* v : {a.x, a.residual, channel ? a.gate : nullptr, a.post_weight, a.pre_weight,
+                        (const void*)a.residual_out, (const void*)a.out, (const void*)a.xq})
+    if (!aligned16(v)) return ENGRAM_EINVAL;
+  const bool i8 = a.q_format == ENGRAM_Q_INT8;
+  if ((a.gate && ((uintptr_t)a.gate & 3u)) || (i8 && ((uintptr_t)a.xs & 3u))) return ENGRAM_EINVAL;
+  // in place is row by row: residual_out on residual and out on x, dense and
+  // whole; any other overlap of an output with another tensor is refused
+  const int64_t n = T * hc * dim;
+  auto rows_of = [&](const void* v, int64_t st, int64_t sh, int64_t width, int64_t size) {
+    return Span{v, size * ((T - 1) * st + (hc - 1) * sh + width)};
+  };
+  const Span in[5] = {rows_of(a.x, a.x_stride_t, a.x_stride_h, dim, 2),
+                      rows_of(a.residual, a.residual_stride_t, a.residual_stride_h, dim, 2),
+                      rows_of(a.gate, a.gate_stride_t, a.gate_stride_h, channel ? dim : 1, channel ? 2 : 4),
+                      {a.post_weight, 2 * a.post_weight_hc * dim}, {a.pre_weight, 2 * a.pre_weight_hc * dim}};
+  const Span out[4] = {{a.out, 2 * n}, {a.residual_out, 2 * n}, {a.xq, n}, {a.xs, i8 ? 4 * T * hc : n / 32}};
+  auto dense = [&](int64_t st, int64_t sh) { return (T == 1 || st == hc * dim) && (hc == 1 || sh == dim); };
+  const bool whole[2] = {dense(a.x_stride_t, a.x_stride_h), dense(a.residual_stride_t, a.residual_stride_h)};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 5; ++j)
+      if (meet(out[i], in[j]) && !(i == j && j < 2 && out[i].p == in[j].p && whole[j])) return ENGRAM_EINVAL;
+    for (int j = 0; j < i; ++j)
+      if (meet(out[i], out[j])) return ENGRAM_EINVAL;
+  }
+  const PostPreNormArgs k{(const uint16_t*)a.x, a.x_stride_t, a.x_stride_h, (const uint16_t*)a.residual,
+                          a.residual_stride_t, a.residual_stride_h, a.gate, a.gate_stride_t, a.gate_stride_h,
+                          a.gate_format, a.gate_sigmoid, (const uint16_t*)a.post_weight,
+                          (const uint16_t*)a.pre_weight, a.post_weight_hc, a.pre_weight_hc, a.post_norm, T * hc,
+                          a.hc, a.dim, a.post_eps, a.eps, a.residual_scale, a.branch_scale,
+                          (uint16_t*)a.residual_out, (uint16_t*)a.out, a.q_format, a.xq, a.xs};
+  return hip_status(launch_post_pre_norm(k, (hipStream_t)stream));
 }
 
 int engram_add_rms_norm(const void* x, int64_t x_stride_t, int64_t x_stride_h, const void* residual,
@@ -443,6 +571,13 @@ static int check_forward(const engram_forward_args* a, void* workspace, size_t w
   return ENGRAM_OK;
 }
 
+// Formats whose plain store may take 128x128 tiles where the epilogue has
+// 256x256 ones, and whether it would take the latter.
+static bool checks_small_tiles(int32_t w_format) { return w_format == ENGRAM_W_MXFP4 || w_format == ENGRAM_W_INT8; }
+static bool big_tiles(int32_t w_format, int64_t T, int32_t N, int32_t K) {
+  return w_format == ENGRAM_W_MXFP4 ? gemm_mxfp4_big_tiles(T, N, K) : gemm_int8_big_tiles(T, N, K);
+}
+
 // engram_forward's launches, given checked arguments and the workspace past
 // its flag area (rows | kv | MXFP8 staging; nothing in it needs to start at
 // zero: every byte a kernel reads was written earlier in the same call).
@@ -458,6 +593,7 @@ static int run_forward(const engram_forward_args* a, int32_t K, int32_t N, uint8
   // workspace.
   const bool tiled = a->w_format == ENGRAM_W_BF16    ? !gemv_bf16_supported(a->T, K, N)
                      : a->w_format == ENGRAM_W_MXFP8 ? !gemv_mxfp8_supported(a->T, K)
+                     : a->w_format == ENGRAM_W_INT8  ? true
                                                      : !gemv_mxfp4_supported(a->T, K, false);
   // MXFP4 weights: only where the plain store would take the epilogue's
   // 256x256 tile as well, or kv is too large to wait for the gate in the
@@ -465,7 +601,7 @@ static int run_forward(const engram_forward_args* a, int32_t K, int32_t N, uint8
   // dim 4096, epilogue / kv stored: K 2048, T 300 59 / 43 us, T 1000 118 / 100, T
   // 4096 340 / 358; K 256, T 1000 51 / 42, T 4096 139 / 155).
   const bool epi = !(a->options & ENGRAM_FORWARD_STORE_KV) && tiled && a->dim % 256 == 0 &&
-                   (a->w_format != ENGRAM_W_MXFP4 || gemm_mxfp4_big_tiles(a->T, N, K) ||
+                   (!checks_small_tiles(a->w_format) || big_tiles(a->w_format, a->T, N, K) ||
                     a->T * (int64_t)N * 2 > (128 << 20));
   uint16_t* value = (uint16_t*)kv;
   float2* part = (float2*)((uint8_t*)kv + round_up((size_t)a->T * a->dim * 2));
@@ -473,7 +609,15 @@ static int run_forward(const engram_forward_args* a, int32_t K, int32_t N, uint8
                                    (const uint16_t*)a->k_weight, value, part, a->hc, a->dim}
                          : kPlainStore;
   hipError_t e;
-  if (a->w_format == ENGRAM_W_MXFP8 && a->head_dim % 32 == 0) {
+  if (a->w_format == ENGRAM_W_INT8) {
+    uint8_t* xq = (uint8_t*)mx;
+    float* xs = int8_stage_scales(mx, a->T, K);
+    e = launch_gather_int8(a->table, a->table_scales, a->num_rows, a->head_dim, a->hash_ids, a->ids_stride_t,
+                           a->ids_stride_c, a->T, a->n_cols, xq, xs, a->err_flag, s);
+    if (e != hipSuccess) return ENGRAM_EHIP;
+    e = run_int8_projection(xq, xs, a->T, K, a->w, a->w_scales, N, kv, s, ep);
+    if (e != hipSuccess) return ENGRAM_EHIP;
+  } else if (a->w_format == ENGRAM_W_MXFP8 && a->head_dim % 32 == 0) {
     // the gather feeds the quantizer directly: bf16 staged rows never reach HBM
     uint8_t* xq = (uint8_t*)mx;
     uint8_t* xs = xq + round_up((size_t)a->T * K);

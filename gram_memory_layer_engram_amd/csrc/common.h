@@ -104,6 +104,40 @@ struct RmsNormArgs {
 };
 hipError_t launch_add_rms_norm(const RmsNormArgs& a, hipStream_t s);
 
+// The norms around a block (post_pre_norm.hip). residual, gate, the weights,
+// residual_out, out and (xq, xs) may be null; strides in elements.
+enum { kGateNone = 0, kGateRow = 1, kGateChannel = 2 };
+enum { kQNone = 0, kQMx = 1, kQInt8 = 2 };
+struct PostPreNormArgs {
+  const uint16_t* x;
+  int64_t x_st, x_sh;
+  const uint16_t* residual;
+  int64_t r_st, r_sh;
+  const void* gate;              // fp32 (kGateRow) or bf16 rows (kGateChannel)
+  int64_t g_st, g_sh;
+  int gate_format, sigmoid;
+  const uint16_t* post_weight;   // [post_hc, dim]
+  const uint16_t* pre_weight;    // [pre_hc, dim]
+  int post_hc, pre_hc, post_norm;
+  int64_t rows;                  // T * hc
+  int hc, dim;
+  float post_eps, eps, residual_scale, branch_scale;
+  uint16_t* residual_out;        // [T, hc, dim]
+  uint16_t* out;                 // [T, hc, dim]
+  int q_format;
+  uint8_t* xq;                   // [T, hc, dim]
+  void* xs;                      // E8M0 [T, hc, dim / 32] or fp32 [T, hc]
+};
+hipError_t launch_post_pre_norm(const PostPreNormArgs& a, hipStream_t s);
+
+// Rows in int8 with one fp32 scale each (int8q.hip; K % 16 == 0, K < 2^17): of
+// x [T, K], and of the gathered rows (an fp8 table when table_scales is not
+// null; K = n_cols * head_dim).
+hipError_t launch_int8_quantize(const void* x, int64_t T, int K, uint8_t* xq, float* xs, hipStream_t s);
+hipError_t launch_gather_int8(const void* table, const uint8_t* table_scales, int64_t num_rows, int head_dim,
+                              const int32_t* ids, int64_t st, int64_t sc, int64_t T, int n_cols, uint8_t* xq, float* xs,
+                              int32_t* err, hipStream_t s);
+
 // Row gather fused with the MXFP8 quantizer (head_dim % 32 == 0); an fp8
 // table when table_scales is not null.
 hipError_t launch_gather_quantize(const void* table, const uint8_t* table_scales, int64_t num_rows,
@@ -147,6 +181,12 @@ bool gemm_mxfp4_big_tiles(int64_t T, int N, int K);
 // codes when xs is not null.
 hipError_t launch_gemm_mxfp4(const void* x, const uint8_t* xs, int64_t T, int K, const uint8_t* w,
                              const uint8_t* ws, int N, void* kv, hipStream_t s, const GateEpi& ep);
+
+// Tiled int8 GEMM (K % 16 == 0, K < 2^17, N % 4 == 0), and whether it stores
+// kv with the 256x256 tiles that the gate's epilogue has, all of it.
+bool gemm_int8_big_tiles(int64_t T, int N, int K);
+hipError_t launch_gemm_int8(const uint8_t* xq, const float* xs, int64_t T, int K, const uint8_t* w, const float* ws,
+                            int N, void* kv, hipStream_t s, const GateEpi& ep);
 
 // Largest T the decode GEMV serves; above it the tiled GEMM runs.
 constexpr int kGemvMaxT = 64;

@@ -1,0 +1,233 @@
+// Tiled projection GEMM in 8-bit integers: kv[T, N] = bf16(float(x . W^T) * xs[t]
+// * ws[n]), x int8 [T, K] with one fp32 scale a token, W int8 [N, K] with one a
+// row, K % 16 == 0, N % 4 == 0.
+//
+// The sums are whole numbers in 32 bits, exact for K < 2^17 (128 * 128 * K <
+// 2^31), so every order of them gives the same kv: tiles, the small-batch
+// kernel (gemv_int8.hip) and any split agree bit for bit. Three fp32 roundings
+// (the sum to fp32, two scales) and kv's own are left.
+//
+// v_mfma_i32_32x32x32_i8 takes in lane l (row l%32, half h = l/32) 16 bytes of k,
+// and the order of k is free as long as both operands follow it: sub-step kk
+// (0..3) of a 128-byte slice is pieces 2kk + h of the rows, the byte layout of
+// the bf16 GEMM (gemm.hip) with twice the k in a slice, at the same cycles a
+// matrix instruction. So the block (256 x 256, four waves of 128 x 128, or 128 x
+// 128 with two workgroups on a compute unit), the ring of five LDS chunks, the
+// tile order and the epilogue are that kernel's; the schedule is described
+// there.
+//
+// The scales wait in registers, two of the wave's 128 (64) rows and tokens a
+// lane, and go through LDS once the loop has left it: 256 different ones a
+// lane would be needed at its accumulators.
+#include "gemm_tile.h"
+
+namespace engram {
+
+namespace {
+
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+
+template <int NT, bool KTAIL>
+__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(NT == 4 ? 1 : 2, NT == 4 ? 1 : 2)))
+void gemm_int8_kernel(const uint8_t* __restrict__ xq, const float* __restrict__ xs, int T, int K,
+                      const uint8_t* __restrict__ w, const float* __restrict__ ws, int N, uint16_t* __restrict__ kv,
+                      int tn0, int tiles_n, int tiles_t, GateEpi ep) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  int tn, tt;
+  tile_of(blockIdx.x, tiles_n, tiles_t, tn, tt);
+  constexpr int TILE = 64 * NT, CH = Q_ROW * TILE, NDMA = 2 * NT;   // a chunk in LDS, a wave's DMAs for it
+  const int n0 = (tn0 + tn) * TILE, t0 = tt * TILE;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = (wave >> 1) * (32 * NT), wt = (wave & 1) * (32 * NT);
+  const uint32_t row_bytes = (uint32_t)K;
+  const rsrc_t ra = make_rsrc(w + (int64_t)n0 * K, (uint32_t)min(TILE, N - n0) * row_bytes);
+  const rsrc_t rb = make_rsrc(xq + (int64_t)t0 * K, (uint32_t)min(TILE, T - t0) * row_bytes);
+  const uint32_t oob = (uint32_t)TILE * row_bytes;   // at or past both ranges
+  const int nk = (K + Q_ROW - 1) / Q_ROW;
+
+  // scales of the wave's rows and tokens lane and 64 + lane (rows past the end: the last's, never stored)
+  float wsc[NT / 2], xsc[NT / 2];
+#pragma unroll
+  for (int k = 0; k < NT / 2; ++k) {
+    wsc[k] = ws[min(n0 + wn + 64 * k + lane, N - 1)];
+    xsc[k] = xs[min(t0 + wt + 64 * k + lane, T - 1)];
+  }
+
+  const dma::Lane dl = dma::lane_of(wave, lane, row_bytes);
+  auto dma = [&](int slot_ofs, int op, uint32_t kofs, int i) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(op ? rb : ra, (lds_ptr_t)(smem + slot_ofs + (wave + 4 * i) * 1024), 16,
+                                             dma::voffset(dl, i, kofs, row_bytes, oob, KTAIL), 0, 0, 0);
+  };
+
+  i32x16 acc[NT][NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
+
+  const int lrow = lane & 31, lhalf = lane >> 5;
+  const int fsw = (lrow >> 1) & 7;
+  i32x4 a[2][NT], b[2][NT];
+  // fragment f (b of each token block, then a of each row block) of sub-step kk into register set c
+  auto frag = [&](int sa, int sb, int kk, int c, int f) {
+    const int i = f % NT;
+    const int row = (f < NT ? wt : wn) + i * 32 + lrow;
+    const int piece = (2 * kk + lhalf) ^ fsw;
+    const i32x4 v = *reinterpret_cast<const i32x4*>(smem + (f < NT ? sb : sa) + row * Q_ROW + piece * 16);
+    if (f < NT) b[c][i] = v; else a[c][i] = v;
+  };
+  auto mfma_row = [&](int c, int i) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[c][i], b[c][j], acc[i][j], 0, 0, 0);
+  };
+
+  // prologue: A0 -> slot 0, B0 -> slot 1, A1 -> slot 2
+#pragma unroll
+  for (int i = 0; i < NDMA; ++i) dma(0, 0, 0u, i);
+#pragma unroll
+  for (int i = 0; i < NDMA; ++i) dma(CH, 1, 0u, i);
+#pragma unroll
+  for (int i = 0; i < NDMA; ++i) dma(2 * CH, 0, nk > 1 ? (uint32_t)Q_ROW : oob, i);
+  wait_vm<NDMA>();
+  // a use here keeps the scale loads ahead of the DMAs
+#pragma unroll
+  for (int k = 0; k < NT / 2; ++k) asm volatile("" : "+v"(wsc[k]), "+v"(xsc[k]));
+  bare_barrier();
+#pragma unroll
+  for (int f = 0; f < 2 * NT; ++f) frag(0, CH, 0, 0, f);
+
+  // Chunk c (A_d = 2d, B_d = 2d+1) lives in ring slot c % 5. While slice d is
+  // computed, B_{d+1} and A_{d+2} are fetched into the slots of A_{d-1} and
+  // B_{d-1}, freed by the previous slice's barrier.
+  int base = 0;   // (2d) % 5
+  for (int d = 0; d < nk; ++d) {
+    auto slot = [&](int m) { const int v = base + m; return (v >= Q_SLOTS ? v - Q_SLOTS : v) * CH; };
+    const int sa = slot(0), sb = slot(1), sa1 = slot(2), sb1 = slot(3), sa2 = slot(4);
+    const uint32_t kb1 = d + 1 < nk ? (uint32_t)(d + 1) * Q_ROW : oob;
+    const uint32_t ka2 = d + 2 < nk ? (uint32_t)(d + 2) * Q_ROW : oob;
+    // sub-step 0: MFMAs on set 0; sub-step 1's fragments into set 1; B_{d+1}
+#pragma unroll
+    for (int q = 0; q < NT; ++q) {
+      __builtin_amdgcn_sched_barrier(0);
+      dma(sb1, 1, kb1, 2 * q);
+      dma(sb1, 1, kb1, 2 * q + 1);
+      frag(sa, sb, 1, 1, 2 * q);
+      frag(sa, sb, 1, 1, 2 * q + 1);
+      mfma_row(0, q);
+      SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_DSR, 1);
+      if (NT == 4) { SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_MFMA, 1); SGB(SG_DSR, 1); SGB(SG_MFMA, 1); }
+      else { SGB(SG_VMEM, 1); SGB(SG_DSR, 1); SGB(SG_MFMA, 1); }
+    }
+    // sub-steps 1 and 2: A_{d+2}
+#pragma unroll
+    for (int kk = 1; kk < 3; ++kk) {
+#pragma unroll
+      for (int q = 0; q < NT; ++q) {
+        __builtin_amdgcn_sched_barrier(0);
+        dma(sa2, 0, ka2, (kk - 1) * NT + q);
+        frag(sa, sb, kk + 1, (kk + 1) & 1, 2 * q);
+        frag(sa, sb, kk + 1, (kk + 1) & 1, 2 * q + 1);
+        mfma_row(kk & 1, q);
+        if (NT == 4) {
+          SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_MFMA, 1); SGB(SG_DSR, 1); SGB(SG_MFMA, 1); SGB(SG_DSR, 1);
+          SGB(SG_MFMA, 1);
+        } else {
+          SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_DSR, 2); SGB(SG_MFMA, 1);
+        }
+      }
+    }
+    // sub-step 3, first row block, then publish slice d+1: only A_{d+2}'s DMAs may still fly
+    __builtin_amdgcn_sched_barrier(0);
+    mfma_row(1, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vm<NDMA>();
+    wait_lgkm0();
+    bare_barrier();
+    // the other row blocks: slice d+1's sub-step-0 fragments into set 0
+#pragma unroll
+    for (int q = 1; q < NT; ++q) {
+      __builtin_amdgcn_sched_barrier(0);
+      const int f0 = NT == 2 ? 0 : 3 * (q - 1), nf = NT == 2 ? 4 : q == 3 ? 2 : 3;
+#pragma unroll
+      for (int f = 0; f < nf; ++f) frag(sa1, sb1, 0, 0, f0 + f);
+      mfma_row(1, q);
+      if (NT == 2) {
+        SGB(SG_MFMA, 1); SGB(SG_DSR, 4); SGB(SG_MFMA, 1);
+      } else if (q < 3) {
+        SGB(SG_MFMA, 1); SGB(SG_DSR, 1); SGB(SG_MFMA, 1); SGB(SG_DSR, 1); SGB(SG_MFMA, 1); SGB(SG_DSR, 1);
+        SGB(SG_MFMA, 1);
+      } else {
+        SGB(SG_MFMA, 1); SGB(SG_DSR, 1); SGB(SG_MFMA, 1); SGB(SG_DSR, 1); SGB(SG_MFMA, 2);
+      }
+    }
+    base = base + 2 >= Q_SLOTS ? base + 2 - Q_SLOTS : base + 2;
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  wait_vm<0>();   // the zero-fill DMAs of the last slices land before LDS is reused
+  wait_lgkm0();
+  bare_barrier();
+
+  // the wave's scales through its own KiB of LDS past the epilogue's staging tile
+  float* sl = reinterpret_cast<float*>(smem + TILE * 2 * TILE) + wave * 256;
+#pragma unroll
+  for (int k = 0; k < NT / 2; ++k) {
+    sl[64 * k + lane] = wsc[k];
+    sl[128 + 64 * k + lane] = xsc[k];
+  }
+  wait_lgkm0();
+  float tx[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) tx[j] = sl[128 + j * 32 + lrow];
+  f32x16 out[NT][NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      // accumulator r of lane l: row 8*(r/4) + 4*(l/32) + r%4, token l%32
+      const f32x4 wv = *reinterpret_cast<const f32x4*>(sl + i * 32 + 8 * g + 4 * lhalf);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[i][j][4 * g + e] = (float)acc[i][j][4 * g + e] * tx[j] * wv[e];
+    }
+  store_tile<NT>(out, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
+}
+
+template <int NT>
+hipError_t launch_tile(const uint8_t* xq, const float* xs, int T, int K, const uint8_t* w, const float* ws, int N,
+                       uint16_t* kv, int tn0, int tiles_n, hipStream_t s, const GateEpi& ep) {
+  const int tiles_t = (T + 64 * NT - 1) / (64 * NT);
+  constexpr int lds = Q_LDS * NT / 4;
+  const auto fn = K % Q_ROW ? gemm_int8_kernel<NT, true> : gemm_int8_kernel<NT, false>;
+  const hipError_t e = set_lds((const void*)fn, lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(fn, dim3(tiles_n * tiles_t), dim3(THREADS), lds, s, xq, xs, T, K, w, ws, N, kv, tn0, tiles_n,
+                     tiles_t, ep);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+static int int8_big_columns(int64_t T, int N, int K) {
+  return big_columns(T, N, K, {8000, 1400, 3200, 950, 3200, 660});
+}
+
+bool gemm_int8_big_tiles(int64_t T, int N, int K) { return int8_big_columns(T, N, K) == (N + 255) / 256; }
+
+// The gate's epilogue has the 256x256 tile only.
+hipError_t launch_gemm_int8(const uint8_t* xq, const float* xs, int64_t T, int K, const uint8_t* w, const float* ws,
+                            int N, void* kv, hipStream_t s, const GateEpi& ep) {
+  uint16_t* out = (uint16_t*)kv;
+  const int big = ep.hidden ? (N + 255) / 256 : int8_big_columns(T, N, K);
+  if (big) {
+    const hipError_t e = launch_tile<4>(xq, xs, (int)T, K, w, ws, N, out, 0, big, s, ep);
+    if (e != hipSuccess || 256 * (int64_t)big >= N) return e;
+  }
+  return launch_tile<2>(xq, xs, (int)T, K, w, ws, N, out, 2 * big, (N + 127) / 128 - 2 * big, s, ep);
+}
+
+}  // namespace engram

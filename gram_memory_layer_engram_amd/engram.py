@@ -18,7 +18,9 @@ LIB_PATH = os.path.join(_HERE, "libengram.so")
 
 ENGRAM_OK, ENGRAM_EINVAL, ENGRAM_EUNSUPPORTED, ENGRAM_EHIP, ENGRAM_ENOSPACE = 0, 1, 2, 3, 4
 NOALLOC_SCRATCH_BYTES = 32 << 20
-W_BF16, W_MXFP8, W_MXFP4 = 0, 1, 2
+W_BF16, W_MXFP8, W_MXFP4, W_INT8 = 0, 1, 2, 3
+GATE_NONE, GATE_ROW, GATE_CHANNEL = 0, 1, 2
+Q_NONE, Q_MXFP8, Q_INT8 = 0, 1, 2
 FORWARD_STORE_KV = 1
 
 _vp = ctypes.c_void_p
@@ -28,7 +30,7 @@ _f32 = ctypes.c_float
 _sz = ctypes.c_size_t
 
 # names of the calls that count in single tokens, looked up once
-_BF16, _U8 = torch.bfloat16, torch.uint8
+_BF16, _U8, _I8, _F32 = torch.bfloat16, torch.uint8, torch.int8, torch.float32
 _empty_strided = torch.empty_strided
 _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
@@ -49,6 +51,22 @@ class ForwardArgs(ctypes.Structure):
     ]
 
 
+class PostPreNormArgs(ctypes.Structure):
+    """Mirror of ``engram_post_pre_norm_args``."""
+
+    _fields_ = [
+        ("x", _vp), ("x_stride_t", _i64), ("x_stride_h", _i64),
+        ("residual", _vp), ("residual_stride_t", _i64), ("residual_stride_h", _i64),
+        ("gate", _vp), ("gate_stride_t", _i64), ("gate_stride_h", _i64),
+        ("gate_format", _i32), ("gate_sigmoid", _i32),
+        ("post_weight", _vp), ("pre_weight", _vp), ("post_weight_hc", _i32), ("pre_weight_hc", _i32),
+        ("T", _i64), ("hc", _i32), ("dim", _i32), ("post_norm", _i32),
+        ("post_eps", _f32), ("eps", _f32), ("residual_scale", _f32), ("branch_scale", _f32),
+        ("q_format", _i32),
+        ("residual_out", _vp), ("out", _vp), ("xq", _vp), ("xs", _vp),
+    ]
+
+
 EXPORTS = {
     "engram_abi_version": (_i32, []),
     "engram_status_string": (ctypes.c_char_p, [_i32]),
@@ -63,6 +81,9 @@ EXPORTS = {
     "engram_wkv_gate_partials": (_i32, [_vp, _i64, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp,
                                         _vp, _sz, _vp]),
     "engram_wkv_mx": (_i32, [_vp, _vp, _i64, _i32, _vp, _vp, _i32, _i32, _vp, _vp]),
+    "engram_int8_quantize": (_i32, [_vp, _i64, _i32, _vp, _vp, _vp]),
+    "engram_wkv_int8": (_i32, [_vp, _vp, _i64, _i32, _vp, _vp, _i32, _vp, _vp]),
+    "engram_post_pre_norm": (_i32, [ctypes.POINTER(PostPreNormArgs), _vp]),
     "engram_add_rms_norm": (_i32, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i32, _i64, _i32, _i32, _f32, _vp, _vp,
                                    _vp, _vp, _vp]),
     "engram_gate": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _f32, _f32, _vp, _vp, _vp]),
@@ -173,15 +194,20 @@ def _stream() -> int:
 
 def _format(w: torch.Tensor, w_scales, N: int, K: int) -> int:
     """The wkv weight format by its tensors: bf16 [N, K] without scales, MXFP8
-    codes [N, K] with scales [N/32, K/32], or MXFP4 codes [N, K/2] with scales
-    [N, K/32]. The kernels read all of them: anything else is refused."""
+    codes [N, K] with scales [N/32, K/32], MXFP4 codes [N, K/2] with scales
+    [N, K/32], or int8 [N, K] with fp32 scales [N]. The kernels read all of
+    them: anything else is refused."""
     shape = w.shape
+    if w_scales is not None and w_scales.dtype == _F32:
+        _check_int8(w, w_scales, N, K)
+        return W_INT8
     if w_scales is not None and shape == (N, K // 2):
         _check_mxfp4(w, w_scales, N, K)
         return W_MXFP4
     if shape != (N, K) or w.element_size() != (2 if w_scales is None else 1):
         raise ValueError(f"w must be bf16 [{N}, {K}], codes [{N}, {K}] with scales [{N // 32}, {K // 32}] (MXFP8) or "
-                         f"[{N}, {K // 2}] with [{N}, {K // 32}] (MXFP4), got {w.dtype} {tuple(shape)}")
+                         f"[{N}, {K // 2}] with [{N}, {K // 32}] (MXFP4) or int8 [{N}, {K}] with fp32 [{N}], got "
+                         f"{w.dtype} {tuple(shape)}")
     if w_scales is None:
         return W_BF16
     if w_scales.shape != (N // 32, K // 32) or w_scales.element_size() != 1 or not w_scales.is_contiguous():
@@ -193,6 +219,12 @@ def _check_mxfp4(w: torch.Tensor, w_scales: torch.Tensor, N: int, K: int) -> Non
     if (w.dtype != _U8 or w_scales.dtype != _U8 or w_scales.shape != (N, K // 32)
             or not w_scales.is_contiguous()):
         raise ValueError("MXFP4 wkv needs uint8 codes [N, K/2] and contiguous uint8 scales [N, K/32]")
+
+
+def _check_int8(w: torch.Tensor, w_scales: torch.Tensor, N: int, K: int) -> None:
+    if (w.dtype != _I8 or w.shape != (N, K) or w_scales.dtype != _F32 or w_scales.shape != (N,)
+            or not w_scales.is_contiguous()):
+        raise ValueError(f"int8 wkv needs int8 w [{N}, {K}] and contiguous fp32 scales [{N}]")
 
 
 def _device_of(*tensors) -> int:
@@ -287,13 +319,16 @@ def wkv(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor | None = None,
         kv: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """kv = bf16(x . W^T). ``w_scales`` given: MXFP8 (w = uint8 codes [N, K],
     scales [N/32, K/32]) or MXFP4 (w = uint8 packed codes [N, K/2], scales
-    [N, K/32]), told apart by w's shape."""
+    [N, K/32]), told apart by w's shape, or int8 (w = int8 [N, K], scales fp32
+    [N]; x is quantized to int8, one scale a token)."""
     L = _lib or load_library()
     if not x.is_contiguous() or not w.is_contiguous():
         raise ValueError("x and w must be contiguous")
     T, K = x.shape
     wshape = w.shape
     N = wshape[0]
+    if w_scales is not None and w_scales.dtype == _F32:
+        return _wkv_int8_weight(L, x, T, K, w, w_scales, N, kv, workspace)
     if w_scales is not None and len(wshape) == 2 and 2 * wshape[1] == K:
         _check_mxfp4(w, w_scales, N, K)
         if x.dtype != _BF16:
@@ -337,6 +372,74 @@ def _product_out(dev, w, w_scales, T, N, kv):
         return _empty_strided((T, N), (N, 1), dtype=_BF16, device=w.device)
     if kv.shape != (T, N) or kv.dtype != _BF16 or not kv.is_contiguous() or kv.get_device() != dev:
         raise ValueError(f"kv must be bf16 [{T}, {N}], contiguous, on x's device")
+    return kv
+
+
+def _wkv_int8_weight(L, x, T, K, w, w_scales, N, kv, workspace):
+    _check_int8(w, w_scales, N, K)
+    if x.dtype != _BF16:
+        raise ValueError("int8 wkv needs bf16 x (wkv_int8 takes int8 activations)")
+    dev = x.get_device()
+    kv = _product_out(dev, w, w_scales, T, N, kv)
+    need = L.engram_wkv_workspace_size(T, K, N, W_INT8)
+    if workspace is None:
+        workspace = _empty_strided((need,), (1,), dtype=_U8, device=w.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous, on x's device")
+    args = (x.data_ptr(), T, K, w.data_ptr(), w_scales.data_ptr(), W_INT8, N, kv.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+    if dev != _current_device():
+        _run_on(dev, L.engram_wkv, *args)
+    elif status := L.engram_wkv(*args, _raw_stream(dev)):
+        _check(status)
+    return kv
+
+
+def int8_quantize(x: torch.Tensor, xq: torch.Tensor | None = None, xs: torch.Tensor | None = None):
+    """bf16 [T, K] -> (int8 codes [T, K], fp32 scales [T], one a row): code * scale
+    is the row within half a step of its largest magnitude / 127."""
+    L = _lib or load_library()
+    _dense(x, "x")
+    if x.dim() != 2 or x.dtype != _BF16:
+        raise ValueError("x must be bf16 [T, K]")
+    T, K = x.shape
+    dev = _device_of(x)
+    if xq is None:
+        xq = _empty_strided((T, K), (K, 1), dtype=_I8, device=x.device)
+    if xs is None:
+        xs = _empty_strided((T,), (1,), dtype=_F32, device=x.device)
+    if xq.shape != (T, K) or xq.dtype != _I8 or not xq.is_contiguous():
+        raise ValueError(f"xq must be int8 [{T}, {K}], contiguous")
+    if xs.shape != (T,) or xs.dtype != _F32 or not xs.is_contiguous():
+        raise ValueError(f"xs must be fp32 [{T}], contiguous")
+    _device_of(x, xq, xs)
+    _run(dev, L.engram_int8_quantize, x.data_ptr(), T, K, xq.data_ptr(), xs.data_ptr())
+    return xq, xs
+
+
+def wkv_int8(xq: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+             kv: torch.Tensor | None = None) -> torch.Tensor:
+    """kv = bf16((xq . w^T) * xs[t] * w_scales[n]): the projection from int8
+    activations (int8 codes [T, K], fp32 scales [T], as int8_quantize or
+    post_pre_norm give them), w int8 [N, K], w_scales fp32 [N]. Sums are exact."""
+    L = _lib or load_library()
+    if not (xq.dtype == w.dtype == _I8 and xs.dtype == w_scales.dtype == _F32 and xq.is_contiguous()
+            and xs.is_contiguous() and w.is_contiguous() and w_scales.is_contiguous()):
+        raise ValueError("xq and w must be contiguous int8 matrices, xs and w_scales contiguous fp32")
+    T, K = xq.shape
+    N, KW = w.shape
+    if KW != K or xs.shape != (T,) or w_scales.shape != (N,):
+        raise ValueError(f"xs must be [{T}], w [N, {K}] and w_scales [N], got {tuple(xs.shape)}, {tuple(w.shape)} and "
+                         f"{tuple(w_scales.shape)}")
+    dev = xq.get_device()
+    if dev != xs.get_device():
+        raise ValueError("xq and xs are on different devices")
+    kv = _product_out(dev, w, w_scales, T, N, kv)
+    args = (xq.data_ptr(), xs.data_ptr(), T, K, w.data_ptr(), w_scales.data_ptr(), N, kv.data_ptr())
+    if dev != _current_device():
+        _run_on(dev, L.engram_wkv_int8, *args)
+    elif status := L.engram_wkv_int8(*args, _raw_stream(dev)):
+        _check(status)
     return kv
 
 
@@ -471,6 +574,120 @@ def add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None = None, weight: 
     if dev != _current_device():
         _run_on(dev, L.engram_add_rms_norm, *args)
     elif status := L.engram_add_rms_norm(*args, _raw_stream(dev)):
+        _check(status)
+    return residual_out, out, xq, xs
+
+
+def _norm_weight(weight, name, hc, dim, dev):
+    """(pointer, rows) of a norm's weight, [dim] or [hc, dim]."""
+    ws = weight.shape
+    rows = ws[0] if len(ws) == 2 else 1
+    if weight.dtype != _BF16 or not weight.is_contiguous() or not 1 <= len(ws) <= 2 or ws[-1] != dim or (
+            rows != 1 and rows != hc):
+        raise ValueError(f"{name} must be bf16 [{dim}] or [{hc}, {dim}], contiguous")
+    if weight.get_device() != dev:
+        raise ValueError(f"{name} is not on x's device")
+    return weight.data_ptr(), rows
+
+
+def _rows(t, name, shape, dev, T, hc, dim):
+    """(pointer, stride_t, stride_h) of bf16 rows [T, hc, dim] or [T, dim]."""
+    stride = t.stride()
+    if t.dtype != _BF16 or t.shape != shape or (stride[-1] != 1 and dim > 1):
+        raise ValueError(f"{name} must be bf16 {tuple(shape)}, contiguous in its last dimension")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is not on x's device")
+    # the stride of a dimension of one element is never used, whatever torch says it is
+    return t.data_ptr(), stride[0] if T > 1 else 0, stride[1] if len(shape) == 3 and hc > 1 else 0
+
+
+def post_pre_norm(x: torch.Tensor, residual: torch.Tensor | None = None, post_weight: torch.Tensor | None = None,
+                  pre_weight: torch.Tensor | None = None, gate: torch.Tensor | None = None, *,
+                  gate_act: str = "none", post_norm: bool = True, residual_scale: float = 1.0,
+                  branch_scale: float = 1.0, post_eps: float | None = None, eps: float = 1e-6,
+                  out_format: str = "bf16", q_format: str = "mxfp8", residual_out: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None, xq: torch.Tensor | None = None, xs: torch.Tensor | None = None):
+    """The norms around a block: with p = norm(x) * post_weight (post_norm false:
+    x * post_weight), s = residual_scale * residual + branch_scale * gate * p and
+    y = norm(s) * pre_weight, returns (residual_out = bf16(s), out = bf16(y),
+    xq, xs = y in 8 bits), None for what is not asked for: ``out_format`` is
+    "bf16", "mxfp8", "int8" (int8 codes, one fp32 scale a row), "both" (bf16 and
+    ``q_format``) or "none" (residual_out alone).
+
+    x and residual: bf16 [T, hc, dim] (or [T, dim]), last dimension contiguous,
+    other strides free. gate: fp32 [T, hc] (or [T]), one factor a row, or bf16 of
+    x's shape; ``gate_act`` "sigmoid" takes it through one. Weights: bf16 [dim],
+    or [hc, dim]. post_eps is eps where not given. The outputs may be given
+    (contiguous); residual_out may be residual itself and out may be x itself."""
+    L = _lib or load_library()
+    shape = x.shape
+    if len(shape) == 3:
+        T, hc, dim = shape
+        dense, rows, rows_dense = (hc * dim, dim, 1), (T, hc), (hc, 1)
+    elif len(shape) == 2:
+        (T, dim), hc = shape, 1
+        dense, rows, rows_dense = (dim, 1), (T,), (1,)
+    else:
+        raise ValueError("x must be [T, hc, dim] or [T, dim]")
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError("libengram takes device tensors only")
+    device = x.device
+    xp, xst, xsh = _rows(x, "x", shape, dev, T, hc, dim)
+    rp, rst, rsh = (None, 0, 0) if residual is None else _rows(residual, "residual", shape, dev, T, hc, dim)
+    gp, gst, gsh, gf = None, 0, 0, GATE_NONE
+    if gate is not None:
+        if gate.dtype == _F32:
+            if gate.shape != rows or gate.get_device() != dev:
+                raise ValueError(f"an fp32 gate must be {tuple(rows)}, on x's device")
+            gs = gate.stride()
+            gp, gst, gsh, gf = gate.data_ptr(), gs[0] if T > 1 else 0, gs[1] if hc > 1 else 0, GATE_ROW
+        else:
+            gp, gst, gsh = _rows(gate, "gate", shape, dev, T, hc, dim)
+            gf = GATE_CHANNEL
+    if gate_act != "none" and gate_act != "sigmoid":
+        raise ValueError('gate_act must be "none" or "sigmoid"')
+    w1, h1 = (None, 1) if post_weight is None else _norm_weight(post_weight, "post_weight", hc, dim, dev)
+    w2, h2 = (None, 1) if pre_weight is None else _norm_weight(pre_weight, "pre_weight", hc, dim, dev)
+
+    def output(t, name, dtype, size, strides):
+        if t is None:
+            return _empty_strided(size, strides, dtype=dtype, device=device)
+        if t.dtype != dtype or t.shape != size or not t.is_contiguous() or t.get_device() != dev:
+            raise ValueError(f"{name} must be {dtype} {tuple(size)}, contiguous, on x's device")
+        return t
+
+    if out_format == "bf16" or out_format == "none":
+        qf = Q_NONE
+    else:
+        q = q_format if out_format == "both" else out_format
+        if q != "mxfp8" and q != "int8":
+            raise ValueError('out_format must be "bf16", "mxfp8", "int8", "both" or "none", q_format "mxfp8" or "int8"')
+        qf = Q_INT8 if q == "int8" else Q_MXFP8
+    residual_out = output(residual_out, "residual_out", _BF16, shape, dense)
+    op = qp = sp = None
+    if out_format == "bf16" or out_format == "both":
+        out = output(out, "out", _BF16, shape, dense)
+        op = out.data_ptr()
+    elif out is not None:
+        raise ValueError(f'out is not written with out_format "{out_format}"')
+    if qf == Q_INT8:
+        xq = output(xq, "xq", _I8, shape, dense)
+        xs = output(xs, "xs", _F32, rows, rows_dense)
+        qp, sp = xq.data_ptr(), xs.data_ptr()
+    elif qf == Q_MXFP8:
+        nb = dim // 32
+        xq = output(xq, "xq", _U8, shape, dense)
+        xs = output(xs, "xs", _U8, (*rows, nb), (hc * nb, nb, 1) if len(shape) == 3 else (nb, 1))
+        qp, sp = xq.data_ptr(), xs.data_ptr()
+    elif xq is not None or xs is not None:
+        raise ValueError(f'xq and xs are not written with out_format "{out_format}"')
+    args = PostPreNormArgs(xp, xst, xsh, rp, rst, rsh, gp, gst, gsh, gf, gate_act == "sigmoid", w1, w2, h1, h2, T, hc,
+                           dim, bool(post_norm), eps if post_eps is None else post_eps, eps, residual_scale,
+                           branch_scale, qf, residual_out.data_ptr(), op, qp, sp)
+    if dev != _current_device():
+        _run_on(dev, L.engram_post_pre_norm, args)
+    elif status := L.engram_post_pre_norm(args, _raw_stream(dev)):
         _check(status)
     return residual_out, out, xq, xs
 

@@ -35,7 +35,9 @@ extern "C" {
 #endif
 
 /* ENGRAM_W_MXFP4, engram_wkv_mx and engram_add_rms_norm joined version 5
-   together: a library has all three where the symbol engram_wkv_mx is there. */
+   together: a library has all three where the symbol engram_wkv_mx is there.
+   So have ENGRAM_W_INT8, engram_int8_quantize, engram_wkv_int8 and
+   engram_post_pre_norm, all four where engram_wkv_int8 is there. */
 #define ENGRAM_ABI_VERSION 5
 
 /* Status codes. */
@@ -52,10 +54,13 @@ enum {
 enum {
   ENGRAM_W_BF16 = 0,  /* W bf16 [N, K] row-major */
   ENGRAM_W_MXFP8 = 1, /* W e4m3fn codes [N, K] row-major + E8M0 bytes [N/32, K/32] */
-  ENGRAM_W_MXFP4 = 2  /* W e2m1 codes [N, K/2] row-major, two per byte (the lower k in
+  ENGRAM_W_MXFP4 = 2, /* W e2m1 codes [N, K/2] row-major, two per byte (the lower k in
                          the low nibble) + E8M0 bytes [N, K/32], one per row and 32 k:
                          OCP MX v1.0 MXFP4; W[n,k] = e2m1(code) * 2^(byte - 127),
                          byte 255 is NaN */
+  ENGRAM_W_INT8 = 3   /* W int8 [N, K] row-major + fp32 [N], one scale per row (output
+                         channel): W[n,k] = code * scale[n]. The scales go where the
+                         other formats' bytes do: (const uint8_t*) of the floats */
 };
 
 /* Version of this ABI (ENGRAM_ABI_VERSION). */
@@ -166,6 +171,22 @@ int engram_mx_quantize(const void* x, int64_t T, int32_t K, uint8_t* xq,
                        uint8_t* xs, void* stream);
 
 /*
+ * engram_int8_quantize -- bf16 rows to 8-bit integers with one fp32 scale a row
+ *   (symmetric, per token), the activations of engram_wkv_int8. For a row with
+ *   largest magnitude a:
+ *     xs[t]    = a / 127                       (fp32)
+ *     xq[t, k] = rne(x[t, k] * (127 / a))      (fp32 quotient and product)
+ *   so codes are in -127..127. A row of zeros gets scale 0 and codes 0; a row
+ *   with an infinity or a NaN scale NaN and codes 0 (its products are NaN).
+ *   Where a < 2^-100 the row is first multiplied by 2^100 (exact); scales below
+ *   2^-126 are subnormal and lose bits.
+ *
+ *   x   bf16 [T, K];  xq  int8 [T, K];  xs  fp32 [T], 4-byte aligned.
+ *   K % 16 == 0, K <= 131056. Outputs on x or on each other: ENGRAM_EINVAL.
+ */
+int engram_int8_quantize(const void* x, int64_t T, int32_t K, int8_t* xq, float* xs, void* stream);
+
+/*
  * engram_wkv -- the wkv projection kv = bf16(x . W^T), fp32 accumulation
  *   (with MXFP8 weights less, see engram_wkv_mx), round-to-nearest-even to bf16.
  *   [P-common] Engram.__init__ / forward: bias-free linear from
@@ -175,19 +196,24 @@ int engram_mx_quantize(const void* x, int64_t T, int32_t K, uint8_t* xq,
  *   E8M0 scales per 32x32 block [N/32, K/32].
  *
  *   x          bf16 [T, K] (the staged rows [T, C, head_dim] viewed flat).
- *   w          bf16 [N, K] (ENGRAM_W_BF16), uint8 codes [N, K] (ENGRAM_W_MXFP8)
- *              or packed codes [N, K/2] (ENGRAM_W_MXFP4).
+ *   w          bf16 [N, K] (ENGRAM_W_BF16), uint8 codes [N, K] (ENGRAM_W_MXFP8),
+ *              packed codes [N, K/2] (ENGRAM_W_MXFP4) or int8 [N, K]
+ *              (ENGRAM_W_INT8).
  *   w_scales   uint8 [N/32, K/32] for MXFP8 (4-byte aligned), [N, K/32] for
- *              MXFP4 (16-byte aligned), NULL for bf16.
- *   kv         bf16 [T, N]; on no operand (MXFP4: ENGRAM_EINVAL).
+ *              MXFP4 (16-byte aligned), fp32 [N] for INT8 (16-byte aligned),
+ *              NULL for bf16.
+ *   kv         bf16 [T, N]; on no operand (MXFP4, INT8: ENGRAM_EINVAL).
  *   workspace  device scratch of at least engram_wkv_workspace_size() bytes
- *              (NULL allowed when that size is 0). For MXFP8 it holds x's
- *              MXFP8 codes and scales. 256-byte aligned.
+ *              (NULL allowed when that size is 0). For MXFP8 and INT8 it holds
+ *              x's codes and scales (INT8: on no operand and not on kv, else
+ *              ENGRAM_EINVAL). 256-byte aligned.
  *   With MXFP4 weights x stays bf16 and W enters as its bf16 values, which
  *   are exact (a value of 2^128 or more, scale bytes 253 and 254 only, is an
- *   infinity); engram_wkv_mx takes 8-bit activations.
+ *   infinity); engram_wkv_mx takes 8-bit activations. With INT8 weights x is
+ *   quantized by engram_int8_quantize's rule; the sums are engram_wkv_int8's.
  *   Shapes: bf16 needs K % 8 == 0 and N % 4 == 0; MXFP8 needs K % 128 == 0
- *   and N % 32 == 0; MXFP4 needs K % 128 == 0, N % 4 == 0 and N <= 2^28; all
+ *   and N % 32 == 0; MXFP4 needs K % 128 == 0, N % 4 == 0 and N <= 2^28; INT8
+ *   needs K % 16 == 0, K <= 131056, N % 4 == 0 and N <= 2^28; all
  *   need K <= 2^20 (32-bit buffer offsets). Other shapes return
  *   ENGRAM_EUNSUPPORTED.
  *   Kernels: a tiled GEMM; for T <= 64 a weight-streaming GEMV instead
@@ -228,6 +254,22 @@ int engram_wkv_mx(const uint8_t* xq, const uint8_t* xs, int64_t T, int32_t K, co
                   const uint8_t* w_scales, int32_t w_format, int32_t N, void* kv, void* stream);
 
 /*
+ * engram_wkv_int8 -- the projection from int8 activations, the 8-bit output of
+ *   engram_int8_quantize or engram_post_pre_norm:
+ *     kv[t, n] = bf16(float(sum_k xq[t, k] * w[n, k]) * xs[t] * w_scales[n])
+ *   The sums are exact in 32 bits (any codes -128..127), then three fp32
+ *   roundings and kv's; the same kv bit for bit whatever T and the kernel.
+ *
+ *   xq        int8 [T, K], 16-byte aligned;  xs  fp32 [T], 4-byte aligned.
+ *   w         int8 [N, K], w_scales fp32 [N], both 16-byte aligned.
+ *   kv        bf16 [T, N]; on an operand: ENGRAM_EINVAL.
+ *   Shapes: K % 16 == 0, K <= 131056, N % 4 == 0, N <= 2^28, T < 2^31; else
+ *   ENGRAM_EUNSUPPORTED.
+ */
+int engram_wkv_int8(const int8_t* xq, const float* xs, int64_t T, int32_t K, const int8_t* w, const float* w_scales,
+                    int32_t N, void* kv, void* stream);
+
+/*
  * engram_add_rms_norm -- residual addition and root-mean-square norm of the
  *   streams, with the output in bf16, in MXFP8, or both in one pass.
  *   [P-common] Engram.__init__ / forward: streams [T, hc_mult, dim] and
@@ -266,6 +308,72 @@ int engram_add_rms_norm(const void* x, int64_t x_stride_t, int64_t x_stride_h, c
                         void* out, uint8_t* xq, uint8_t* xs, void* stream);
 
 /*
+ * engram_post_pre_norm -- the norm after a block, its gate, the scaled residual
+ *   and the norm before the next block, in one pass.
+ *   [P-common] Engram.__init__ / forward: streams [T, hc_mult, dim],
+ *   rms_norm_eps, a gated branch added to each stream. For every row (t, h):
+ *     p   = x / sqrt(sum(x^2)/dim + post_eps) * post_weight[h,:]
+ *           (post_norm 0: x * post_weight[h,:])
+ *     s   = residual_scale * residual + branch_scale * (g * p)   (no residual: 0)
+ *     y   = s / sqrt(sum(s^2)/dim + eps) * pre_weight[h,:]
+ *     residual_out = bf16(s);  out = bf16(y);
+ *     xq, xs       = y in MXFP8, as engram_add_rms_norm gives it, or in int8 by
+ *                    the rule of engram_int8_quantize on the row's fp32 y
+ *   g is 1, one factor per row (ENGRAM_GATE_ROW, such as gate_out of
+ *   engram_gate) or one per channel (ENGRAM_GATE_CHANNEL), through a sigmoid
+ *   where gate_sigmoid is set. Everything is fp32 up to the outputs, each rounded
+ *   once from there (the norm is of the unrounded s); sums in a fixed order. An
+ *   |x| or |s| past about 1e18 overflows its square. NaN and infinities spread
+ *   over their row as the formulas say; an int8 row with one of them in s *
+ *   pre_weight gets scale NaN.
+ *
+ *   x, residual   bf16, element (t, h, d) at t*stride_t + h*stride_h + d (strides
+ *                 in elements, multiples of 8, >= 0; stride_h 0: one row for
+ *                 every copy). residual may be NULL.
+ *   gate          fp32 at t*stride_t + h*stride_h (any strides >= 0, 4-byte
+ *                 aligned), or bf16 laid out as x is; NULL with ENGRAM_GATE_NONE.
+ *   post_weight, pre_weight   bf16 [hc or 1, dim]; NULL: ones.
+ *   residual_out, out         optional, bf16 [T, hc, dim] contiguous; may be
+ *                 `residual` and `x` themselves (in place) where those are
+ *                 contiguous. Any other overlap of an output with another
+ *                 tensor's address range is ENGRAM_EINVAL.
+ *   xq, xs        both where q_format asks for them, NULL otherwise: uint8
+ *                 [T, hc, dim] and [T, hc, dim/32] (MXFP8), int8 [T, hc, dim] and
+ *                 fp32 [T, hc] (INT8, 4-byte aligned). At least one output.
+ *   Shapes: dim % 8 == 0 (dim % 32 == 0 for MXFP8), dim <= 16384, T*hc < 2^31;
+ *   else ENGRAM_EUNSUPPORTED. Pointers 16-byte aligned unless said.
+ */
+enum { ENGRAM_GATE_NONE = 0, ENGRAM_GATE_ROW = 1, ENGRAM_GATE_CHANNEL = 2 };
+enum { ENGRAM_Q_NONE = 0, ENGRAM_Q_MXFP8 = 1, ENGRAM_Q_INT8 = 2 };
+
+typedef struct engram_post_pre_norm_args {
+  const void* x;
+  int64_t x_stride_t, x_stride_h;
+  const void* residual;
+  int64_t residual_stride_t, residual_stride_h;
+  const void* gate;
+  int64_t gate_stride_t, gate_stride_h;
+  int32_t gate_format;
+  int32_t gate_sigmoid;     /* 0 or 1 */
+  const void* post_weight;
+  const void* pre_weight;
+  int32_t post_weight_hc;   /* rows of the weight: 1 (shared) or hc */
+  int32_t pre_weight_hc;
+  int64_t T;
+  int32_t hc, dim;
+  int32_t post_norm;        /* 0 or 1 */
+  float post_eps, eps;      /* >= 0 */
+  float residual_scale, branch_scale;
+  int32_t q_format;
+  void* residual_out;
+  void* out;
+  uint8_t* xq;
+  void* xs;
+} engram_post_pre_norm_args;
+
+int engram_post_pre_norm(const engram_post_pre_norm_args* a, void* stream);
+
+/*
  * engram_wkv_gate_partials -- the projection fused with the gate's kv-side
  *   sums: [P-rocm] _engram_gate_partials_kernel / _engram_gate_finish_kernel
  *   split the gate into per-shard partial sums and a finish step; here a
@@ -286,8 +394,8 @@ int engram_add_rms_norm(const void* x, int64_t x_stride_t, int64_t x_stride_h, c
  *   partials    fp32 [hc, T, dim/256, 2], 8-byte aligned
  *   workspace   engram_wkv_workspace_size(T, K, (hc+1)*dim, w_format) bytes
  *   Errors: ENGRAM_EINVAL for hc or dim <= 0, a NULL or misaligned pointer,
- *   or a short workspace; with MXFP4 weights, value or partials on an operand
- *   or on each other; T = 0 is a no-op. Asynchronous on `stream`.
+ *   or a short workspace; with MXFP4 or INT8 weights, value or partials on an
+ *   operand or on each other; with INT8 the workspace on any of them; T = 0 is a no-op. Asynchronous on `stream`.
  *   Shapes: as engram_wkv, plus dim % 256 == 0 and 1 <= hc <= 8; other
  *   shapes return ENGRAM_EUNSUPPORTED. This always runs the tiled GEMM
  *   (engram_wkv may take a GEMV for T <= 64).
@@ -351,7 +459,8 @@ int engram_gate(const void* hidden, const void* kv, const void* q_weight,
 /*
  * engram_forward -- one Engram layer forward: lookup -> (MXFP8 quantize) ->
  *   wkv -> gate, all on `stream`. With ENGRAM_W_MXFP4 the staged rows stay
- *   bf16 (no quantize step), as engram_wkv.
+ *   bf16 (no quantize step), as engram_wkv; with ENGRAM_W_INT8 the gather
+ *   quantizes each token's row of K (engram_int8_quantize's rule).
  *   [P-common] Engram.forward: kv = wkv(embed(hash_ids).flatten(-2)), then the
  *   fused gate over [T, hc, dim]; the staged rows and kv live in the caller's
  *   workspace (the pages keep them as persistent buffers: Engram.staged_rows,
@@ -372,7 +481,7 @@ typedef struct engram_forward_args {
   int64_t ids_stride_t;
   int64_t ids_stride_c;
   const void* w;           /* wkv weight, see engram_wkv */
-  const uint8_t* w_scales; /* MXFP8 and MXFP4, see engram_wkv */
+  const uint8_t* w_scales; /* MXFP8, MXFP4 and INT8, see engram_wkv */
   int32_t w_format;
   const void* hidden;      /* bf16 [T, hc, dim] */
   const void* q_weight;    /* bf16 [hc, dim] */
@@ -408,7 +517,7 @@ typedef struct engram_forward_args {
  *   value, so the keys never reach HBM; a small finish kernel then forms the
  *   gate and the update. ENGRAM_FORWARD_STORE_KV turns this off: kv is
  *   stored whole and the plain gate kernel reads it back (the composition of
- *   engram_wkv and engram_gate). With ENGRAM_W_MXFP4
+ *   engram_wkv and engram_gate). With ENGRAM_W_MXFP4 and ENGRAM_W_INT8
  *   the epilogue is used only where T and N fill the compute
  *   units with 256x256 tiles or kv is larger than 128 MiB. Elsewhere the option has no effect. The two
  *   routes agree to the rounding of the gate's sums (the same bf16 keys

@@ -256,6 +256,56 @@ def add_rms_norm(x_bits, residual_bits, weight_bits, eps):
     return s, y
 
 
+def post_pre_norm(x, residual, post_weight, pre_weight, gate, post_norm, residual_scale, branch_scale, post_eps, eps):
+    """The norms around a block, in fp64 on values (not bits), x ``[T, hc, dim]``:
+    p = x / sqrt(mean(x^2) + post_eps) * post_weight (without post_norm x *
+    post_weight), s = residual_scale * residual + branch_scale * gate * p, y = s /
+    sqrt(mean(s^2) + eps) * pre_weight. gate is the factor itself, broadcast to x.
+    Returns (s, y, mass): mass = |residual_scale * residual| + |branch_scale * gate
+    * p|, what the roundings of s are relative to."""
+    p = x
+    if post_norm:
+        p = p / np.sqrt(np.mean(p * p, axis=-1, keepdims=True) + post_eps)
+    if post_weight is not None:
+        p = p * post_weight
+    p = branch_scale * p
+    if gate is not None:
+        p = p * gate
+    r = 0.0 * p if residual is None else residual_scale * residual
+    s = r + p
+    y = s / np.sqrt(np.mean(s * s, axis=-1, keepdims=True) + eps)
+    if pre_weight is not None:
+        y = y * pre_weight
+    return s, y, np.abs(r) + np.abs(p)
+
+
+def int8_quantize(x_bits):
+    """bf16 rows ``[T, K]`` -> (int8 codes, fp32 scales ``[T]``): with a the row's
+    largest magnitude scale = a / 127 and code = rne(x * (127 / a)), the quotients
+    and the product in fp32 (where a < 2^-100 on the row times 2^100). Rows of
+    zeros: scale 0, codes 0; rows with an infinity or a NaN: scale NaN, codes 0."""
+    x = bf16_to_f64(x_bits).astype(np.float32)
+    a = np.abs(x).max(axis=1)
+    finite = np.isfinite(a)
+    a = np.where(finite, a, np.float32(0))
+    up = np.where(a < np.float32(2.0 ** -100), np.float32(2.0 ** 100), np.float32(1))
+    with np.errstate(divide="ignore"):
+        inv = np.where(a > 0, np.float32(127) / (a * up), np.float32(0)).astype(np.float32)
+    x = np.where(finite[:, None], x, np.float32(0))
+    codes = np.rint((x * up[:, None]).astype(np.float32) * inv[:, None]).astype(np.int8)
+    return codes, np.where(finite, a / np.float32(127), np.float32(np.nan)).astype(np.float32)
+
+
+def int8_product(xq, xs, wq, ws):
+    """kv of int8 rows ``[T, K]`` and weights ``[N, K]`` with fp32 scales ``[T]`` and
+    ``[N]``: (bf16 bits of the sums, exact, in fp32 times xs and then ws, each
+    product rounded to fp32; fp64 exact)."""
+    acc = xq.astype(np.float64) @ wq.astype(np.float64).T       # whole numbers below 2^53
+    with np.errstate(over="ignore", invalid="ignore"):
+        kv = (acc.astype(np.float32) * xs[:, None]) * ws[None, :]
+    return round_to_bf16(kv.astype(np.float64)), acc * xs[:, None].astype(np.float64) * ws[None, :].astype(np.float64)
+
+
 # ---------------------------------------------------------------------------
 # Step 1: row gather
 # ---------------------------------------------------------------------------
