@@ -13,7 +13,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libengram.so")
 SOURCES = ["abi.hip", "lookup.hip", "gate.hip", "mxq.hip", "gemm.hip", "gemv_mxfp8.hip", "gemv_bf16.hip", "decode_forward.hip",
-           "probe.hip", "rms_norm.hip", "gemv_mxfp4.hip", "gemm_fp4.hip", "post_pre_norm.hip", "int8q.hip", "gemm_int8.hip"]
+           "probe.hip", "rms_norm.hip", "gemv_mxfp4.hip", "gemm_fp4.hip", "post_pre_norm.hip", "int8q.hip", "gemm_int8.hip",
+           "gemv_int8.hip"]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

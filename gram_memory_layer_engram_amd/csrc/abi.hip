@@ -127,10 +127,12 @@ bool stage_meets(const void* stage, size_t bytes, int64_t T, int64_t K, int64_t 
 
 constexpr GateEpi kPlainStore{nullptr, nullptr, nullptr, nullptr, nullptr, 0, 0};
 
-// The projection from int8 activations.
+// The projection from int8 activations: GEMV for small T (which stores kv; `ep`
+// is for the tiled GEMM only).
 hipError_t run_int8_projection(const uint8_t* xq, const float* xs, int64_t T, int32_t K, const void* w,
                                const uint8_t* w_scales, int32_t N, void* kv, hipStream_t s, const GateEpi& ep) {
-  return launch_gemm_int8(xq, xs, T, K, (const uint8_t*)w, (const float*)w_scales, N, kv, s, ep);
+  return T <= kGemvMaxT ? launch_gemv_int8(xq, xs, T, K, (const uint8_t*)w, (const float*)w_scales, N, kv, s)
+                        : launch_gemm_int8(xq, xs, T, K, (const uint8_t*)w, (const float*)w_scales, N, kv, s, ep);
 }
 
 // Whether a format's outputs are checked against its operands (the formats that
@@ -152,6 +154,8 @@ int run_wkv(const void* x, int64_t T, int32_t K, const void* w,
   }
   uint8_t* xq = (uint8_t*)workspace;
   if (w_format == ENGRAM_W_INT8) {
+    if (gemv_int8_bf16_supported(T, K, N))
+      return hip_status(launch_gemv_int8_bf16(x, T, K, (const uint8_t*)w, (const float*)w_scales, N, kv, s));
     float* xs8 = int8_stage_scales(workspace, T, K);
     if (launch_int8_quantize(x, T, K, xq, xs8, s) != hipSuccess) return ENGRAM_EHIP;
     return hip_status(run_int8_projection(xq, xs8, T, K, w, w_scales, N, kv, s, ep));
@@ -593,7 +597,7 @@ static int run_forward(const engram_forward_args* a, int32_t K, int32_t N, uint8
   // workspace.
   const bool tiled = a->w_format == ENGRAM_W_BF16    ? !gemv_bf16_supported(a->T, K, N)
                      : a->w_format == ENGRAM_W_MXFP8 ? !gemv_mxfp8_supported(a->T, K)
-                     : a->w_format == ENGRAM_W_INT8  ? true
+                     : a->w_format == ENGRAM_W_INT8  ? a->T > kGemvMaxT
                                                      : !gemv_mxfp4_supported(a->T, K, false);
   // MXFP4 weights: only where the plain store would take the epilogue's
   // 256x256 tile as well, or kv is too large to wait for the gate in the

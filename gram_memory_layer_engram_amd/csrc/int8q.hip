@@ -70,13 +70,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void int8_quantize_kernel(co
   if (SRC != kDense && bad && a.err) atomicOr(a.err, 1);
   uint32_t m = 0;
 #pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const uint32_t w[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = max(m, max(w[i] << 16 & 0x7fff0000u, w[i] & 0x7fff0000u));
-  }
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));
+  for (int p = 0; p < P; ++p) m = int8_amax8(v[p], m);
+  m = int8_wave_amax(m);
   if constexpr (WPR > 1) {
     if (lane == 0) red[wave] = m;
     __syncthreads();
@@ -89,9 +84,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void int8_quantize_kernel(co
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     if (i0 + p * TPR >= pieces) break;
-    const float f[8] = {bf16lo(v[p].x), bf16hi(v[p].x), bf16lo(v[p].y), bf16hi(v[p].y),
-                        bf16lo(v[p].z), bf16hi(v[p].z), bf16lo(v[p].w), bf16hi(v[p].w)};
-    reinterpret_cast<uint2*>(a.xq)[t * pieces + i0 + p * TPR] = make_uint2(int8_codes4(f, r), int8_codes4(f + 4, r));
+    reinterpret_cast<uint2*>(a.xq)[t * pieces + i0 + p * TPR] = int8_codes8(v[p], r);
   }
   if (i0 == 0) a.xs[t] = r.scale;
 }

@@ -205,7 +205,8 @@ __global__ __launch_bounds__(TPR < 256 && 256 % TPR == 0 ? 256 : TPR) void post_
       for (int e = 0; e < 8; ++e) y[e] *= f[e];
     }
     if (a.q_format == kQInt8) {
-      const u32x2 c = {int8_codes4(y, q8), int8_codes4(y + 4, q8)};
+      const uint2 q = int8_codes8(y, q8);
+      const u32x2 c = {q.x, q.y};
       __builtin_nontemporal_store(c, reinterpret_cast<u32x2*>(a.xq + (base + p * 64) * 8));
     }
 #pragma unroll
