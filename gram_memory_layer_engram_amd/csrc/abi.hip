@@ -131,8 +131,8 @@ constexpr GateEpi kPlainStore{nullptr, nullptr, nullptr, nullptr, nullptr, 0, 0}
 // is for the tiled GEMM only).
 hipError_t run_int8_projection(const uint8_t* xq, const float* xs, int64_t T, int32_t K, const void* w,
                                const uint8_t* w_scales, int32_t N, void* kv, hipStream_t s, const GateEpi& ep) {
-  return T <= kGemvMaxT ? launch_gemv_int8(xq, xs, T, K, (const uint8_t*)w, (const float*)w_scales, N, kv, s)
-                        : launch_gemm_int8(xq, xs, T, K, (const uint8_t*)w, (const float*)w_scales, N, kv, s, ep);
+  return gemv_int8_supported(T, N) ? launch_gemv_int8(xq, xs, T, K, (const uint8_t*)w, (const float*)w_scales, N, kv, s)
+                                   : launch_gemm_int8(xq, xs, T, K, (const uint8_t*)w, (const float*)w_scales, N, kv, s, ep);
 }
 
 // Whether a format's outputs are checked against its operands (the formats that
@@ -597,7 +597,7 @@ static int run_forward(const engram_forward_args* a, int32_t K, int32_t N, uint8
   // workspace.
   const bool tiled = a->w_format == ENGRAM_W_BF16    ? !gemv_bf16_supported(a->T, K, N)
                      : a->w_format == ENGRAM_W_MXFP8 ? !gemv_mxfp8_supported(a->T, K)
-                     : a->w_format == ENGRAM_W_INT8  ? a->T > kGemvMaxT
+                     : a->w_format == ENGRAM_W_INT8  ? !gemv_int8_supported(a->T, N)
                                                      : !gemv_mxfp4_supported(a->T, K, false);
   // MXFP4 weights: only where the plain store would take the epilogue's
   // 256x256 tile as well, or kv is too large to wait for the gate in the

@@ -204,8 +204,10 @@ bool gemv_mxfp4_supported(int64_t T, int K, bool x_mxfp8);
 hipError_t launch_gemv_mxfp4(const void* x, const uint8_t* xs, int64_t T, int K, const void* w, const uint8_t* ws,
                              int N, void* kv, hipStream_t s);
 
-// Small-batch int8 projection (T <= kGemvMaxT, K % 16 == 0, K < 2^17, N % 4 == 0),
-// from int8 activations (xs: one scale a token), and for a few tokens from bf16 x.
+// Small-batch int8 projection (K % 16 == 0, K < 2^17, N % 4 == 0): whether it takes
+// (T, N), and its launches, from int8 activations (xs: one scale a token), and for a
+// few tokens from bf16 x.
+bool gemv_int8_supported(int64_t T, int N);
 hipError_t launch_gemv_int8(const uint8_t* xq, const float* xs, int64_t T, int K, const uint8_t* w, const float* ws, int N,
                             void* kv, hipStream_t s);
 bool gemv_int8_bf16_supported(int64_t T, int K, int N);

@@ -17,8 +17,7 @@
 // there.
 //
 // The scales wait in registers, two of the wave's 128 (64) rows and tokens a
-// lane, and go through LDS once the loop has left it: 256 different ones a
-// lane would be needed at its accumulators.
+// lane, and go through LDS once the loop has left it.
 #include "gemm_tile.h"
 
 namespace engram {
@@ -26,6 +25,40 @@ namespace engram {
 namespace {
 
 typedef int i32x16 __attribute__((ext_vector_type(16)));
+
+// The accumulators as fp32 times their scales, and to kv (store_tile). The wave's
+// scales go through its own KiB of LDS past the epilogue's staging tile: 64 * NT
+// different ones a lane would be needed at its accumulators. LDS is free.
+template <int NT>
+__device__ __forceinline__ void scale_and_store(const i32x16 (&acc)[NT][NT], const float (&wsc)[NT / 2],
+                                                const float (&xsc)[NT / 2], char* smem, uint16_t* __restrict__ kv, int T,
+                                                int N, int t0, int n0, int wn, int wt, int lane, int wave,
+                                                const GateEpi& ep) {
+  const int lrow = lane & 31, lhalf = lane >> 5;
+  float* sl = reinterpret_cast<float*>(smem + 64 * NT * 128 * NT) + wave * 256;
+#pragma unroll
+  for (int k = 0; k < NT / 2; ++k) {
+    sl[64 * k + lane] = wsc[k];
+    sl[128 + 64 * k + lane] = xsc[k];
+  }
+  wait_lgkm0();
+  float tx[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) tx[j] = sl[128 + j * 32 + lrow];
+  f32x16 out[NT][NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      // accumulator r of lane l: row 8*(r/4) + 4*(l/32) + r%4, token l%32
+      const f32x4 wv = *reinterpret_cast<const f32x4*>(sl + i * 32 + 8 * g + 4 * lhalf);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[i][j][4 * g + e] = (float)acc[i][j][4 * g + e] * tx[j] * wv[e];
+    }
+  store_tile<NT>(out, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
+}
 
 template <int NT, bool KTAIL>
 __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(NT == 4 ? 1 : 2, NT == 4 ? 1 : 2)))
@@ -171,30 +204,124 @@ void gemm_int8_kernel(const uint8_t* __restrict__ xq, const float* __restrict__ 
   wait_lgkm0();
   bare_barrier();
 
-  // the wave's scales through its own KiB of LDS past the epilogue's staging tile
-  float* sl = reinterpret_cast<float*>(smem + TILE * 2 * TILE) + wave * 256;
-#pragma unroll
-  for (int k = 0; k < NT / 2; ++k) {
-    sl[64 * k + lane] = wsc[k];
-    sl[128 + 64 * k + lane] = xsc[k];
-  }
-  wait_lgkm0();
-  float tx[NT];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) tx[j] = sl[128 + j * 32 + lrow];
-  f32x16 out[NT][NT];
+  scale_and_store<NT>(acc, wsc, xsc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
+}
+
+// 128x128 tiles where there are fewer than compute units: nothing else covers a late
+// slice there, so all of LDS is one ring of five slices (A and B, 32 KiB), fetched
+// four ahead, and the workgroups start at different slices (rows some KiB apart that
+// are all read at the same k fall on few memory channels; the order of k is free).
+// K 8192, N 8192, T 180 36.0 -> 26.0 us; K 4096, N 12288, T 180 21.1 -> 17.1; K 2048, N
+// 20480, T 128 12.9 -> 11.2. What is left is LDS: a wave's 64 x 64 reads 64 KiB a slice
+// and workgroup, its DMAs write 32, at 128 bytes a clock more than its 512 clocks of
+// matrix instructions.
+constexpr int kDeep = 5;
+
+template <bool KTAIL>
+__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void gemm_int8_deep_kernel(const uint8_t* __restrict__ xq, const float* __restrict__ xs, int T, int K,
+                           const uint8_t* __restrict__ w, const float* __restrict__ ws, int N,
+                           uint16_t* __restrict__ kv, int tiles_n, int tiles_t) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  int tn, tt;
+  tile_of(blockIdx.x, tiles_n, tiles_t, tn, tt);
+  constexpr int NT = 2, TILE = 128, CH = Q_ROW * TILE, SLOT = 2 * CH, NDMA = 4;   // of an operand and wave
+  const int n0 = tn * TILE, t0 = tt * TILE;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = (wave >> 1) * 64, wt = (wave & 1) * 64;
+  const uint32_t row_bytes = (uint32_t)K;
+  const rsrc_t ra = make_rsrc(w + (int64_t)n0 * K, (uint32_t)min(TILE, N - n0) * row_bytes);
+  const rsrc_t rb = make_rsrc(xq + (int64_t)t0 * K, (uint32_t)min(TILE, T - t0) * row_bytes);
+  const uint32_t oob = (uint32_t)TILE * row_bytes;   // at or past both ranges
+  const int nk = (K + Q_ROW - 1) / Q_ROW;
+  float wsc[1] = {ws[min(n0 + wn + lane, N - 1)]}, xsc[1] = {xs[min(t0 + wt + lane, T - 1)]};
+
+  const dma::Lane dl = dma::lane_of(wave, lane, row_bytes);
+  int at = tn % nk, left = nk, wslot = 0;      // the slice to fetch next, and its slot
+  auto fetch = [&](int i) {                    // DMA i of A (0..3), then of B
+    const uint32_t kofs = left > 0 ? (uint32_t)at * Q_ROW : oob;
+    const int q = i & 3;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(i < NDMA ? ra : rb,
+                                             (lds_ptr_t)(smem + wslot + (i < NDMA ? 0 : CH) + (wave + 4 * q) * 1024), 16,
+                                             dma::voffset(dl, q, kofs, row_bytes, oob, KTAIL), 0, 0, 0);
+  };
+  auto fetched = [&]() {
+    at = at + 1 == nk ? 0 : at + 1;
+    --left;
+    wslot = wslot == (kDeep - 1) * SLOT ? 0 : wslot + SLOT;
+  };
+
+  i32x16 acc[NT][NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      // accumulator r of lane l: row 8*(r/4) + 4*(l/32) + r%4, token l%32
-      const f32x4 wv = *reinterpret_cast<const f32x4*>(sl + i * 32 + 8 * g + 4 * lhalf);
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
+
+  const int lrow = lane & 31, lhalf = lane >> 5;
+  const int fsw = (lrow >> 1) & 7;
+  i32x4 a[2][NT], b[2][NT];
+  auto frags = [&](int slot, int kk, int c) {
+    const int piece = ((2 * kk + lhalf) ^ fsw) * 16;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) out[i][j][4 * g + e] = (float)acc[i][j][4 * g + e] * tx[j] * wv[e];
+    for (int i = 0; i < NT; ++i) {
+      b[c][i] = *reinterpret_cast<const i32x4*>(smem + slot + CH + (wt + i * 32 + lrow) * Q_ROW + piece);
+      a[c][i] = *reinterpret_cast<const i32x4*>(smem + slot + (wn + i * 32 + lrow) * Q_ROW + piece);
     }
-  store_tile<NT>(out, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
+  };
+  auto mfma_row = [&](int c, int i) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[c][i], b[c][j], acc[i][j], 0, 0, 0);
+  };
+
+  __builtin_amdgcn_sched_barrier(0);   // the scale loads first
+#pragma unroll
+  for (int d = 0; d < kDeep - 1; ++d) {
+#pragma unroll
+    for (int i = 0; i < 2 * NDMA; ++i) fetch(i);
+    fetched();
+  }
+  wait_vm<(kDeep - 2) * 2 * NDMA>();
+  asm volatile("" : "+v"(wsc[0]), "+v"(xsc[0]));
+  bare_barrier();
+  frags(0, 0, 0);
+  int slot = 0;
+  for (int d = 0; d < nk; ++d) {
+#pragma unroll
+    for (int kk = 0; kk < 3; ++kk) {
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 3 * kk; i < (kk == 2 ? 8 : 3 * kk + 3); ++i) fetch(i);
+      frags(slot, kk + 1, (kk + 1) & 1);
+      mfma_row(kk & 1, 0);
+      mfma_row(kk & 1, 1);
+      SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_DSR, 1); SGB(SG_MFMA, 1); SGB(SG_VMEM, 1); SGB(SG_DSR, 1);
+      SGB(SG_MFMA, 1);
+      if (kk < 2) SGB(SG_VMEM, 1);
+      SGB(SG_DSR, 2); SGB(SG_MFMA, 1);
+    }
+    fetched();
+    const int next = slot == (kDeep - 1) * SLOT ? 0 : slot + SLOT;
+    __builtin_amdgcn_sched_barrier(0);
+    mfma_row(1, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vm<(kDeep - 2) * 2 * NDMA>();   // slice d+1 is there
+    wait_lgkm0();
+    bare_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    frags(next, 0, 0);
+    mfma_row(1, 1);
+    SGB(SG_MFMA, 1); SGB(SG_DSR, 4); SGB(SG_MFMA, 1);
+    slot = next;
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  wait_vm<0>();   // the zero-fill DMAs of the last slices land before LDS is reused
+  wait_lgkm0();
+  bare_barrier();
+  scale_and_store<NT>(acc, wsc, xsc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, GateEpi{});
 }
 
 template <int NT>
@@ -210,7 +337,26 @@ hipError_t launch_tile(const uint8_t* xq, const float* xs, int T, int K, const u
   return hipGetLastError();
 }
 
+hipError_t launch_deep(const uint8_t* xq, const float* xs, int T, int K, const uint8_t* w, const float* ws, int N,
+                       uint16_t* kv, hipStream_t s) {
+  const int tiles_n = (N + 127) / 128, tiles_t = (T + 127) / 128;
+  constexpr int lds = kDeep * 2 * 128 * Q_ROW;
+  const auto fn = K % Q_ROW ? gemm_int8_deep_kernel<true> : gemm_int8_deep_kernel<false>;
+  const hipError_t e = set_lds((const void*)fn, lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(fn, dim3(tiles_n * tiles_t), dim3(THREADS), lds, s, xq, xs, T, K, w, ws, N, kv, tiles_n, tiles_t);
+  return hipGetLastError();
+}
+
 }  // namespace
+
+// Few tiles and enough slices that their latency counts (K 2048, N 4096: nothing
+// gained; from three quarters of the compute units on, T 128, N 28672, K 4096: 24.1 us,
+// deep 28.4).
+static bool int8_deep(int64_t T, int N, int K) {
+  const int64_t tiles = ((N + 127) / 128) * ((T + 127) / 128), cus = dev_info().num_cus;
+  return 4 * tiles <= 3 * cus && (K >= 4096 || (K >= 2048 && 2 * tiles > cus));
+}
 
 static int int8_big_columns(int64_t T, int N, int K) {
   return big_columns(T, N, K, {8000, 1400, 3200, 950, 3200, 660});
@@ -222,6 +368,7 @@ bool gemm_int8_big_tiles(int64_t T, int N, int K) { return int8_big_columns(T, N
 hipError_t launch_gemm_int8(const uint8_t* xq, const float* xs, int64_t T, int K, const uint8_t* w, const float* ws,
                             int N, void* kv, hipStream_t s, const GateEpi& ep) {
   uint16_t* out = (uint16_t*)kv;
+  if (!ep.hidden && int8_deep(T, N, K)) return launch_deep(xq, xs, (int)T, K, w, ws, N, out, s);
   const int big = ep.hidden ? (N + 255) / 256 : int8_big_columns(T, N, K);
   if (big) {
     const hipError_t e = launch_tile<4>(xq, xs, (int)T, K, w, ws, N, out, 0, big, s, ep);

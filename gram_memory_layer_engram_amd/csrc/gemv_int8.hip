@@ -1,4 +1,4 @@
-// Projection in 8-bit integers for small batches (T <= 64): kv[T, N] =
+// Projection in 8-bit integers for small batches (T <= 128): kv[T, N] =
 // bf16(float(x . W^T) * xs[t] * ws[n]), x int8 with one fp32 scale a token, or (up
 // to 8 tokens) bf16, quantized by the rule of int8_rule.h on the way.
 //
@@ -18,7 +18,9 @@
 // of it an empty kernel's; a plain read of the same bytes 7.9 us): T 1 / 16 / 32 /
 // 48 / 61 in 7.7 / 8.0 / 8.5 / 9.1 / 9.8 us (128x128 GEMM tiles 11.2 - 12.2), from
 // bf16 x T 1 / 4 / 8 7.8 / 7.9 / 8.1. Up to 32 tokens that stream bounds it. Beyond,
-// x is read by every workgroup from L2 as well, 125 KB each at T 61.
+// x is read by every workgroup from L2 as well, 125 KB each at T 61. Past 64 tokens
+// it still beats the GEMM's few tiles: N 12288, K 4096, T 96 / 128 12.0 / 14.1 against
+// 20 us, N 4096, K 2048 6.0 / 6.6 against 9.2 - 9.7.
 #include <algorithm>
 
 #include "common.h"
@@ -307,8 +309,8 @@ __global__ __launch_bounds__(NT * KS * 64) void gemv_int8_slice_kernel(const Gem
     wait_lgkm0();
     slot = slot == lds + (D - 1) * S::SLOT ? lds : slot + S::SLOT;
   }
+  wait_vm<0>();   // the last slices' DMAs of zeros: none may land once the wave has ended
   if constexpr (KS > 1) {
-    wait_vm<0>();
     bare_barrier();   // no DMA and no read is left
     i32x4* red = reinterpret_cast<i32x4*>(lds);
 #pragma unroll
@@ -383,20 +385,27 @@ hipError_t run_reg_bf16(const GemvI8Args& a, hipStream_t s) {
 // and the slice's halves on two waves. Beyond: smaller rings, more workgroups on a
 // compute unit; from 33 tokens on seven row tiles where the compute units then have
 // fewer rows in their fullest round (N 28672, T 61: 23.9 us, three 31.6; N 20480
-// 10.4, three 9.8).
+// 10.4, three 9.8). Past 64 tokens six or eight waves, a token tile each, are enough
+// without halves.
 template <int NT>
 hipError_t run_slices(const GemvI8Args& a, hipStream_t s) {
   const int tiles = (a.N + 15) / 16, cus = dev_info().num_cus;
+  auto rows = [&](int rt) { return ((tiles + rt - 1) / rt + cus - 1) / cus * rt; };
   if constexpr (NT == 1) {
     return tiles <= cus ? slices<1, 1, 2, 4>(a, s) : slices<1, 1, 1, 4>(a, s);
   } else if constexpr (NT == 2) {
     return tiles <= cus ? slices<1, 2, 1, 4>(a, s) : tiles <= 4 * cus ? slices<2, 2, 2, 4>(a, s) : slices<2, 2, 1, 3>(a, s);
-  } else {
-    auto rows = [&](int rt) { return ((tiles + rt - 1) / rt + cus - 1) / cus * rt; };
+  } else if constexpr (NT <= 4) {
     return tiles <= cus        ? slices<1, NT, 1, 4>(a, s)
            : tiles <= 4 * cus  ? slices<3, NT, 2, 4>(a, s)
            : rows(7) < rows(3) ? slices<7, NT, 2, 3>(a, s)
                                : slices<3, NT, 2, 3>(a, s);
+  } else if constexpr (NT == 6) {
+    return tiles <= cus                               ? slices<1, NT, 1, 3>(a, s)
+           : tiles > 4 * cus && rows(7) < rows(3) ? slices<7, NT, 1, 3>(a, s)
+                                                      : slices<3, NT, 1, 3>(a, s);
+  } else {
+    return tiles <= cus ? slices<1, NT, 1, 3>(a, s) : slices<3, NT, 1, 3>(a, s);
   }
 }
 
@@ -409,7 +418,18 @@ hipError_t launch_gemv_int8(const uint8_t* xq, const float* xs, int64_t T, int K
                             void* kv, hipStream_t s) {
   const GemvI8Args a{xq, xs, w, ws, (uint16_t*)kv, (int)T, K, N};
   if (T <= 8 ? K <= 8192 : T <= 16 && K <= 4096 && (N + 15) / 16 <= 2 * dev_info().num_cus) return run_reg(a, s);
-  return T <= 16 ? run_slices<1>(a, s) : T <= 32 ? run_slices<2>(a, s) : T <= 48 ? run_slices<3>(a, s) : run_slices<4>(a, s);
+  return T <= 16   ? run_slices<1>(a, s)
+         : T <= 32 ? run_slices<2>(a, s)
+         : T <= 48 ? run_slices<3>(a, s)
+         : T <= 64 ? run_slices<4>(a, s)
+         : T <= 96 ? run_slices<6>(a, s)
+                   : run_slices<8>(a, s);
+}
+
+// Up to 96 tokens, and up to 128 while the row tiles are few: with many the GEMM's
+// tiles fill the compute units (T 128, N 20480, K 2048: 11.2 us, here 13.3).
+bool gemv_int8_supported(int64_t T, int N) {
+  return T >= 1 && (T <= 96 || (T <= 128 && (N + 15) / 16 <= 4 * dev_info().num_cus));
 }
 
 // Quantizing on the way pays while the launch it saves (2.0 to 2.4 us) is more than

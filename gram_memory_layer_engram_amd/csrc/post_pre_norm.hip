@@ -72,6 +72,9 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   return v;
 }
 
+// A barrier for LDS alone: __syncthreads() also waits for every store in flight.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 // Pointers are not __restrict__: residual_out may be residual and out may be
 // x; a thread reads all of its pieces before it writes any of them.
 template <int P, int TPR>
@@ -110,7 +113,7 @@ __global__ __launch_bounds__(TPR < 256 && 256 % TPR == 0 ? 256 : TPR) void post_
       if (a.pre_weight) qv[p] = w2[p * 64];
     }
   }
-  float rg = a.branch_scale;
+  float rg = a.branch_scale;   // every factor of the row
   if (a.gate_format == kGateRow && live) {
     const float g = ((const float*)a.gate)[t * a.g_st + h * a.g_sh];
     rg *= a.sigmoid ? sigmoid(g) : g;
@@ -124,26 +127,27 @@ __global__ __launch_bounds__(TPR < 256 && 256 % TPR == 0 ? 256 : TPR) void post_
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum = fmaf(s[p][e], s[p][e], sum);
   }
-  float inv1 = 1.f;
   if (a.post_norm) {
     sum = wave_sum(sum);
     if constexpr (WPR > 1) {
       if (lane == 0) red[0][wave] = sum;
-      __syncthreads();
+      lds_barrier();
       sum = 0.f;
 #pragma unroll
       for (int w = 0; w < WPR; ++w) sum += red[0][w0 + w];
     }
-    inv1 = 1.0f / sqrtf(sum / (float)a.dim + a.post_eps);
+    rg *= 1.0f / sqrtf(sum / (float)a.dim + a.post_eps);
   }
 
+  // s, stored at once, and in its place s * pre_weight
   sum = 0.f;
-  uint32_t amax = 0;   // of s * pre_weight; magnitudes order like unsigned integers, NaN above infinity
+  const int64_t base = row * pieces + i0;
+  uint32_t amax[P];   // magnitudes order like unsigned integers, NaN above infinity
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     float f[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s[p][e] *= inv1;
+    for (int e = 0; e < 8; ++e) s[p][e] *= rg;
     if (a.post_weight) {
       unpack8(pv[p], f);
 #pragma unroll
@@ -154,72 +158,69 @@ __global__ __launch_bounds__(TPR < 256 && 256 % TPR == 0 ? 256 : TPR) void post_
 #pragma unroll
       for (int e = 0; e < 8; ++e) s[p][e] *= a.sigmoid ? sigmoid(f[e]) : f[e];
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s[p][e] *= rg;
     if (a.residual) {
       unpack8(rv[p], f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) s[p][e] = fmaf(a.residual_scale, f[e], s[p][e]);
     }
+    if (a.residual_out && live && i0 + p * 64 < pieces) store16_nt(a.residual_out + (base + p * 64) * 8, pack8(s[p]));
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum = fmaf(s[p][e], s[p][e], sum);
-    if (a.q_format == kQInt8) {
+    if (a.pre_weight) {
       unpack8(qv[p], f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        amax = max(amax, __float_as_uint(a.pre_weight ? s[p][e] * f[e] : s[p][e]) & 0x7fffffffu);
+      for (int e = 0; e < 8; ++e) s[p][e] *= f[e];
+    }
+    amax[p] = 0;
+    if (a.q_format == kQInt8) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax[p] = max(amax[p], __float_as_uint(s[p][e]) & 0x7fffffffu);
     }
   }
   sum = wave_sum(sum);
-  if (a.q_format == kQInt8) amax = wave_max(amax);
+  uint32_t rmax = 0;
+  if (a.q_format == kQInt8) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) rmax = max(rmax, amax[p]);
+    rmax = wave_max(rmax);
+  }
   if constexpr (WPR > 1) {
     if (lane == 0) {
       red[1][wave] = sum;
-      redm[wave] = amax;
+      redm[wave] = rmax;
     }
-    __syncthreads();
+    lds_barrier();
     sum = 0.f;
 #pragma unroll
     for (int w = 0; w < WPR; ++w) {
       sum += red[1][w0 + w];
-      amax = max(amax, redm[w0 + w]);
+      rmax = max(rmax, redm[w0 + w]);
     }
   }
   const float inv2 = 1.0f / sqrtf(sum / (float)a.dim + a.eps);
   if (!live) return;
 
-  const Int8Row q8 = int8_row(amax, inv2);
-  const int64_t base = row * pieces + i0;
+  const Int8Row q8 = int8_row(rmax, inv2);
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     // the four lanes of an MX block are live together (dim % 32 == 0 then)
     if (i0 + p * 64 >= pieces) break;
-    if (a.residual_out) store16_nt(a.residual_out + (base + p * 64) * 8, pack8(s[p]));
-    float y[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = s[p][e];
-    if (a.pre_weight) {
-      float f[8];
-      unpack8(qv[p], f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] *= f[e];
-    }
     if (a.q_format == kQInt8) {
-      const uint2 q = int8_codes8(y, q8);
+      const uint2 q = int8_codes8(s[p], q8);
       const u32x2 c = {q.x, q.y};
       __builtin_nontemporal_store(c, reinterpret_cast<u32x2*>(a.xq + (base + p * 64) * 8));
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] *= inv2;
-    if (a.out) store16_nt(a.out + (base + p * 64) * 8, pack8(y));
+    for (int e = 0; e < 8; ++e) s[p][e] *= inv2;
+    if (a.out) store16_nt(a.out + (base + p * 64) * 8, pack8(s[p]));
     if (a.q_format == kQMx) {
       uint32_t m = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(y[e]) & 0x7fffffffu);
+      for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(s[p][e]) & 0x7fffffffu);
       m = max(m, quad_xor1(m));
       m = max(m, quad_xor2(m));
       uint32_t packed[2];
-      const int byte = mx_piece_f32(y, m, packed);
+      const int byte = mx_piece_f32(s[p], m, packed);
       const u32x2 c = {packed[0], packed[1]};
       __builtin_nontemporal_store(c, reinterpret_cast<u32x2*>(a.xq + (base + p * 64) * 8));
       if ((lane & 3) == 0) sbytes[wave][p * 16 + (lane >> 2)] = (uint8_t)byte;

@@ -26,6 +26,7 @@ import pytest
 import torch
 
 from oracle import engram_oracle as o
+from tests import _int8_shapes as S
 from tests._block_inputs import BF16_U, F32_U, bf16, mxfp8_rows
 from tests._util import bf16_values, bits, sample_tokens, u8
 
@@ -74,12 +75,8 @@ def _check_kv(kv, xq, xs, wq, ws, what):
     assert np.array_equal(bits(kv), want), what
 
 
-# K: one 16-byte piece, odd counts of them, whole and ragged slices of 128, long ones
-KN = [(16, 4), (48, 20), (128, 96), (144, 36), (256, 260), (496, 132), (2048, 1280), (2064, 516), (4096, 512)]
-
-
-@pytest.mark.parametrize("K,N", KN)
-@pytest.mark.parametrize("T", [1, 2, 7, 16, 17, 33, 48, 64, 65, 130, 300])
+@pytest.mark.parametrize("K,N", S.KN)
+@pytest.mark.parametrize("T", S.T)
 def test_int8_products(T, K, N):
     E = _E()
     _say(f"int8 {T} {K} {N}")
@@ -98,8 +95,22 @@ def test_int8_products(T, K, N):
     _check_kv(E.wkv(x.to(DEV), _dev(wq), _dev(ws)), cq, cs, wq, ws, "wkv")
 
 
-@pytest.mark.parametrize("T,K,N", [(1500, 256, 20480), (1500, 512, 20476), (515, 1024, 20480), (515, 1136, 20476),
-                                   (4096, 400, 5116), (3000, 144, 7172), (4000, 4112, 5120)])
+@pytest.mark.parametrize("T,K,N", S.SMALL)
+def test_int8_small_batches(T, K, N):
+    """Row tiles in each of the ranges that the small-batch kernels are chosen by."""
+    E = _E()
+    _say(f"int8 small {T} {K} {N}")
+    rng = np.random.default_rng(K + N)
+    xq, xs = _int8(rng, T, K)
+    wq, ws = _int8(rng, N, K)
+    wd, sd = _dev(wq), _dev(ws)
+    _check_kv(E.wkv_int8(_dev(xq), _dev(xs), wd, sd), xq, xs, wq, ws, "wkv_int8")
+    if T <= 8:
+        x = bf16(rng, T, K)
+        _check_kv(E.wkv(x.to(DEV), wd, sd), *o.int8_quantize(bits(x)), wq, ws, "wkv")
+
+
+@pytest.mark.parametrize("T,K,N", S.TILES)
 def test_int8_many_tiles(T, K, N):
     E = _E()
     _say(f"int8 tiles {T} {K} {N}")
@@ -175,9 +186,7 @@ def test_int8_weight_offsets_past_32_bits():
 
 # --------------------------------------------------------------- quantizer --
 
-@pytest.mark.parametrize("T,K", [(1, 16), (5, 48), (3, 512), (2, 528), (1, 2048), (4, 2064), (7, 8192), (2, 8208),
-                                 (1, 32768), (3, 40000), (2, 131056), (300, 512), (1029, 1040), (300, 2048),
-                                 (259, 8192), (257, 16400), (260, 32768), (258, 40016)])
+@pytest.mark.parametrize("T,K", S.ROWS)
 def test_int8_quantizer(T, K):
     E = _E()
     _say(f"quantize {T} {K}")
@@ -463,9 +472,7 @@ def _forward_case(rng, T, dim, hc, C, hd, R, fp8_table):
     return wq, ws, ids, hidden, q, k, mask, table, ts, rows
 
 
-@pytest.mark.parametrize("T,dim,hc,C,hd", [(1, 512, 4, 8, 64), (16, 256, 2, 8, 64), (40, 136, 2, 8, 64), (64, 512, 1, 6, 64),
-                                           (65, 512, 2, 8, 64), (300, 512, 4, 8, 64), (257, 264, 2, 8, 64),
-                                           (90, 136, 2, 3, 32), (5, 256, 2, 16, 128), (1, 256, 2, 40, 1024)])
+@pytest.mark.parametrize("T,dim,hc,C,hd", S.FORWARD)
 @pytest.mark.parametrize("fp8_table", [False, True])
 def test_forward_int8(T, dim, hc, C, hd, fp8_table):
     """The layer's forward on an int8 wkv weight against the oracle's steps, the
@@ -514,12 +521,12 @@ def test_forward_int8_bad_ids():
     assert torch.equal(out, E.gate(hidden, kv, q, k))
 
 
-@pytest.mark.parametrize("C", [8, 5])
-def test_forward_int8_gate_epilogue(C):
+@pytest.mark.parametrize("C,hd", [(16, 64), (9, 112)])
+def test_forward_int8_gate_epilogue(C, hd):
     """Enough tokens that the default is the GEMM's gate epilogue."""
     E = _E()
     rng = np.random.default_rng(21)
-    T, dim, hc, hd = 1491, 4096, 4, 48
+    T, dim, hc = 1491, 4096, 4
     wq, ws, ids, hidden, q, k, mask, table, ts, rows = _forward_case(rng, T, dim, hc, C, hd, 301, False)
     wd, sd, idd = _dev(wq), _dev(ws), _dev(ids)
     gates = [torch.full((T, hc), -1.0, dtype=torch.float32, device=DEV) for _ in range(2)]
@@ -630,7 +637,7 @@ def test_every_route_gives_the_same_kv():
     x = bf16(rng, 700, K).to(DEV)
     q, s = E.int8_quantize(x)
     full = E.wkv_int8(q, s, wd, sd)
-    for T in (1, 5, 16, 17, 40, 64, 65, 128, 300, 600):
+    for T in (1, 5, 8, 9, 16, 17, 40, 64, 65, 96, 100, 128, 129, 300, 600):
         assert torch.equal(E.wkv_int8(q[:T], s[:T], wd, sd), full[:T]), T
         assert torch.equal(E.wkv(x[:T], wd, sd), full[:T]), T
 
