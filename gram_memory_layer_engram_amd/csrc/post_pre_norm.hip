@@ -19,6 +19,17 @@
 // Layout: as rms_norm.hip. A row is owned by TPR threads, each wave a contiguous
 // run of P * 64 pieces of 8 elements, all of x, residual, gate and both weights
 // in registers before the first sum: one pass, two reductions.
+//
+// Bound: HBM. Per element 2 bytes of x, 4 of the stream in and out, 2 of a channel
+// gate, 2 of out or 1 and a bit of codes; weights come from L2. 8192 tokens of four
+// streams of 4096, x of its own for each: int8 162 us (939 MB, 5.8 TB/s), bf16 181 us
+// (5.9); one x for four streams, MXFP8 142-147 us (742 MB, 5.1), bf16 157 (5.6): there
+// the rows' own latency shows, 16 waves a compute unit with both sums to wait for. One
+// token: 3.8 us, a launch, one trip to memory and two sums.
+// Without profit: the weights loaded behind the first sum (fewer registers: 2-8%
+// slower); one workgroup for the copies that share x, its norm taken once, the next
+// copy's operands in flight (163 us); a persistent grid with the next row in flight and
+// the weights kept in registers (161 us); larger and smaller workgroups.
 #include <algorithm>
 
 #include "common.h"
@@ -252,8 +263,10 @@ hipError_t launch(const PostPreNormArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Few rows: latency counts, one piece a thread. Many: four pieces a thread keep
-// more bytes in flight per wave.
+// Few rows: latency counts, one piece a thread (T 61, four rows of 2048 bf16: 3.7 us,
+// two pieces 4.1). Some more: two (400 rows of 4096: 4.9, four pieces 5.8, one 5.5).
+// Many: four keep more bytes in flight per wave (2000 rows of 4096 mxfp8 10.5, two
+// 11.5).
 hipError_t launch_post_pre_norm(const PostPreNormArgs& a, hipStream_t s) {
   const int pieces = a.dim / 8;
   if (pieces <= 64) return launch<1, 64>(a, s);
@@ -265,6 +278,12 @@ hipError_t launch_post_pre_norm(const PostPreNormArgs& a, hipStream_t s) {
     return launch<2, 1024>(a, s);   // dim <= 16384
   }
   if (pieces <= 128) return launch<2, 64>(a, s);
+  if (a.rows <= 3 * dev_info().num_cus) {
+    if (pieces <= 256) return launch<2, 128>(a, s);
+    if (pieces <= 512) return launch<2, 256>(a, s);
+    if (pieces <= 1024) return launch<2, 512>(a, s);
+    return launch<2, 1024>(a, s);
+  }
   if (pieces <= 256) return launch<4, 64>(a, s);
   if (pieces <= 512) return launch<4, 128>(a, s);
   if (pieces <= 1024) return launch<4, 256>(a, s);

@@ -294,7 +294,8 @@ def _cut(t, rows):
 SHAPES = [(1, 1, 32), (1, 4, 4096), (3, 2, 64), (5, 3, 544), (17, 1, 1024), (2, 8, 2080), (33, 4, 2048), (4, 2, 4128),
           (9, 1, 7168), (3, 4, 8192), (2, 1, 8224), (3, 2, 16384), (700, 4, 256), (1030, 1, 512), (150, 2, 544),
           (300, 1, 1024), (131, 3, 2048), (97, 4, 2080), (70, 4, 4096), (65, 4, 4128), (259, 1, 7168), (90, 3, 8224),
-          (260, 1, 16384)]
+          (260, 1, 16384), (800, 1, 2048), (200, 4, 4096), (1000, 1, 4096), (100, 8, 8192), (400, 2, 7168),
+          (300, 3, 16384)]
 
 
 @pytest.mark.parametrize("T,hc,dim", SHAPES)
