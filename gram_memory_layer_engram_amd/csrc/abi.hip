@@ -321,7 +321,12 @@ int engram_int8_quantize(const void* x, int64_t T, int32_t K, int8_t* xq, float*
 
 size_t engram_wkv_workspace_size(int64_t T, int32_t K, int32_t N,
                                  int32_t w_format) {
-  (void)N;
+  if (T <= 0 || K <= 0 || (w_format == ENGRAM_W_INT8 && gemv_int8_bf16_supported(T, K, N))) return 0;
+  return wkv_scratch_bytes(T, K, w_format);
+}
+
+size_t engram_wkv_gate_partials_workspace_size(int64_t T, int32_t K, int32_t hc, int32_t dim, int32_t w_format) {
+  (void)hc, (void)dim;
   return T <= 0 || K <= 0 ? 0 : wkv_scratch_bytes(T, K, w_format);
 }
 
@@ -350,7 +355,7 @@ int engram_wkv_gate_partials(const void* x, int64_t T, int32_t K, const void* w,
           meet(o, {q_weight, (int64_t)2 * hc * dim}) || meet(o, {k_weight, (int64_t)2 * hc * dim}))
         return ENGRAM_EINVAL;
   }
-  const size_t need = engram_wkv_workspace_size(T, K, N, w_format);
+  const size_t need = engram_wkv_gate_partials_workspace_size(T, K, hc, dim, w_format);
   if (workspace_bytes < need || (need && (!workspace || ((uintptr_t)workspace % kAlign))))
     return ENGRAM_EINVAL;
   if (w_format == ENGRAM_W_INT8) {

@@ -78,6 +78,7 @@ EXPORTS = {
     "engram_mx_quantize": (_i32, [_vp, _i64, _i32, _vp, _vp, _vp]),
     "engram_wkv_workspace_size": (_sz, [_i64, _i32, _i32, _i32]),
     "engram_wkv": (_i32, [_vp, _i64, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _sz, _vp]),
+    "engram_wkv_gate_partials_workspace_size": (_sz, [_i64, _i32, _i32, _i32, _i32]),
     "engram_wkv_gate_partials": (_i32, [_vp, _i64, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp,
                                         _vp, _sz, _vp]),
     "engram_wkv_mx": (_i32, [_vp, _vp, _i64, _i32, _vp, _vp, _i32, _i32, _vp, _vp]),
@@ -381,13 +382,15 @@ def _wkv_int8_weight(L, x, T, K, w, w_scales, N, kv, workspace):
         raise ValueError("int8 wkv needs bf16 x (wkv_int8 takes int8 activations)")
     dev = x.get_device()
     kv = _product_out(dev, w, w_scales, T, N, kv)
-    need = L.engram_wkv_workspace_size(T, K, N, W_INT8)
-    if workspace is None:
+    wp, need = None, L.engram_wkv_workspace_size(T, K, N, W_INT8)
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous, on x's device")
+        wp, need = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif need:
         workspace = _empty_strided((need,), (1,), dtype=_U8, device=w.device)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous, on x's device")
-    args = (x.data_ptr(), T, K, w.data_ptr(), w_scales.data_ptr(), W_INT8, N, kv.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size())
+        wp = workspace.data_ptr()
+    args = (x.data_ptr(), T, K, w.data_ptr(), w_scales.data_ptr(), W_INT8, N, kv.data_ptr(), wp, need)
     if dev != _current_device():
         _run_on(dev, L.engram_wkv, *args)
     elif status := L.engram_wkv(*args, _raw_stream(dev)):
@@ -601,6 +604,11 @@ def _rows(t, name, shape, dev, T, hc, dim):
     return t.data_ptr(), stride[0] if T > 1 else 0, stride[1] if len(shape) == 3 and hc > 1 else 0
 
 
+def _check_output(t, name, dtype, size, dev):
+    if t.dtype != dtype or t.shape != size or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name} must be {dtype} {tuple(size)}, contiguous, on x's device")
+
+
 def post_pre_norm(x: torch.Tensor, residual: torch.Tensor | None = None, post_weight: torch.Tensor | None = None,
                   pre_weight: torch.Tensor | None = None, gate: torch.Tensor | None = None, *,
                   gate_act: str = "none", post_norm: bool = True, residual_scale: float = 1.0,
@@ -650,13 +658,6 @@ def post_pre_norm(x: torch.Tensor, residual: torch.Tensor | None = None, post_we
     w1, h1 = (None, 1) if post_weight is None else _norm_weight(post_weight, "post_weight", hc, dim, dev)
     w2, h2 = (None, 1) if pre_weight is None else _norm_weight(pre_weight, "pre_weight", hc, dim, dev)
 
-    def output(t, name, dtype, size, strides):
-        if t is None:
-            return _empty_strided(size, strides, dtype=dtype, device=device)
-        if t.dtype != dtype or t.shape != size or not t.is_contiguous() or t.get_device() != dev:
-            raise ValueError(f"{name} must be {dtype} {tuple(size)}, contiguous, on x's device")
-        return t
-
     if out_format == "bf16" or out_format == "none":
         qf = Q_NONE
     else:
@@ -664,21 +665,34 @@ def post_pre_norm(x: torch.Tensor, residual: torch.Tensor | None = None, post_we
         if q != "mxfp8" and q != "int8":
             raise ValueError('out_format must be "bf16", "mxfp8", "int8", "both" or "none", q_format "mxfp8" or "int8"')
         qf = Q_INT8 if q == "int8" else Q_MXFP8
-    residual_out = output(residual_out, "residual_out", _BF16, shape, dense)
+    if residual_out is None:
+        residual_out = _empty_strided(shape, dense, dtype=_BF16, device=device)
+    else:
+        _check_output(residual_out, "residual_out", _BF16, shape, dev)
     op = qp = sp = None
     if out_format == "bf16" or out_format == "both":
-        out = output(out, "out", _BF16, shape, dense)
+        if out is None:
+            out = _empty_strided(shape, dense, dtype=_BF16, device=device)
+        else:
+            _check_output(out, "out", _BF16, shape, dev)
         op = out.data_ptr()
     elif out is not None:
         raise ValueError(f'out is not written with out_format "{out_format}"')
-    if qf == Q_INT8:
-        xq = output(xq, "xq", _I8, shape, dense)
-        xs = output(xs, "xs", _F32, rows, rows_dense)
-        qp, sp = xq.data_ptr(), xs.data_ptr()
-    elif qf == Q_MXFP8:
-        nb = dim // 32
-        xq = output(xq, "xq", _U8, shape, dense)
-        xs = output(xs, "xs", _U8, (*rows, nb), (hc * nb, nb, 1) if len(shape) == 3 else (nb, 1))
+    if qf != Q_NONE:
+        if qf == Q_INT8:
+            qt, st, sshape, sdense = _I8, _F32, rows, rows_dense
+        else:
+            nb = dim // 32
+            qt, st, sshape = _U8, _U8, (*rows, nb)
+            sdense = (hc * nb, nb, 1) if len(shape) == 3 else (nb, 1)
+        if xq is None:
+            xq = _empty_strided(shape, dense, dtype=qt, device=device)
+        else:
+            _check_output(xq, "xq", qt, shape, dev)
+        if xs is None:
+            xs = _empty_strided(sshape, sdense, dtype=st, device=device)
+        else:
+            _check_output(xs, "xs", st, sshape, dev)
         qp, sp = xq.data_ptr(), xs.data_ptr()
     elif xq is not None or xs is not None:
         raise ValueError(f'xq and xs are not written with out_format "{out_format}"')
@@ -716,7 +730,7 @@ def wkv_gate_partials(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor |
         raise ValueError(f"partials must be fp32 [{hc}, {T}, {dim // 256}, 2]")
     _dense(value, "value")
     _dense(partials, "partials")
-    need = L.engram_wkv_workspace_size(T, K, N, fmt)
+    need = L.engram_wkv_gate_partials_workspace_size(T, K, hc, dim, fmt)
     if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     ws_bytes = 0 if workspace is None else workspace.numel()

@@ -36,8 +36,9 @@ extern "C" {
 
 /* ENGRAM_W_MXFP4, engram_wkv_mx and engram_add_rms_norm joined version 5
    together: a library has all three where the symbol engram_wkv_mx is there.
-   So have ENGRAM_W_INT8, engram_int8_quantize, engram_wkv_int8 and
-   engram_post_pre_norm, all four where engram_wkv_int8 is there. */
+   So have ENGRAM_W_INT8, engram_int8_quantize, engram_wkv_int8,
+   engram_wkv_gate_partials_workspace_size and engram_post_pre_norm, all where
+   engram_wkv_int8 is there. */
 #define ENGRAM_ABI_VERSION 5
 
 /* Status codes. */
@@ -206,7 +207,9 @@ int engram_int8_quantize(const void* x, int64_t T, int32_t K, int8_t* xq, float*
  *   workspace  device scratch of at least engram_wkv_workspace_size() bytes
  *              (NULL allowed when that size is 0). For MXFP8 and INT8 it holds
  *              x's codes and scales (INT8: on no operand and not on kv, else
- *              ENGRAM_EINVAL). 256-byte aligned.
+ *              ENGRAM_EINVAL; none for up to 8 tokens of K <= 4096 where the
+ *              weight is at most 64 MiB, which are quantized in the product's
+ *              launch). 256-byte aligned.
  *   With MXFP4 weights x stays bf16 and W enters as its bf16 values, which
  *   are exact (a value of 2^128 or more, scale bytes 253 and 254 only, is an
  *   infinity); engram_wkv_mx takes 8-bit activations. With INT8 weights x is
@@ -392,7 +395,9 @@ int engram_post_pre_norm(const engram_post_pre_norm_args* a, void* stream);
  *   hidden      bf16 [T, hc, dim];  q_weight, k_weight  bf16 [hc, dim]
  *   value       bf16 [T, dim] (kv's value block)
  *   partials    fp32 [hc, T, dim/256, 2], 8-byte aligned
- *   workspace   engram_wkv_workspace_size(T, K, (hc+1)*dim, w_format) bytes
+ *   workspace   engram_wkv_gate_partials_workspace_size() bytes: for all formats
+ *               but INT8 those of engram_wkv_workspace_size(T, K, (hc+1)*dim,
+ *               w_format)
  *   Errors: ENGRAM_EINVAL for hc or dim <= 0, a NULL or misaligned pointer,
  *   or a short workspace; with MXFP4 or INT8 weights, value or partials on an
  *   operand or on each other; with INT8 the workspace on any of them; T = 0 is a no-op. Asynchronous on `stream`.
@@ -400,6 +405,7 @@ int engram_post_pre_norm(const engram_post_pre_norm_args* a, void* stream);
  *   shapes return ENGRAM_EUNSUPPORTED. This always runs the tiled GEMM
  *   (engram_wkv may take a GEMV for T <= 64).
  */
+size_t engram_wkv_gate_partials_workspace_size(int64_t T, int32_t K, int32_t hc, int32_t dim, int32_t w_format);
 int engram_wkv_gate_partials(const void* x, int64_t T, int32_t K, const void* w,
                              const uint8_t* w_scales, int32_t w_format, int32_t hc,
                              int32_t dim, const void* hidden, const void* q_weight,

@@ -124,23 +124,31 @@ def test_product_refusals(lib):
 
 
 def test_wkv_and_partials_with_int8_weights_refuse(lib):
-    need = lib.engram_wkv_workspace_size(3, 64, 32, I8)
-    assert need == 256 + 256
+    # a few tokens are quantized in the product's launch
+    assert [lib.engram_wkv_workspace_size(T, 64, 32, I8) for T in (0, 1, 8, 9)] == [0, 0, 0, 1024]
+    assert lib.engram_wkv_workspace_size(8, 4096, 16384, I8) == 0
+    assert lib.engram_wkv_workspace_size(8, 4112, 64, I8) == 8 * 4112 + 256 - 8 * 4112 % 256 + 256
+    assert lib.engram_wkv_workspace_size(8, 4096, 16388, I8) == 8 * 4096 + 256
+    need = lib.engram_wkv_workspace_size(12, 64, 32, I8)
+    assert need == 768 + 256
     WK = 13 << 28
 
     def f(kv=KV, ws=WK, n=need, x=X, K=64):
-        return lib.engram_wkv(x, 3, K, W, WS, I8, 32, kv, ws, n, None)
+        return lib.engram_wkv(x, 12, K, W, WS, I8, 32, kv, ws, n, None)
 
     assert f(n=need - 1) == INV and f(ws=None) == INV and f(ws=WK + 16) == INV and f(K=72) == UNS
-    for base in (X, X + 256, W, W + 1792, WS, KV):
+    for base in (X, X + 1280, W, W + 1792, WS, KV, KV + 512):
         assert f(ws=base) == INV, hex(base)
     for kv in (X, W + 2032, WS + 112):
         assert f(kv=kv) == INV
+        assert lib.engram_wkv(X, 3, 64, W, WS, I8, 32, kv, None, 0, None) == INV
     assert lib.engram_wkv(X, 3, 64, W, None, I8, 32, KV, WK, need, None) == INV
     assert lib.engram_wkv(None, 0, 64, None, None, I8, 32, None, None, 0, None) == OK
 
     T, K, hc, dim = 4, 256, 2, 256
-    need = lib.engram_wkv_workspace_size(T, K, (hc + 1) * dim, I8)
+    need = lib.engram_wkv_gate_partials_workspace_size(T, K, hc, dim, I8)
+    assert need == 1024 + 256 and lib.engram_wkv_gate_partials_workspace_size(T, K, hc, dim, 2) == 0
+    assert lib.engram_wkv_gate_partials_workspace_size(T, K, hc, dim, 1) == lib.engram_wkv_workspace_size(T, K, 768, 1)
     H, Q, KW, V, PA = (i << 28 for i in range(14, 19))
 
     def g(value=V, partials=PA, ws=WK):
@@ -255,7 +263,7 @@ def test_products_refuse():
         with pytest.raises(ValueError):
             E.wkv(x, wt, sc)
     with pytest.raises(ValueError, match="workspace"):
-        E.wkv(dev(3, 64), w, s, kv=dev(3, 32), workspace=dev(4096, dtype=U8, cls=Elsewhere))
+        E.wkv(dev(9, 64), w, s, kv=dev(9, 32), workspace=dev(4096, dtype=U8, cls=Elsewhere))
 
 
 def test_quantizer_binding_refuses():
