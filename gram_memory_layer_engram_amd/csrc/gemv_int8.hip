@@ -413,11 +413,13 @@ hipError_t run_slices(const GemvI8Args& a, hipStream_t s) {
 
 // Few tokens: x in registers up to K 8192, from 9 tokens on (16 rows of x to
 // fetch for a wave) only where the workgroups are few: N 4096, K 2048, T 16: 3.2 us,
-// slices 3.6; N 20480 8.8, slices 8.0.
+// slices 3.6; N 20480 8.8, slices 8.0. (A grid holds fewer than 2^32 threads, and
+// these have up to 1024 for 16 rows: past N 2^24 the slices' 64 take over.)
 hipError_t launch_gemv_int8(const uint8_t* xq, const float* xs, int64_t T, int K, const uint8_t* w, const float* ws, int N,
                             void* kv, hipStream_t s) {
   const GemvI8Args a{xq, xs, w, ws, (uint16_t*)kv, (int)T, K, N};
-  if (T <= 8 ? K <= 8192 : T <= 16 && K <= 4096 && (N + 15) / 16 <= 2 * dev_info().num_cus) return run_reg(a, s);
+  if (T <= 8 ? K <= 8192 && N <= 1 << 24 : T <= 16 && K <= 4096 && (N + 15) / 16 <= 2 * dev_info().num_cus)
+    return run_reg(a, s);
   return T <= 16   ? run_slices<1>(a, s)
          : T <= 32 ? run_slices<2>(a, s)
          : T <= 48 ? run_slices<3>(a, s)

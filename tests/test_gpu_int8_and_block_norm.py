@@ -221,6 +221,18 @@ def test_int8_quantizer_rows_that_are_not_ordinary(K):
     assert np.isnan(ws[4:7]).all() and xq.cpu().numpy()[9, :4].tolist() == [0, 127, 0, 2]
 
 
+def test_int8_quantizer_offsets_past_32_bits():
+    E = _E()
+    T, K = 33001, 131056                       # 4.3e9 elements
+    g = torch.Generator(device=DEV).manual_seed(3)
+    part = torch.randn((67, K), generator=g, device=DEV).to(torch.bfloat16)
+    x = part.repeat((T + 66) // 67, 1)[:T]
+    xq, xs = E.int8_quantize(x)
+    q, s = E.int8_quantize(part)
+    for at in (0, 16385, 16386, 32771, 32772, T - 1):
+        assert torch.equal(xq[at], q[at % 67]) and float(xs[at]) == float(s[at % 67])
+
+
 # ------------------------------------------------------------------- norms --
 
 def _norm_case(rng, T, hc, dim, gate, bcast=False, pad=0):

@@ -115,3 +115,15 @@ def test_forward_routes(dispatch):
     assert route("forward 8192 4 4096 16 128 3 1") == ("gemm_int8_kernel<4,false>", False)
     for c, hd, tail in ((16, 64, "false"), (9, 112, "true")):      # the epilogue's own GPU test
         assert route(f"forward 1491 4 4096 {c} {hd} 3 0") == (f"gemm_int8_kernel<4,{tail}>", True)
+
+
+def test_grids_stay_below_what_a_dimension_holds(dispatch):
+    """Fewer than 2^32 threads a dimension, up to N 2^28 and 2^31 - 1 rows."""
+    lines = [f"i8 {T} {K} {N}" for T in (1, 8, 9, 16, 20, 40, 64, 90, 130) for K in (16, 1040, 2064, 8192, 131056)
+             for N in (1 << 24, (1 << 24) + 4, 1 << 27, 1 << 28)]
+    lines += [f"i8q {T} {K}" for T in (1 << 20, (1 << 31) - 1) for K in (16, 2048, 8192, 40000)]
+    lines += [f"ppn {T} 1 {d} 2" for T in ((1 << 22) + 1, (1 << 31) - 1) for d in (8, 1024, 16384)]
+    for line, (status, launches) in zip(lines, dispatch.calls(lines)):
+        assert status == 0 and launches, line
+        for la in launches:
+            assert la.grid[0] * la.block < 1 << 32 and la.grid[1] < 1 << 16, (line, la)
