@@ -604,11 +604,12 @@ static int run_forward(const engram_forward_args* a, int32_t K, int32_t N, uint8
                      : a->w_format == ENGRAM_W_MXFP8 ? !gemv_mxfp8_supported(a->T, K)
                      : a->w_format == ENGRAM_W_INT8  ? !gemv_int8_supported(a->T, N)
                                                      : !gemv_mxfp4_supported(a->T, K, false);
-  // MXFP4 weights: only where the plain store would take the epilogue's
+  // MXFP4 and INT8 weights: only where the plain store would take the epilogue's
   // 256x256 tile as well, or kv is too large to wait for the gate in the
   // Infinity Cache; elsewhere 128x128 tiles and a gate from kv beat it (hc 4,
-  // dim 4096, epilogue / kv stored: K 2048, T 300 59 / 43 us, T 1000 118 / 100, T
-  // 4096 340 / 358; K 256, T 1000 51 / 42, T 4096 139 / 155).
+  // dim 4096, epilogue / kv stored: MXFP4, K 2048, T 300 59 / 43 us, T 1000 118 /
+  // 100, T 4096 340 / 358; K 256, T 1000 51 / 42, T 4096 139 / 155; INT8, K 2048, T
+  // 8192 482 / 518).
   const bool epi = !(a->options & ENGRAM_FORWARD_STORE_KV) && tiled && a->dim % 256 == 0 &&
                    (!checks_small_tiles(a->w_format) || big_tiles(a->w_format, a->T, N, K) ||
                     a->T * (int64_t)N * 2 > (128 << 20));
