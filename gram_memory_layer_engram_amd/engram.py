@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -31,7 +32,7 @@ _sz = ctypes.c_size_t
 
 # names of the calls that count in single tokens, looked up once
 _BF16, _U8, _I8, _F32 = torch.bfloat16, torch.uint8, torch.int8, torch.float32
-_empty_strided = torch.empty_strided
+_empty_strided, _empty_like = torch.empty_strided, torch.empty_like
 _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -67,6 +68,10 @@ class PostPreNormArgs(ctypes.Structure):
     ]
 
 
+# The same bytes a microsecond sooner than the Structure (a decode call takes ten).
+_pack_post_pre_norm = struct.Struct("@PqqPqqPqqiiPPiiqiiiffffiPPPP").pack
+
+
 EXPORTS = {
     "engram_abi_version": (_i32, []),
     "engram_status_string": (ctypes.c_char_p, [_i32]),
@@ -84,7 +89,7 @@ EXPORTS = {
     "engram_wkv_mx": (_i32, [_vp, _vp, _i64, _i32, _vp, _vp, _i32, _i32, _vp, _vp]),
     "engram_int8_quantize": (_i32, [_vp, _i64, _i32, _vp, _vp, _vp]),
     "engram_wkv_int8": (_i32, [_vp, _vp, _i64, _i32, _vp, _vp, _i32, _vp, _vp]),
-    "engram_post_pre_norm": (_i32, [ctypes.POINTER(PostPreNormArgs), _vp]),
+    "engram_post_pre_norm": (_i32, [_vp, _vp]),   # the struct's address: post_pre_norm packs its bytes itself
     "engram_add_rms_norm": (_i32, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i32, _i64, _i32, _i32, _f32, _vp, _vp,
                                    _vp, _vp, _vp]),
     "engram_gate": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _f32, _f32, _vp, _vp, _vp]),
@@ -542,7 +547,7 @@ def add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None = None, weight: 
         if weight.get_device() != dev:
             _device_of(x, weight)
         wp = weight.data_ptr()
-    op = qp = sp = None
+    op = qp = sp = 0
     if out_format != "mxfp8":
         if out_format != "bf16" and out_format != "both":
             raise ValueError('out_format must be "bf16", "mxfp8" or "both"')
@@ -642,8 +647,8 @@ def post_pre_norm(x: torch.Tensor, residual: torch.Tensor | None = None, post_we
         raise ValueError("libengram takes device tensors only")
     device = x.device
     xp, xst, xsh = _rows(x, "x", shape, dev, T, hc, dim)
-    rp, rst, rsh = (None, 0, 0) if residual is None else _rows(residual, "residual", shape, dev, T, hc, dim)
-    gp, gst, gsh, gf = None, 0, 0, GATE_NONE
+    rp, rst, rsh = (0, 0, 0) if residual is None else _rows(residual, "residual", shape, dev, T, hc, dim)
+    gp, gst, gsh, gf = 0, 0, 0, GATE_NONE
     if gate is not None:
         if gate.dtype == _F32:
             if gate.shape != rows or gate.get_device() != dev:
@@ -655,8 +660,8 @@ def post_pre_norm(x: torch.Tensor, residual: torch.Tensor | None = None, post_we
             gf = GATE_CHANNEL
     if gate_act != "none" and gate_act != "sigmoid":
         raise ValueError('gate_act must be "none" or "sigmoid"')
-    w1, h1 = (None, 1) if post_weight is None else _norm_weight(post_weight, "post_weight", hc, dim, dev)
-    w2, h2 = (None, 1) if pre_weight is None else _norm_weight(pre_weight, "pre_weight", hc, dim, dev)
+    w1, h1 = (0, 1) if post_weight is None else _norm_weight(post_weight, "post_weight", hc, dim, dev)
+    w2, h2 = (0, 1) if pre_weight is None else _norm_weight(pre_weight, "pre_weight", hc, dim, dev)
 
     if out_format == "bf16" or out_format == "none":
         qf = Q_NONE
@@ -669,10 +674,10 @@ def post_pre_norm(x: torch.Tensor, residual: torch.Tensor | None = None, post_we
         residual_out = _empty_strided(shape, dense, dtype=_BF16, device=device)
     else:
         _check_output(residual_out, "residual_out", _BF16, shape, dev)
-    op = qp = sp = None
+    op = qp = sp = 0
     if out_format == "bf16" or out_format == "both":
         if out is None:
-            out = _empty_strided(shape, dense, dtype=_BF16, device=device)
+            out = _empty_like(residual_out)
         else:
             _check_output(out, "out", _BF16, shape, dev)
         op = out.data_ptr()
@@ -686,7 +691,7 @@ def post_pre_norm(x: torch.Tensor, residual: torch.Tensor | None = None, post_we
             qt, st, sshape = _U8, _U8, (*rows, nb)
             sdense = (hc * nb, nb, 1) if len(shape) == 3 else (nb, 1)
         if xq is None:
-            xq = _empty_strided(shape, dense, dtype=qt, device=device)
+            xq = _empty_like(residual_out, dtype=qt)
         else:
             _check_output(xq, "xq", qt, shape, dev)
         if xs is None:
@@ -696,9 +701,9 @@ def post_pre_norm(x: torch.Tensor, residual: torch.Tensor | None = None, post_we
         qp, sp = xq.data_ptr(), xs.data_ptr()
     elif xq is not None or xs is not None:
         raise ValueError(f'xq and xs are not written with out_format "{out_format}"')
-    args = PostPreNormArgs(xp, xst, xsh, rp, rst, rsh, gp, gst, gsh, gf, gate_act == "sigmoid", w1, w2, h1, h2, T, hc,
-                           dim, bool(post_norm), eps if post_eps is None else post_eps, eps, residual_scale,
-                           branch_scale, qf, residual_out.data_ptr(), op, qp, sp)
+    args = _pack_post_pre_norm(xp, xst, xsh, rp, rst, rsh, gp, gst, gsh, gf, gate_act == "sigmoid", w1, w2, h1, h2, T,
+                               hc, dim, bool(post_norm), eps if post_eps is None else post_eps, eps, residual_scale,
+                               branch_scale, qf, residual_out.data_ptr(), op, qp, sp)
     if dev != _current_device():
         _run_on(dev, L.engram_post_pre_norm, args)
     elif status := L.engram_post_pre_norm(args, _raw_stream(dev)):

@@ -91,6 +91,9 @@ def test_args_layout_matches_c(tmp_path):
     vals = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
     assert vals[0] == ctypes.sizeof(E.PostPreNormArgs)
     assert [getattr(E.PostPreNormArgs, f).offset for f in fields] == vals[1:]
+    # the binding packs the same bytes
+    v = [i + 1 if t not in (ctypes.c_float,) else 0.5 + i for i, (_, t) in enumerate(E.PostPreNormArgs._fields_)]
+    assert E._pack_post_pre_norm(*v) == bytes(E.PostPreNormArgs(*v))
 
 
 X, XS, W, WS, KV, R, G, P1, P2, RO, OUT, XQ = (i << 28 for i in range(1, 13))
