@@ -207,26 +207,29 @@ void gemm_int8_kernel(const uint8_t* __restrict__ xq, const float* __restrict__ 
   scale_and_store<NT>(acc, wsc, xsc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
 }
 
-// 128x128 tiles where there are fewer than compute units: nothing else covers a late
-// slice there, so all of LDS is one ring of five slices (A and B, 32 KiB), fetched
+// 128x128 tiles where there are at most as many as compute units: nothing else covers a
+// late slice there, so all of LDS is one ring of five slices (A and B, 32 KiB), fetched
 // four ahead, and the workgroups start at different slices (rows some KiB apart that
 // are all read at the same k fall on few memory channels; the order of k is free).
-// K 8192, N 8192, T 180 36.0 -> 26.0 us; K 4096, N 12288, T 180 21.1 -> 17.1; K 2048, N
-// 20480, T 128 12.9 -> 11.2. What is left is LDS: a wave's 64 x 64 reads 64 KiB a slice
-// and workgroup, its DMAs write 32, at 128 bytes a clock more than its 512 clocks of
-// matrix instructions.
+// K 8192, N 8192, T 180 36.0 -> 26.0 us; K 4096, N 12288, T 180 21.1 -> 17.1, N 16384, T
+// 256 27.7 -> 20.5; K 2048, N 20480, T 128 12.9 -> 11.2; behind a round of 256x256 tiles
+// (the 64 of 320 at N 20480, K 4096, T 1000) 80.9 -> 77.1 for both. What is left is LDS:
+// a wave's 64 x 64 reads 64 KiB a slice and workgroup, its DMAs write 32, at 128 bytes a
+// clock more than its 512 clocks of matrix instructions. (256 x 128 with two thirds of
+// that a product, three slices in the ring: as fast as two 128x128 workgroups on a
+// compute unit within 3%, 7% faster where they just fill a round; not taken.)
 constexpr int kDeep = 5;
 
 template <bool KTAIL>
 __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void gemm_int8_deep_kernel(const uint8_t* __restrict__ xq, const float* __restrict__ xs, int T, int K,
                            const uint8_t* __restrict__ w, const float* __restrict__ ws, int N,
-                           uint16_t* __restrict__ kv, int tiles_n, int tiles_t) {
+                           uint16_t* __restrict__ kv, int tn0, int tiles_n, int tiles_t) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   int tn, tt;
   tile_of(blockIdx.x, tiles_n, tiles_t, tn, tt);
   constexpr int NT = 2, TILE = 128, CH = Q_ROW * TILE, SLOT = 2 * CH, NDMA = 4;   // of an operand and wave
-  const int n0 = tn * TILE, t0 = tt * TILE;
+  const int n0 = (tn0 + tn) * TILE, t0 = tt * TILE;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = (wave >> 1) * 64, wt = (wave & 1) * 64;
@@ -338,24 +341,26 @@ hipError_t launch_tile(const uint8_t* xq, const float* xs, int T, int K, const u
 }
 
 hipError_t launch_deep(const uint8_t* xq, const float* xs, int T, int K, const uint8_t* w, const float* ws, int N,
-                       uint16_t* kv, hipStream_t s) {
-  const int tiles_n = (N + 127) / 128, tiles_t = (T + 127) / 128;
+                       uint16_t* kv, int tn0, int tiles_n, hipStream_t s) {
+  const int tiles_t = (T + 127) / 128;
   constexpr int lds = kDeep * 2 * 128 * Q_ROW;
   const auto fn = K % Q_ROW ? gemm_int8_deep_kernel<true> : gemm_int8_deep_kernel<false>;
   const hipError_t e = set_lds((const void*)fn, lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(fn, dim3(tiles_n * tiles_t), dim3(THREADS), lds, s, xq, xs, T, K, w, ws, N, kv, tiles_n, tiles_t);
+  hipLaunchKernelGGL(fn, dim3(tiles_n * tiles_t), dim3(THREADS), lds, s, xq, xs, T, K, w, ws, N, kv, tn0, tiles_n,
+                     tiles_t);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// Few tiles and enough slices that their latency counts (K 2048, N 4096: nothing
-// gained; from three quarters of the compute units on, T 128, N 28672, K 4096: 24.1 us,
-// deep 28.4).
-static bool int8_deep(int64_t T, int N, int K) {
-  const int64_t tiles = ((N + 127) / 128) * ((T + 127) / 128), cus = dev_info().num_cus;
-  return 4 * tiles <= 3 * cus && (K >= 4096 || (K >= 2048 && 2 * tiles > cus));
+// 128x128 tiles of `rows` W rows: at most one for a compute unit and enough slices
+// that their latency counts (K 2048, N 4096, T 180: nothing gained). Of one tile of
+// tokens, where the weight streams from HBM, three quarters as many (T 128, N 28672, K
+// 4096: 24.1 us, deep 28.4).
+static bool int8_deep(int64_t T, int64_t rows, int K) {
+  const int64_t tiles = ((rows + 127) / 128) * ((T + 127) / 128), cus = dev_info().num_cus;
+  return 4 * tiles <= (T <= 128 ? 3 : 4) * cus && (K >= 4096 || (K >= 2048 && 2 * tiles > cus));
 }
 
 static int int8_big_columns(int64_t T, int N, int K) {
@@ -368,13 +373,14 @@ bool gemm_int8_big_tiles(int64_t T, int N, int K) { return int8_big_columns(T, N
 hipError_t launch_gemm_int8(const uint8_t* xq, const float* xs, int64_t T, int K, const uint8_t* w, const float* ws,
                             int N, void* kv, hipStream_t s, const GateEpi& ep) {
   uint16_t* out = (uint16_t*)kv;
-  if (!ep.hidden && int8_deep(T, N, K)) return launch_deep(xq, xs, (int)T, K, w, ws, N, out, s);
-  const int big = ep.hidden ? (N + 255) / 256 : int8_big_columns(T, N, K);
+  const int big = ep.hidden ? (N + 255) / 256 : int8_deep(T, N, K) ? 0 : int8_big_columns(T, N, K);
   if (big) {
     const hipError_t e = launch_tile<4>(xq, xs, (int)T, K, w, ws, N, out, 0, big, s, ep);
     if (e != hipSuccess || 256 * (int64_t)big >= N) return e;
   }
-  return launch_tile<2>(xq, xs, (int)T, K, w, ws, N, out, 2 * big, (N + 127) / 128 - 2 * big, s, ep);
+  const int tn0 = 2 * big, tiles_n = (N + 127) / 128 - tn0;
+  if (int8_deep(T, N - 128 * (int64_t)tn0, K)) return launch_deep(xq, xs, (int)T, K, w, ws, N, out, tn0, tiles_n, s);
+  return launch_tile<2>(xq, xs, (int)T, K, w, ws, N, out, tn0, tiles_n, s, ep);
 }
 
 }  // namespace engram
