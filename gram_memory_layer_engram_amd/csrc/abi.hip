@@ -79,7 +79,7 @@ int check_wkv(const void* x, int64_t T, int32_t K, const void* w,
     if (K % 128 != 0 || N % 4 != 0 || N > (1 << 28)) return ENGRAM_EUNSUPPORTED;
   } else if (w_format == ENGRAM_W_INT8) {
     if (T > 0 && (!w_scales || !aligned16(w_scales))) return ENGRAM_EINVAL;
-    if (K % 16 != 0 || K > kInt8MaxK || N % 4 != 0 || N > (1 << 28)) return ENGRAM_EUNSUPPORTED;
+    if (K % 16 != 0 || K > kInt8MaxK || N % 4 != 0 || N > (1 << 28) || T > (1 << 30)) return ENGRAM_EUNSUPPORTED;
   } else {
     return ENGRAM_EINVAL;
   }

@@ -60,16 +60,28 @@ __device__ __forceinline__ void scale_and_store(const i32x16 (&acc)[NT][NT], con
   store_tile<NT>(out, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
 }
 
+struct GemmI8Args {
+  const uint8_t* xq;
+  const float* xs;
+  const uint8_t* w;
+  const float* ws;
+  uint16_t* kv;
+  int T, K, N;
+};
+
+// The 64 * NT square tile of workgroup bid.
 template <int NT, bool KTAIL>
-__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(NT == 4 ? 1 : 2, NT == 4 ? 1 : 2)))
-void gemm_int8_kernel(const uint8_t* __restrict__ xq, const float* __restrict__ xs, int T, int K,
-                      const uint8_t* __restrict__ w, const float* __restrict__ ws, int N, uint16_t* __restrict__ kv,
-                      int tn0, int tiles_n, int tiles_t, GateEpi ep) {
-  extern __shared__ __attribute__((aligned(1024))) char smem[];
+__device__ __forceinline__ void ring_tile(const GemmI8Args& p, char* smem, int bid, int tiles_n, int tiles_t,
+                                          const GateEpi& ep) {
+  const uint8_t* __restrict__ xq = p.xq;
+  const uint8_t* __restrict__ w = p.w;
+  const float* __restrict__ xs = p.xs;
+  const float* __restrict__ ws = p.ws;
+  const int T = p.T, K = p.K, N = p.N;
   int tn, tt;
-  tile_of(blockIdx.x, tiles_n, tiles_t, tn, tt);
+  tile_of(bid, tiles_n, tiles_t, tn, tt);
   constexpr int TILE = 64 * NT, CH = Q_ROW * TILE, NDMA = 2 * NT;   // a chunk in LDS, a wave's DMAs for it
-  const int n0 = (tn0 + tn) * TILE, t0 = tt * TILE;
+  const int n0 = tn * TILE, t0 = tt * TILE;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = (wave >> 1) * (32 * NT), wt = (wave & 1) * (32 * NT);
@@ -204,7 +216,7 @@ void gemm_int8_kernel(const uint8_t* __restrict__ xq, const float* __restrict__ 
   wait_lgkm0();
   bare_barrier();
 
-  scale_and_store<NT>(acc, wsc, xsc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, ep);
+  scale_and_store<NT>(acc, wsc, xsc, smem, p.kv, T, N, t0, n0, wn, wt, lane, wave, ep);
 }
 
 // 128x128 tiles where there are at most as many as compute units: nothing else covers a
@@ -212,22 +224,23 @@ void gemm_int8_kernel(const uint8_t* __restrict__ xq, const float* __restrict__ 
 // four ahead, and the workgroups start at different slices (rows some KiB apart that
 // are all read at the same k fall on few memory channels; the order of k is free).
 // K 8192, N 8192, T 180 36.0 -> 26.0 us; K 4096, N 12288, T 180 21.1 -> 17.1, N 16384, T
-// 256 27.7 -> 20.5; K 2048, N 20480, T 128 12.9 -> 11.2; behind a round of 256x256 tiles
-// (the 64 of 320 at N 20480, K 4096, T 1000) 80.9 -> 77.1 for both. What is left is LDS:
-// a wave's 64 x 64 reads 64 KiB a slice and workgroup, its DMAs write 32, at 128 bytes a
-// clock more than its 512 clocks of matrix instructions. (256 x 128 with two thirds of
-// that a product, three slices in the ring: as fast as two 128x128 workgroups on a
-// compute unit within 3%, 7% faster where they just fill a round; not taken.)
+// 256 27.7 -> 20.5; K 2048, N 20480, T 128 12.9 -> 11.2. What is left is LDS: a wave's 64
+// x 64 reads 64 KiB a slice and workgroup, its DMAs write 32, at 128 bytes a clock more
+// than its 512 clocks of matrix instructions. (256 x 128 with three quarters of that a
+// product, three slices in the ring: as fast as two 128x128 workgroups on a compute unit
+// within 3%, 7% faster where it just fills a round; not taken.)
 constexpr int kDeep = 5;
 
+// The 128x128 tile of workgroup bid, tile columns from tn0 on.
 template <bool KTAIL>
-__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(1, 1)))
-void gemm_int8_deep_kernel(const uint8_t* __restrict__ xq, const float* __restrict__ xs, int T, int K,
-                           const uint8_t* __restrict__ w, const float* __restrict__ ws, int N,
-                           uint16_t* __restrict__ kv, int tn0, int tiles_n, int tiles_t) {
-  extern __shared__ __attribute__((aligned(1024))) char smem[];
+__device__ __forceinline__ void deep_tile(const GemmI8Args& p, char* smem, int bid, int tn0, int tiles_n, int tiles_t) {
+  const uint8_t* __restrict__ xq = p.xq;
+  const uint8_t* __restrict__ w = p.w;
+  const float* __restrict__ xs = p.xs;
+  const float* __restrict__ ws = p.ws;
+  const int T = p.T, K = p.K, N = p.N;
   int tn, tt;
-  tile_of(blockIdx.x, tiles_n, tiles_t, tn, tt);
+  tile_of(bid, tiles_n, tiles_t, tn, tt);
   constexpr int NT = 2, TILE = 128, CH = Q_ROW * TILE, SLOT = 2 * CH, NDMA = 4;   // of an operand and wave
   const int n0 = (tn0 + tn) * TILE, t0 = tt * TILE;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -324,42 +337,76 @@ void gemm_int8_deep_kernel(const uint8_t* __restrict__ xq, const float* __restri
   wait_vm<0>();   // the zero-fill DMAs of the last slices land before LDS is reused
   wait_lgkm0();
   bare_barrier();
-  scale_and_store<NT>(acc, wsc, xsc, smem, kv, T, N, t0, n0, wn, wt, lane, wave, GateEpi{});
+  scale_and_store<NT>(acc, wsc, xsc, smem, p.kv, T, N, t0, n0, wn, wt, lane, wave, GateEpi{});
 }
+
+template <int NT, bool KTAIL>
+__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(NT == 4 ? 1 : 2, NT == 4 ? 1 : 2)))
+void gemm_int8_kernel(const GemmI8Args p, int tiles_n, int tiles_t, GateEpi ep) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  ring_tile<NT, KTAIL>(p, smem, blockIdx.x, tiles_n, tiles_t, ep);
+}
+
+template <bool KTAIL>
+__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void gemm_int8_deep_kernel(const GemmI8Args p, int tiles_n, int tiles_t) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  deep_tile<KTAIL>(p, smem, blockIdx.x, 0, tiles_n, tiles_t);
+}
+
+// Whole rounds of 256x256 tiles (`big` columns of them), then 128x128 ones on the
+// compute units as they come free. One launch: N 20480, K 4096, T 1000 (256 + 256 tiles)
+// 76 us, two launches 79 - 81; N 12288, K 4096, T 2048 91 against 92. The small tiles
+// have all of LDS here and so take the deep ring; two in half of it each, in a launch of
+// their own, are 1.5% faster at best (N 28672, K 2048, T 700 46.6 against 47.3).
+template <bool KTAIL>
+__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void gemm_int8_mixed_kernel(const GemmI8Args p, int big) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  const int tiles_t = (p.T + 255) / 256, first = big * tiles_t, bid = blockIdx.x;
+  if (bid < first)
+    ring_tile<4, KTAIL>(p, smem, bid, big, tiles_t, GateEpi{});
+  else
+    deep_tile<KTAIL>(p, smem, bid - first, 2 * big, (p.N + 127) / 128 - 2 * big, (p.T + 127) / 128);
+}
+
+template <typename F, typename... A>
+hipError_t launch_gemm(F fn, int64_t grid, int lds, hipStream_t s, const A&... args) {
+  const hipError_t e = set_lds((const void*)fn, lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(fn, dim3((uint32_t)grid), dim3(THREADS), lds, s, args...);
+  return hipGetLastError();
+}
+
+constexpr int kDeepLds = kDeep * 2 * 128 * Q_ROW;
+static_assert(kDeepLds <= Q_LDS, "one workgroup's LDS");
 
 template <int NT>
-hipError_t launch_tile(const uint8_t* xq, const float* xs, int T, int K, const uint8_t* w, const float* ws, int N,
-                       uint16_t* kv, int tn0, int tiles_n, hipStream_t s, const GateEpi& ep) {
-  const int tiles_t = (T + 64 * NT - 1) / (64 * NT);
-  constexpr int lds = Q_LDS * NT / 4;
-  const auto fn = K % Q_ROW ? gemm_int8_kernel<NT, true> : gemm_int8_kernel<NT, false>;
-  const hipError_t e = set_lds((const void*)fn, lds);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(fn, dim3(tiles_n * tiles_t), dim3(THREADS), lds, s, xq, xs, T, K, w, ws, N, kv, tn0, tiles_n,
-                     tiles_t, ep);
-  return hipGetLastError();
+hipError_t launch_ring(const GemmI8Args& p, hipStream_t s, const GateEpi& ep) {
+  const int tiles_n = (p.N + 64 * NT - 1) / (64 * NT), tiles_t = (p.T + 64 * NT - 1) / (64 * NT);
+  return launch_gemm(p.K % Q_ROW ? gemm_int8_kernel<NT, true> : gemm_int8_kernel<NT, false>, (int64_t)tiles_n * tiles_t,
+                     Q_LDS * NT / 4, s, p, tiles_n, tiles_t, ep);
 }
 
-hipError_t launch_deep(const uint8_t* xq, const float* xs, int T, int K, const uint8_t* w, const float* ws, int N,
-                       uint16_t* kv, int tn0, int tiles_n, hipStream_t s) {
-  const int tiles_t = (T + 127) / 128;
-  constexpr int lds = kDeep * 2 * 128 * Q_ROW;
-  const auto fn = K % Q_ROW ? gemm_int8_deep_kernel<true> : gemm_int8_deep_kernel<false>;
-  const hipError_t e = set_lds((const void*)fn, lds);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(fn, dim3(tiles_n * tiles_t), dim3(THREADS), lds, s, xq, xs, T, K, w, ws, N, kv, tn0, tiles_n,
-                     tiles_t);
-  return hipGetLastError();
+hipError_t launch_deep(const GemmI8Args& p, hipStream_t s) {
+  const int tiles_n = (p.N + 127) / 128, tiles_t = (p.T + 127) / 128;
+  return launch_gemm(p.K % Q_ROW ? gemm_int8_deep_kernel<true> : gemm_int8_deep_kernel<false>, (int64_t)tiles_n * tiles_t,
+                     kDeepLds, s, p, tiles_n, tiles_t);
+}
+
+hipError_t launch_mixed(const GemmI8Args& p, int big, hipStream_t s) {
+  const int64_t grid = (int64_t)big * ((p.T + 255) / 256) + (int64_t)((p.N + 127) / 128 - 2 * big) * ((p.T + 127) / 128);
+  return launch_gemm(p.K % Q_ROW ? gemm_int8_mixed_kernel<true> : gemm_int8_mixed_kernel<false>, grid, Q_LDS, s, p, big);
 }
 
 }  // namespace
 
-// 128x128 tiles of `rows` W rows: at most one for a compute unit and enough slices
-// that their latency counts (K 2048, N 4096, T 180: nothing gained). Of one tile of
+// At most one 128x128 tile for a compute unit and enough slices that their latency
+// counts (K 2048, N 4096, T 180: nothing gained). Of one tile of
 // tokens, where the weight streams from HBM, three quarters as many (T 128, N 28672, K
 // 4096: 24.1 us, deep 28.4).
-static bool int8_deep(int64_t T, int64_t rows, int K) {
-  const int64_t tiles = ((rows + 127) / 128) * ((T + 127) / 128), cus = dev_info().num_cus;
+static bool int8_deep(int64_t T, int64_t N, int K) {
+  const int64_t tiles = ((N + 127) / 128) * ((T + 127) / 128), cus = dev_info().num_cus;
   return 4 * tiles <= (T <= 128 ? 3 : 4) * cus && (K >= 4096 || (K >= 2048 && 2 * tiles > cus));
 }
 
@@ -372,15 +419,10 @@ bool gemm_int8_big_tiles(int64_t T, int N, int K) { return int8_big_columns(T, N
 // The gate's epilogue has the 256x256 tile only.
 hipError_t launch_gemm_int8(const uint8_t* xq, const float* xs, int64_t T, int K, const uint8_t* w, const float* ws,
                             int N, void* kv, hipStream_t s, const GateEpi& ep) {
-  uint16_t* out = (uint16_t*)kv;
-  const int big = ep.hidden ? (N + 255) / 256 : int8_deep(T, N, K) ? 0 : int8_big_columns(T, N, K);
-  if (big) {
-    const hipError_t e = launch_tile<4>(xq, xs, (int)T, K, w, ws, N, out, 0, big, s, ep);
-    if (e != hipSuccess || 256 * (int64_t)big >= N) return e;
-  }
-  const int tn0 = 2 * big, tiles_n = (N + 127) / 128 - tn0;
-  if (int8_deep(T, N - 128 * (int64_t)tn0, K)) return launch_deep(xq, xs, (int)T, K, w, ws, N, out, tn0, tiles_n, s);
-  return launch_tile<2>(xq, xs, (int)T, K, w, ws, N, out, tn0, tiles_n, s, ep);
+  const GemmI8Args p{xq, xs, w, ws, (uint16_t*)kv, (int)T, K, N};
+  if (!ep.hidden && int8_deep(T, N, K)) return launch_deep(p, s);
+  const int tn = (N + 255) / 256, big = ep.hidden ? tn : int8_big_columns(T, N, K);   // of 256x256 tiles
+  return big == tn ? launch_ring<4>(p, s, ep) : big ? launch_mixed(p, big, s) : launch_ring<2>(p, s, ep);
 }
 
 }  // namespace engram

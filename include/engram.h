@@ -216,7 +216,7 @@ int engram_int8_quantize(const void* x, int64_t T, int32_t K, int8_t* xq, float*
  *   quantized by engram_int8_quantize's rule; the sums are engram_wkv_int8's.
  *   Shapes: bf16 needs K % 8 == 0 and N % 4 == 0; MXFP8 needs K % 128 == 0
  *   and N % 32 == 0; MXFP4 needs K % 128 == 0, N % 4 == 0 and N <= 2^28; INT8
- *   needs K % 16 == 0, K <= 131056, N % 4 == 0 and N <= 2^28; all
+ *   needs K % 16 == 0, K <= 131056, N % 4 == 0, N <= 2^28 and T <= 2^30; all
  *   need K <= 2^20 (32-bit buffer offsets). Other shapes return
  *   ENGRAM_EUNSUPPORTED.
  *   Kernels: a tiled GEMM; for T <= 64 a weight-streaming GEMV instead
@@ -267,7 +267,7 @@ int engram_wkv_mx(const uint8_t* xq, const uint8_t* xs, int64_t T, int32_t K, co
  *   xq        int8 [T, K], 16-byte aligned;  xs  fp32 [T], 4-byte aligned.
  *   w         int8 [N, K], w_scales fp32 [N], both 16-byte aligned.
  *   kv        bf16 [T, N]; on an operand: ENGRAM_EINVAL.
- *   Shapes: K % 16 == 0, K <= 131056, N % 4 == 0, N <= 2^28, T < 2^31; else
+ *   Shapes: K % 16 == 0, K <= 131056, N % 4 == 0, N <= 2^28, T <= 2^30; else
  *   ENGRAM_EUNSUPPORTED.
  */
 int engram_wkv_int8(const int8_t* xq, const float* xs, int64_t T, int32_t K, const int8_t* w, const float* w_scales,

@@ -116,7 +116,7 @@ def test_product_refusals(lib):
 
     assert f(None, None, 0, 64, None, None, 32, None) == OK
     assert f(T=-1) == INV and f(K=0) == INV and f(N=0) == INV
-    for kw in (dict(K=8), dict(K=100), dict(K=1 << 17), dict(N=30), dict(N=(1 << 28) + 4), dict(T=1 << 31)):
+    for kw in (dict(K=8), dict(K=100), dict(K=1 << 17), dict(N=30), dict(N=(1 << 28) + 4), dict(T=1 << 31), dict(T=(1 << 30) + 1)):
         assert f(**kw) == UNS, kw
     for name in ("xq", "xs", "w", "ws", "kv"):
         assert f(**{name: None}) == INV

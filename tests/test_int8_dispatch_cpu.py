@@ -82,6 +82,11 @@ def test_grids_cover_and_lds_fits(dispatch):
                         assert T <= 16 and la.block == 64 * int(args[1])
                         assert 128 * int(args[1]) * int(args[3]) >= K, (line, la)   # waves x steps
                     cols = N
+                elif "mixed" in la.kernel:
+                    tt, t1, tn1 = -(-T // 256), -(-T // 128), -(-N // 128)
+                    big, rest = divmod(tn1 * t1 - la.grid[0], 2 * t1 - tt)   # columns of 256x256 tiles
+                    assert rest == 0 and 1 <= big < -(-N // 256) and -(big * tt) % cus < tt, (line, la)
+                    cols = 128 * tn1
                 elif la.kernel.startswith("gemm_int8"):
                     t = 128 if "deep" in la.kernel else 64 * int(args[0])
                     assert la.grid[0] % -(-T // t) == 0
@@ -118,9 +123,10 @@ def test_forward_routes(dispatch):
 
 
 def test_grids_stay_below_what_a_dimension_holds(dispatch):
-    """Fewer than 2^32 threads a dimension, up to N 2^28 and 2^31 - 1 rows."""
+    """Fewer than 2^32 threads a dimension, up to N 2^28, T 2^30 and 2^31 - 1 rows."""
     lines = [f"i8 {T} {K} {N}" for T in (1, 8, 9, 16, 20, 40, 64, 90, 130) for K in (16, 1040, 2064, 8192, 131056)
              for N in (1 << 24, (1 << 24) + 4, 1 << 27, 1 << 28)]
+    lines += [f"i8 {1 << 30} {K} {N}" for K in (16, 2048) for N in (4, 128)]
     lines += [f"i8q {T} {K}" for T in (1 << 20, (1 << 31) - 1) for K in (16, 2048, 8192, 40000)]
     lines += [f"ppn {T} 1 {d} 2" for T in ((1 << 22) + 1, (1 << 31) - 1) for d in (8, 1024, 16384)]
     for line, (status, launches) in zip(lines, dispatch.calls(lines)):
