@@ -68,8 +68,9 @@ __device__ __forceinline__ uint32_t quad_xor2(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xf, 0xf, true);
 }
 
-// exp as a power of two on the hardware's v_exp_f32, reciprocal on v_rcp_f32 (1
-// ulp each): within 2^-20 of the sigmoid for |z| < 80, far under a bf16 step.
+// exp as a power of two on the hardware's v_exp_f32, reciprocal on v_rcp_f32 (1 ulp
+// each); z * log2(e) is rounded in units of its own size, so the sigmoid is within
+// 2^-20 of its value for |z| < 16 and 2^-17 to 80: far under a bf16 step.
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
 
 __device__ __forceinline__ float wave_sum(float v) {

@@ -665,3 +665,62 @@ def test_empty_batch():
     assert E.wkv(torch.empty((0, 128), dtype=torch.bfloat16, device=DEV), wd, sd).shape == (0, 64)
     q, s = E.int8_quantize(torch.empty((0, 128), dtype=torch.bfloat16, device=DEV))
     assert E.wkv_int8(q, s, wd, sd).shape == (0, 64)
+
+
+@pytest.mark.parametrize("T", [2, 40, 600])
+def test_forward_int8_host_table_and_strided_ids(T):
+    """Rows over the host link, and ids laid out column by column: the same output."""
+    E = _E()
+    rng = np.random.default_rng(T)
+    dim, hc, C, hd = 256, 2, 8, 128
+    wq, ws, ids, hidden, q, k, mask, table, _, _ = _forward_case(rng, T, dim, hc, C, hd, 301, False)
+    wd, sd, idd = _dev(wq), _dev(ws), _dev(ids)
+    want = E.forward(table, idd, wd, sd, hidden, q, k, mask)
+    assert torch.equal(E.forward(table, idd.t().contiguous().t(), wd, sd, hidden, q, k, mask), want)
+    _say(f"int8 host table T={T}")
+    ht = E.HostTable(301, hd).copy_from(table)
+    try:
+        got = E.forward(ht, idd, wd, sd, hidden, q, k, mask)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    finally:
+        ht.close()
+
+
+def test_two_threads_at_once():
+    """Calls of two host threads, each on its own stream, of different sizes: every
+    result is the serial one."""
+    import threading
+
+    E = _E()
+    rng = np.random.default_rng(5)
+    hc, start, failed, jobs = 2, threading.Barrier(2), [], []
+    for T, dim, N in ((3, 1024, 4096), (150, 2064, 1280)):
+        x, r, w1, w2, g = (t.contiguous().to(DEV) for t in _norm_case(rng, T, hc, dim, "row"))
+        wq, ws = (_dev(a) for a in _int8(rng, N, dim))
+
+        def calls(x=x, r=r, w1=w1, w2=w2, g=g, wq=wq, ws=ws, n=T * hc, dim=dim):
+            res, out, xq, xs = E.post_pre_norm(x, r, w1, w2, g, out_format="both", q_format="int8")
+            return res, out, xq, xs, E.wkv_int8(xq.view(n, dim), xs.view(n), wq, ws), E.wkv(out.view(n, dim), wq, ws)
+
+        jobs.append((calls, calls(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def work(calls, want, stream):
+        try:
+            with torch.cuda.stream(stream):
+                start.wait(30)
+                got = [calls() for _ in range(60)]
+                stream.synchronize()
+                for i in got:
+                    for a, b in zip(i, want):
+                        assert torch.equal(a, b)
+        except BaseException as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not failed, failed
