@@ -1,11 +1,11 @@
-// Projection in 8-bit integers for small batches (T <= 128): kv[T, N] =
+// Projection in 8-bit integers for small batches, or few rows: kv[T, N] =
 // bf16(float(x . W^T) * xs[t] * ws[n]), x int8 with one fp32 scale a token, or (up
 // to 8 tokens) bf16, quantized by the rule of int8_rule.h on the way.
 //
 // With few tokens the product is a stream of the weight, a byte a weight
 // ("vllm.models.deepseek_v41.amd.mono.attention.gemv": weight loads in flight
 // before the activations, split over k). A workgroup owns RT tiles of 16 rows and
-// all T tokens. The sums are whole numbers, exact in any order: k may be split and
+// all T tokens (past 64 a group of 64 or 128 of them). The sums are whole numbers, exact in any order: k may be split and
 // started anywhere, and kv is that of the tiled GEMM bit for bit.
 //
 // W goes through LDS (gemv_int8_dma.h): a fragment read straight from memory
@@ -20,7 +20,7 @@
 // bf16 x T 1 / 4 / 8 7.8 / 7.9 / 8.1. Up to 32 tokens that stream bounds it. Beyond,
 // x is read by every workgroup from L2 as well, 125 KB each at T 61. Past 64 tokens
 // it still beats the GEMM's few tiles: N 12288, K 4096, T 96 / 128 12.0 / 14.1 against
-// 20 us, N 4096, K 2048 6.0 / 6.6 against 9.2 - 9.7.
+// 20 us, N 4096, K 2048 5.8 / 6.3 against 9.2 - 9.7.
 #include <algorithm>
 
 #include "common.h"
@@ -204,7 +204,7 @@ constexpr int reg_lds(bool xbf, int T) {
 
 // ---- more tokens, or a longer K: a shared ring of slices ----
 //
-// A workgroup's waves share slices of 128 k of its 16*RT rows and of all tokens,
+// A workgroup's waves share slices of 128 k of its 16*RT rows and 16*NT tokens,
 // fetched D - 1 slices ahead into a ring of D. Wave (ks, j) multiplies token tile j
 // with every row tile, both 64-k halves of a slice (KS 1) or one (KS 2), so that
 // little is left to add at the end: with the waves splitting k alone each held every
@@ -234,17 +234,18 @@ __global__ __launch_bounds__(NT * KS * 64) void gemv_int8_slice_kernel(const Gem
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ks = wave / NT, j = wave % NT;
   const int n0 = blockIdx.x * 16 * RT, rows = min(16 * RT, a.N - n0);
+  const int t0 = blockIdx.y * 16 * NT, T = min(16 * NT, a.T - t0);
   const int g = lane >> 4, r = lane & 15;
   const uint32_t K = (uint32_t)a.K;
   const rsrc_t rw = make_rsrc(a.w + (int64_t)n0 * a.K, (uint32_t)rows * K);
-  const rsrc_t rx = make_rsrc(a.x, (uint32_t)a.T * K);
+  const rsrc_t rx = make_rsrc((const uint8_t*)a.x + (int64_t)t0 * a.K, (uint32_t)T * K);
   const int nk = (a.K + i8::kStep - 1) / i8::kStep;
 
   // what this thread adds up and stores: row tiles ks, ks + KS, .. of token tile j
   constexpr int MINE = (RT + KS - 1) / KS;
   const int t = j * 16 + r;
   f32x4 wsc[MINE];
-  const float xsc = t < a.T ? a.xs[t] : 0.f;
+  const float xsc = t < T ? a.xs[t0 + t] : 0.f;
 #pragma unroll
   for (int m = 0; m < MINE; ++m) {
     const int n = n0 + (ks + KS * m) * 16 + 4 * g;
@@ -332,7 +333,7 @@ __global__ __launch_bounds__(NT * KS * 64) void gemv_int8_slice_kernel(const Gem
 #pragma unroll
   for (int m = 0; m < MINE; ++m) {
     const int rt = ks + KS * m, n = n0 + rt * 16 + 4 * g;
-    if (rt < RT && t < a.T && n < a.N) store4(a.kv + (int64_t)t * a.N + n, acc[m], xsc, wsc[m]);   // N % 4 == 0
+    if (rt < RT && t < T && n < a.N) store4(a.kv + (int64_t)(t0 + t) * a.N + n, acc[m], xsc, wsc[m]);   // N % 4 == 0
   }
 }
 
@@ -356,7 +357,8 @@ hipError_t slices(const GemvI8Args& a, hipStream_t s) {
     const hipError_t e = hipFuncSetAttribute((const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(fn, dim3((a.N + 16 * RT - 1) / (16 * RT)), dim3(NT * KS * 64), lds, s, a);
+  hipLaunchKernelGGL(fn, dim3((a.N + 16 * RT - 1) / (16 * RT), (a.T + 16 * NT - 1) / (16 * NT)), dim3(NT * KS * 64), lds, s,
+                     a);
   return hipGetLastError();
 }
 
@@ -385,8 +387,8 @@ hipError_t run_reg_bf16(const GemvI8Args& a, hipStream_t s) {
 // and the slice's halves on two waves. Beyond: smaller rings, more workgroups on a
 // compute unit; from 33 tokens on seven row tiles where the compute units then have
 // fewer rows in their fullest round (N 28672, T 61: 23.9 us, three 31.6; N 20480
-// 10.4, three 9.8). Past 64 tokens six or eight waves, a token tile each, are enough
-// without halves.
+// 10.4, three 9.8). Past 64 tokens six waves, a token tile each, are enough without
+// halves.
 template <int NT>
 hipError_t run_slices(const GemvI8Args& a, hipStream_t s) {
   const int tiles = (a.N + 15) / 16, cus = dev_info().num_cus;
@@ -400,13 +402,16 @@ hipError_t run_slices(const GemvI8Args& a, hipStream_t s) {
            : tiles <= 4 * cus  ? slices<3, NT, 2, 4>(a, s)
            : rows(7) < rows(3) ? slices<7, NT, 2, 3>(a, s)
                                : slices<3, NT, 2, 3>(a, s);
-  } else if constexpr (NT == 6) {
+  } else {
     return tiles <= cus                               ? slices<1, NT, 1, 3>(a, s)
            : tiles > 4 * cus && rows(7) < rows(3) ? slices<7, NT, 1, 3>(a, s)
                                                       : slices<3, NT, 1, 3>(a, s);
-  } else {
-    return tiles <= cus ? slices<1, NT, 1, 3>(a, s) : slices<3, NT, 1, 3>(a, s);
   }
+}
+
+// Workgroups of rt row tiles and nt token tiles.
+int64_t groups(int64_t T, int N, int rt, int nt) {
+  return ((N + 16LL * rt - 1) / (16 * rt)) * ((T + 16LL * nt - 1) / (16 * nt));
 }
 
 }  // namespace
@@ -420,18 +425,26 @@ hipError_t launch_gemv_int8(const uint8_t* xq, const float* xs, int64_t T, int K
   const GemvI8Args a{xq, xs, w, ws, (uint16_t*)kv, (int)T, K, N};
   if (T <= 8 ? K <= 8192 && N <= 1 << 24 : T <= 16 && K <= 4096 && (N + 15) / 16 <= 2 * dev_info().num_cus)
     return run_reg(a, s);
-  return T <= 16   ? run_slices<1>(a, s)
-         : T <= 32 ? run_slices<2>(a, s)
-         : T <= 48 ? run_slices<3>(a, s)
-         : T <= 64 ? run_slices<4>(a, s)
-         : T <= 96 ? run_slices<6>(a, s)
-                   : run_slices<8>(a, s);
+  if (T <= 16) return run_slices<1>(a, s);
+  if (T <= 32) return run_slices<2>(a, s);
+  if (T <= 48) return run_slices<3>(a, s);
+  if (T <= 64) return run_slices<4>(a, s);
+  const int cus = dev_info().num_cus;
+  if (groups(T, N, 1, 4) <= cus) return slices<1, 4, 1, 4>(a, s);
+  if (T <= 96) return run_slices<6>(a, s);
+  return groups(T, N, 4, 4) <= cus ? slices<4, 4, 2, 3>(a, s) : slices<3, 8, 1, 3>(a, s);
 }
 
-// Up to 96 tokens, and up to 128 while the row tiles are few: with many the GEMM's
-// tiles fill the compute units (T 128, N 20480, K 2048: 11.2 us, here 13.3).
+// Past 64 tokens the smallest tiles that a compute unit each is enough for: 16 rows x 64
+// tokens, 64 x 64, 48 x 128. The GEMM's 128 x 128 would leave compute units idle (N 1024,
+// K 2048, T 200 4.9 us, 128x128 tiles 9.3; N 4096, T 256 6.5 against 9.5; N 6000, T 200 8.4
+// against 10.0; T 128 N 1024 4.8, one group of 128 tokens 5.9). From one token tile of
+// its own the GEMM has enough of them only where W is long: up to 96 tokens never, up to
+// 128 past four row tiles a compute unit (T 128, N 20480, K 2048: 11.2 us, here 13.3).
 bool gemv_int8_supported(int64_t T, int N) {
-  return T >= 1 && (T <= 96 || (T <= 128 && (N + 15) / 16 <= 4 * dev_info().num_cus));
+  const int cus = dev_info().num_cus;
+  return T >= 1 && (T <= 96 || (T <= 128 && (N + 15) / 16 <= 4 * cus) || groups(T, N, 4, 4) <= cus ||
+                    groups(T, N, 3, 8) <= cus);
 }
 
 // Quantizing on the way pays while the launch it saves (2.0 to 2.4 us) is more than

@@ -77,7 +77,8 @@ def test_grids_cover_and_lds_fits(dispatch):
                 if la.kernel.startswith("gemv_int8"):
                     assert la.grid[0] == -(-N // (16 * int(args[0]))), (line, la)
                     if "slice" in la.kernel:
-                        assert 16 * int(args[1]) >= T and la.block == 64 * int(args[1]) * int(args[2])
+                        assert 16 * int(args[1]) * la.grid[1] >= T and la.block == 64 * int(args[1]) * int(args[2])
+                        assert 16 * int(args[1]) * (la.grid[1] - 1) < T
                     else:
                         assert T <= 16 and la.block == 64 * int(args[1])
                         assert 128 * int(args[1]) * int(args[3]) >= K, (line, la)   # waves x steps
