@@ -340,10 +340,19 @@ __device__ __forceinline__ void deep_tile(const GemmI8Args& p, char* smem, int b
   scale_and_store<NT>(acc, wsc, xsc, smem, p.kv, T, N, t0, n0, wn, wt, lane, wave, GateEpi{});
 }
 
+// Two 128x128 workgroups on a compute unit that run in step load at the same time,
+// multiply at the same time and store at the same time; over several rounds they may
+// stay so. The second one of the first round therefore starts `pause` * 256 clocks late:
+// 16, about half a small tile, is the best or within 3% of 8 to 32 (N 5784, K 912, T 4643
+// 47.4 -> 45.4 us; N 4264, K 448, T 5058 24.8 -> 21.3; N 9096, K 304, T 3108 29.1 ->
+// 25.9), and without it the same launch now and then takes half as long again (N 10240,
+// K 512, T 3000 27 to 49 us, with it 27 to 30). A launch of one round gains nothing.
 template <int NT, bool KTAIL>
 __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(NT == 4 ? 1 : 2, NT == 4 ? 1 : 2)))
-void gemm_int8_kernel(const GemmI8Args p, int tiles_n, int tiles_t, GateEpi ep) {
+void gemm_int8_kernel(const GemmI8Args p, int tiles_n, int tiles_t, uint32_t cus, int pause, GateEpi ep) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
+  if (NT == 2 && blockIdx.x - cus < cus)
+    for (int i = 0; i < pause; ++i) __builtin_amdgcn_s_sleep(4);
   ring_tile<NT, KTAIL>(p, smem, blockIdx.x, tiles_n, tiles_t, ep);
 }
 
@@ -384,8 +393,9 @@ static_assert(kDeepLds <= Q_LDS, "one workgroup's LDS");
 template <int NT>
 hipError_t launch_ring(const GemmI8Args& p, hipStream_t s, const GateEpi& ep) {
   const int tiles_n = (p.N + 64 * NT - 1) / (64 * NT), tiles_t = (p.T + 64 * NT - 1) / (64 * NT);
-  return launch_gemm(p.K % Q_ROW ? gemm_int8_kernel<NT, true> : gemm_int8_kernel<NT, false>, (int64_t)tiles_n * tiles_t,
-                     Q_LDS * NT / 4, s, p, tiles_n, tiles_t, ep);
+  const int64_t tiles = (int64_t)tiles_n * tiles_t, cus = dev_info().num_cus;
+  return launch_gemm(p.K % Q_ROW ? gemm_int8_kernel<NT, true> : gemm_int8_kernel<NT, false>, tiles, Q_LDS * NT / 4, s, p,
+                     tiles_n, tiles_t, (uint32_t)cus, tiles > 2 * cus ? 16 : 0, ep);
 }
 
 hipError_t launch_deep(const GemmI8Args& p, hipStream_t s) {
@@ -411,7 +421,7 @@ static bool int8_deep(int64_t T, int64_t N, int K) {
 }
 
 static int int8_big_columns(int64_t T, int N, int K) {
-  return big_columns(T, N, K, {8000, 1400, 3200, 950, 3200, 660});
+  return big_columns(T, N, (K + 127) / 128 * 128, {9000, 1430, 3300, 870, 3200, 660});
 }
 
 bool gemm_int8_big_tiles(int64_t T, int N, int K) { return int8_big_columns(T, N, K) == (N + 255) / 256; }
