@@ -1,6 +1,6 @@
 // Projection in 8-bit integers for small batches, or few rows: kv[T, N] =
 // bf16(float(x . W^T) * xs[t] * ws[n]), x int8 with one fp32 scale a token, or (up
-// to 8 tokens) bf16, quantized by the rule of int8_rule.h on the way.
+// to 16 tokens) bf16, quantized by the rule of int8_rule.h on the way.
 //
 // With few tokens the product is a stream of the weight, a byte a weight
 // ("vllm.models.deepseek_v41.amd.mono.attention.gemv": weight loads in flight
@@ -379,7 +379,7 @@ hipError_t run_reg_bf16(const GemvI8Args& a, hipStream_t s) {
   if (a.K <= 512) return reg<1, 4, 1, 1, true>(a, s);
   if (a.K <= 1024) return many ? reg<3, 8, 1, 1, true>(a, s) : reg<1, 8, 1, 1, true>(a, s);
   if (a.K <= 2048) return many ? reg<3, 8, 1, 2, true>(a, s) : reg<1, 8, 2, 2, true>(a, s);
-  return many ? reg<3, 16, 1, 2, true>(a, s) : reg<1, 16, 2, 2, true>(a, s);
+  return many && a.T <= 8 ? reg<3, 16, 1, 2, true>(a, s) : reg<1, 16, 2, 2, true>(a, s);   // LDS holds the codes of T rows
 }
 
 // Slices. Up to one row tile for a compute unit: one a workgroup. Up to four: few
@@ -447,11 +447,13 @@ bool gemv_int8_supported(int64_t T, int N) {
                     groups(T, N, 3, 8) <= cus);
 }
 
-// Quantizing on the way pays while the launch it saves (2.0 to 2.4 us) is more than
-// the work that every workgroup repeats: T 8, N 20480, K 2048 8.1 us against 10.2, T
-// 16 10.9 against 10.3; T 4, N 28672, K 4096 (117 MB of weight) 24.9 against 22.6.
+// Quantizing on the way pays while the launch it saves (2.0 to 2.4 us, and 4 of the host's)
+// is more than the work that every workgroup repeats: T 8, N 20480, K 2048 8.1 us against
+// 10.2, T 16 13.0 against 10.8, N 12288 8.1 against 8.4, N 4096 5.6 against 6.3; K 4096, T
+// 16, N 4096 7.6 against 7.9, N 8192 13.0 against 10.6; T 4, N 28672, K 4096 (117 MB of
+// weight) 24.9 against 22.6.
 bool gemv_int8_bf16_supported(int64_t T, int K, int N) {
-  return T >= 1 && T <= 8 && K <= 4096 && (int64_t)N * K <= 64 << 20;
+  return T >= 1 && (T <= 8 || (T <= 16 && N <= (K <= 2048 ? 12288 : 4096))) && K <= 4096 && (int64_t)N * K <= 64 << 20;
 }
 
 hipError_t launch_gemv_int8_bf16(const void* x, int64_t T, int K, const uint8_t* w, const float* ws, int N, void* kv,

@@ -208,7 +208,8 @@ int engram_int8_quantize(const void* x, int64_t T, int32_t K, int8_t* xq, float*
  *              (NULL allowed when that size is 0). For MXFP8 and INT8 it holds
  *              x's codes and scales (INT8: on no operand and not on kv, else
  *              ENGRAM_EINVAL; none for up to 8 tokens of K <= 4096 where the
- *              weight is at most 64 MiB, which are quantized in the product's
+ *              weight is at most 64 MiB, nor for up to 16 where K <= 2048 and N
+ *              <= 12288 or N <= 4096 as well: they are quantized in the product's
  *              launch). 256-byte aligned.
  *   With MXFP4 weights x stays bf16 and W enters as its bf16 values, which
  *   are exact (a value of 2^128 or more, scale bytes 253 and 254 only, is an

@@ -44,9 +44,9 @@ int main(void) {
   expect(engram_wkv_int8(q, xs, INT64_MAX, 131056, wq, ws, 1 << 28, kv, NULL), UNS, "i8 T too large");
   expect(engram_wkv_int8(q, xs, 4, 256, wq, ws, 64, xs, NULL), INV, "i8 kv on x scales");
   expect(engram_wkv_int8(q, xs, 4, 256, wq, ws, 64, s, NULL), INV, "i8 kv on scales");
-  expect(engram_wkv(x, 12, 256, w, sc, I8, 64, kv, NULL, 0, NULL), INV, "wkv i8 without its workspace");
-  expect(engram_wkv(x, 12, 256, w, sc, I8, 64, kv, kv, 4096, NULL), INV, "wkv i8 workspace on kv");
-  expect(engram_wkv(x, 12, 256, w, NULL, I8, 64, kv, stage, 4096, NULL), INV, "wkv i8 NULL scales");
+  expect(engram_wkv(x, 20, 256, w, sc, I8, 64, kv, NULL, 0, NULL), INV, "wkv i8 without its workspace");
+  expect(engram_wkv(x, 20, 256, w, sc, I8, 64, kv, kv, 4096, NULL), INV, "wkv i8 workspace on kv");
+  expect(engram_wkv(x, 20, 256, w, NULL, I8, 64, kv, stage, 4096, NULL), INV, "wkv i8 NULL scales");
   expect(engram_wkv(x, 4, 256, w, sc, I8, 64, x, NULL, 0, NULL), INV, "wkv i8 kv on x");
   expect(engram_wkv(NULL, 0, 256, NULL, NULL, I8, 64, NULL, NULL, 0, NULL), OK, "wkv i8 T=0");
   expect((int)engram_wkv_workspace_size(4, 256, 64, I8), 0, "no workspace for few tokens");

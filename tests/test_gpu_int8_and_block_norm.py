@@ -105,7 +105,7 @@ def test_int8_small_batches(T, K, N):
     wq, ws = _int8(rng, N, K)
     wd, sd = _dev(wq), _dev(ws)
     _check_kv(E.wkv_int8(_dev(xq), _dev(xs), wd, sd), xq, xs, wq, ws, "wkv_int8")
-    if T <= 8:
+    if T <= 16:
         x = bf16(rng, T, K)
         _check_kv(E.wkv(x.to(DEV), wd, sd), *o.int8_quantize(bits(x)), wq, ws, "wkv")
 

@@ -128,16 +128,17 @@ def test_product_refusals(lib):
 
 def test_wkv_and_partials_with_int8_weights_refuse(lib):
     # a few tokens are quantized in the product's launch
-    assert [lib.engram_wkv_workspace_size(T, 64, 32, I8) for T in (0, 1, 8, 9)] == [0, 0, 0, 1024]
-    assert lib.engram_wkv_workspace_size(8, 4096, 16384, I8) == 0
+    assert [lib.engram_wkv_workspace_size(T, 64, 32, I8) for T in (0, 1, 16, 17)] == [0, 0, 0, 1280 + 256]
+    assert [lib.engram_wkv_workspace_size(8, 4096, 16384, I8), lib.engram_wkv_workspace_size(16, 64, 12288, I8)] == [0, 0]
+    assert lib.engram_wkv_workspace_size(9, 64, 12292, I8) == 768 + 256
     assert lib.engram_wkv_workspace_size(8, 4112, 64, I8) == 8 * 4112 + 256 - 8 * 4112 % 256 + 256
     assert lib.engram_wkv_workspace_size(8, 4096, 16388, I8) == 8 * 4096 + 256
-    need = lib.engram_wkv_workspace_size(12, 64, 32, I8)
-    assert need == 768 + 256
+    need = lib.engram_wkv_workspace_size(20, 64, 32, I8)
+    assert need == 1280 + 256
     WK = 13 << 28
 
     def f(kv=KV, ws=WK, n=need, x=X, K=64):
-        return lib.engram_wkv(x, 12, K, W, WS, I8, 32, kv, ws, n, None)
+        return lib.engram_wkv(x, 20, K, W, WS, I8, 32, kv, ws, n, None)
 
     assert f(n=need - 1) == INV and f(ws=None) == INV and f(ws=WK + 16) == INV and f(K=72) == UNS
     for base in (X, X + 1280, W, W + 1792, WS, KV, KV + 512):

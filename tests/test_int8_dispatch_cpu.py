@@ -101,10 +101,12 @@ def test_grids_cover_and_lds_fits(dispatch):
 
 
 def test_bf16_rows_of_a_few_tokens_take_one_launch(dispatch):
-    (s1, a), (s2, b), (s3, c) = dispatch.calls(["wkv 8 2048 20480 3", "wkv 9 2048 20480 3", "wkv 4 4096 28672 3"])
-    assert (s1, s2, s3) == (0, 0, 0)
-    assert len(a) == 1 and a[0].kernel.endswith("true>")
-    assert len(b) == 2 and len(c) == 2 and b[0].kernel.startswith("int8_quantize")
+    for line, n in (("wkv 8 2048 20480 3", 1), ("wkv 9 2048 20480 3", 2), ("wkv 16 2048 12288 3", 1), ("wkv 17 2048 12288 3", 2),
+                    ("wkv 16 4096 4096 3", 1), ("wkv 16 2064 4100 3", 2), ("wkv 8 2064 4100 3", 1),
+                    ("wkv 16 512 12292 3", 2), ("wkv 4 4096 28672 3", 2)):
+        (status, launches), = dispatch.calls([line])
+        assert status == 0 and len(launches) == n, line
+        assert launches[0].kernel.startswith("int8_quantize") if n == 2 else launches[0].kernel.endswith("true>"), line
 
 
 def test_forward_routes(dispatch):
