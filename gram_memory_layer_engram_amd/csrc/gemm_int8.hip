@@ -18,6 +18,8 @@
 //
 // The scales wait in registers, two of the wave's 128 (64) rows and tokens a
 // lane, and go through LDS once the loop has left it.
+#include <algorithm>
+
 #include "gemm_tile.h"
 
 namespace engram {
@@ -342,11 +344,11 @@ __device__ __forceinline__ void deep_tile(const GemmI8Args& p, char* smem, int b
 
 // Two 128x128 workgroups on a compute unit that run in step load at the same time,
 // multiply at the same time and store at the same time; over several rounds they may
-// stay so. The second one of the first round therefore starts `pause` * 256 clocks late:
-// 16, about half a small tile, is the best or within 3% of 8 to 32 (N 5784, K 912, T 4643
-// 47.4 -> 45.4 us; N 4264, K 448, T 5058 24.8 -> 21.3; N 9096, K 304, T 3108 29.1 ->
-// 25.9), and without it the same launch now and then takes half as long again (N 10240,
-// K 512, T 3000 27 to 49 us, with it 27 to 30). A launch of one round gains nothing.
+// stay so. The second one of the first round therefore starts `pause` * 256 clocks late,
+// about half a tile: N 5784, K 912, T 4643 47.4 -> 42 - 44 us; N 4264, K 448, T 5058 24.8 ->
+// 21 - 22; and without it the same launch may take half as long again (N 10240, K 512, T
+// 3000 27 or 49, with it 26 - 28; N 19828, K 640, T 3388 81 or 116, 70 - 72). A launch of
+// one round gains nothing.
 template <int NT, bool KTAIL>
 __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(NT == 4 ? 1 : 2, NT == 4 ? 1 : 2)))
 void gemm_int8_kernel(const GemmI8Args p, int tiles_n, int tiles_t, uint32_t cus, int pause, GateEpi ep) {
@@ -394,8 +396,9 @@ template <int NT>
 hipError_t launch_ring(const GemmI8Args& p, hipStream_t s, const GateEpi& ep) {
   const int tiles_n = (p.N + 64 * NT - 1) / (64 * NT), tiles_t = (p.T + 64 * NT - 1) / (64 * NT);
   const int64_t tiles = (int64_t)tiles_n * tiles_t, cus = dev_info().num_cus;
+  const int pause = tiles > 2 * cus ? std::min(25, 5 * ((p.K + Q_ROW - 1) / Q_ROW)) : 0;
   return launch_gemm(p.K % Q_ROW ? gemm_int8_kernel<NT, true> : gemm_int8_kernel<NT, false>, tiles, Q_LDS * NT / 4, s, p,
-                     tiles_n, tiles_t, (uint32_t)cus, tiles > 2 * cus ? 16 : 0, ep);
+                     tiles_n, tiles_t, (uint32_t)cus, pause, ep);
 }
 
 hipError_t launch_deep(const GemmI8Args& p, hipStream_t s) {
