@@ -158,7 +158,7 @@ def test_wkv_and_partials_with_int8_weights_refuse(lib):
     def g(value=V, partials=PA, ws=WK):
         return lib.engram_wkv_gate_partials(X, T, K, W, WS, I8, hc, dim, H, Q, KW, value, partials, ws, need, None)
 
-    for base, size in ((X, 2048), (W, 196608), (WS, 3072), (H, 4096), (Q, 1024), (KW, 1024)):
+    for base, size in ((X, 2048), (W, 768 * 256), (WS, 4 * 768), (H, 4096), (Q, 1024), (KW, 1024)):
         assert g(value=base + size - 16) == INV and g(partials=base + size - 8) == INV
         assert g(ws=base + (size - 1) // 256 * 256) == INV, hex(base)
     assert g(partials=V + 2048 - 8) == INV and g(ws=V) == INV and g(ws=PA) == INV
