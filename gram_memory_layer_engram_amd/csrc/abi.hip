@@ -97,14 +97,14 @@ hipError_t run_mx_projection(const uint8_t* xq, const uint8_t* xs, int64_t T, in
              : launch_gemm_mxfp8(xq, xs, T, K, (const uint8_t*)w, w_scales, N, kv, s, ep);
 }
 
-// A tensor's address range; no range where the pointer is null.
+// A tensor's address range; no range where the pointer is null or it has no bytes.
 struct Span {
   const void* p;
   int64_t bytes;
 };
 inline bool meet(const Span& a, const Span& b) {
   const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
-  return x && y && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+  return x && y && a.bytes > 0 && b.bytes > 0 && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
 }
 
 // Whether an output lies on an operand of a product (the tiles that come later
