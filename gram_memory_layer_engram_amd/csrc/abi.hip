@@ -530,9 +530,14 @@ int engram_gate(const void* hidden, const void* kv, const void* q_weight,
 
 // Forward workspace: a 64 KiB flag area (used by engram_forward_single_launch;
 // zero before the first call, left zero by every call), then staged rows
-// [T, K] bf16 | kv [T, N] bf16 | MXFP8 staging, or the single-launch
+// [T, K] bf16 | kv [T, N] bf16 | 8-bit staging, or the single-launch
 // scratch, whichever is larger.
 constexpr size_t kSyncBytes = kDecodeSyncBytes;
+
+// None with INT8 weights: the gather writes the codes.
+static size_t staged_rows_bytes(int32_t w_format, int64_t T, int64_t K) {
+  return w_format == ENGRAM_W_INT8 ? 0 : round_up((size_t)T * K * 2);
+}
 
 static bool use_decode_path(const engram_forward_args* a, int32_t K, int32_t N) {
   return a->w_format == ENGRAM_W_MXFP8 && decode_forward_supported(a->T, K, N, a->head_dim, a->dim, a->hc);
@@ -543,7 +548,7 @@ size_t engram_forward_workspace_size(const engram_forward_args* a) {
     return 0;
   const int64_t K = (int64_t)a->n_cols * a->head_dim;
   const int64_t N = (int64_t)(a->hc + 1) * a->dim;
-  size_t bytes = round_up((size_t)a->T * K * 2) + round_up((size_t)a->T * N * 2);
+  size_t bytes = staged_rows_bytes(a->w_format, a->T, K) + round_up((size_t)a->T * N * 2);
   if (K <= INT32_MAX && N <= INT32_MAX) bytes += wkv_scratch_bytes(a->T, K, a->w_format);
   if (K <= INT32_MAX && N <= INT32_MAX && use_decode_path(a, (int32_t)K, (int32_t)N))
     bytes = std::max(bytes, decode_forward_scratch_bytes(a->T, (int)K, (int)N, a->dim));
@@ -588,12 +593,12 @@ static bool big_tiles(int32_t w_format, int64_t T, int32_t N, int32_t K) {
 }
 
 // engram_forward's launches, given checked arguments and the workspace past
-// its flag area (rows | kv | MXFP8 staging; nothing in it needs to start at
+// its flag area (rows | kv | 8-bit staging; nothing in it needs to start at
 // zero: every byte a kernel reads was written earlier in the same call).
 static int run_forward(const engram_forward_args* a, int32_t K, int32_t N, uint8_t* ws, hipStream_t s) {
   int st = ENGRAM_OK;
   void* rows = ws;
-  void* kv = ws + round_up((size_t)a->T * K * 2);
+  void* kv = ws + staged_rows_bytes(a->w_format, a->T, K);
   void* mx = (uint8_t*)kv + round_up((size_t)a->T * N * 2);
   // Unless ENGRAM_FORWARD_STORE_KV is set, when a tiled GEMM runs and a
   // 256-column tile lies inside one key block (dim % 256 == 0), its epilogue

@@ -469,7 +469,8 @@ int engram_gate(const void* hidden, const void* kv, const void* q_weight,
  * engram_forward -- one Engram layer forward: lookup -> (MXFP8 quantize) ->
  *   wkv -> gate, all on `stream`. With ENGRAM_W_MXFP4 the staged rows stay
  *   bf16 (no quantize step), as engram_wkv; with ENGRAM_W_INT8 the gather
- *   quantizes each token's row of K (engram_int8_quantize's rule).
+ *   quantizes each token's row of K (engram_int8_quantize's rule) and stages
+ *   its codes alone.
  *   [P-common] Engram.forward: kv = wkv(embed(hash_ids).flatten(-2)), then the
  *   fused gate over [T, hc, dim]; the staged rows and kv live in the caller's
  *   workspace (the pages keep them as persistent buffers: Engram.staged_rows,
@@ -569,14 +570,15 @@ int engram_forward_single_launch(const engram_forward_args* a, void* workspace,
  *   device memory (code under HIP graph capture, tight serving loops,
  *   harnesses that forbid hipMalloc): the same launches and results, bit for
  *   bit, as engram_forward with a caller workspace, but the scratch (staged
- *   rows, kv or value + gate partials, MXFP8 staging) lives in a fixed
+ *   rows, kv or value + gate partials, 8-bit staging) lives in a fixed
  *   buffer of ENGRAM_NOALLOC_SCRATCH_BYTES inside the library, one per GPU,
  *   held until the process ends. The call allocates and frees nothing.
  *
  *   Arguments, checks and errors as engram_forward, plus ENGRAM_ENOSPACE
  *   (nothing launched) when engram_forward_workspace_size(a) - 64 KiB
  *   exceeds ENGRAM_NOALLOC_SCRATCH_BYTES: at dim 4096 and K 2048 that is
- *   about 740 tokens; every decode batch (T <= 64) fits.
+ *   about 740 tokens (780 with ENGRAM_W_INT8); every decode batch (T <= 64)
+ *   fits.
  *   Every call on one GPU uses that GPU's one buffer and leaves its last
  *   contents there (nothing in it has to start at zero). Calls that overlap
  *   on one GPU (different streams or threads without ordering between them)

@@ -1,0 +1,63 @@
+"""GPU: calls of the int8 products and of the norms around a block."""
+
+from __future__ import annotations
+
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+
+def _E():
+    from gram_memory_layer_engram_amd import engram as E
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    E.load_library()
+    return E
+
+
+def _say(msg):
+    print(f"[gpu-test] {msg}", flush=True)
+    sys.stdout.flush()
+
+
+def _int8_weight(g, N, K):
+    return (torch.randint(-128, 128, (N, K), generator=g, device=DEV, dtype=torch.int8),
+            torch.rand((N,), generator=g, device=DEV) * 2.0 ** -10 + 2.0 ** -11)
+
+
+def _forward_case(T, dim, hc, C, hd, rows=5000, seed=3):
+    g = torch.Generator(device=DEV).manual_seed(seed + T)
+    bf = lambda *s: torch.randn(s, generator=g, device=DEV).to(torch.bfloat16)   # noqa: E731
+    w, ws = _int8_weight(g, (hc + 1) * dim, C * hd)
+    ids = torch.randint(0, rows, (T, C), generator=g, device=DEV, dtype=torch.int32)
+    return bf(rows, hd), ids, w, ws, bf(T, hc, dim), bf(hc, dim), bf(hc, dim)
+
+
+@pytest.mark.parametrize("T,dim,hc,C,hd", [(1, 512, 4, 8, 64), (70, 512, 2, 8, 64), (300, 512, 2, 9, 112), (770, 4096, 4, 16, 128)])
+@pytest.mark.parametrize("store_kv", [False, True])
+def test_forward_noalloc_and_a_workspace_of_the_stated_size(T, dim, hc, C, hd, store_kv):
+    """A caller's workspace of engram_forward_workspace_size bytes, full of garbage behind
+    its flags, and the library's own scratch give what a fresh workspace gives (with kv
+    stored: what the single calls give); nothing past the workspace is written."""
+    E = _E()
+    _say(f"noalloc int8 {T} {dim} {hc} {C} {hd} {store_kv}")
+    c = _forward_case(T, dim, hc, C, hd)
+    table, ids, w, ws, hidden, q, k = c
+    xq, xs = E.int8_quantize(table[ids.long()].reshape(T, C * hd))
+    kv = E.wkv_int8(xq, xs, w, ws)
+    want = E.gate(hidden, kv, q, k)
+    a = E.forward_args(table, ids, w, ws, hidden, q, k, None, 1e-6, 1e-6, hidden, store_kv=store_kv)
+    need = E.forward_workspace_size(a)
+    room = torch.full((need + 4096,), 0x7f, dtype=torch.uint8, device=DEV)
+    room[:65536] = 0
+    out = E.forward(*c, workspace=room[:need], store_kv=store_kv)
+    assert bool((room[need:] == 0x7f).all()) and not bool(room[:65536].any())
+    assert torch.equal(out, E.forward(*c, store_kv=store_kv))
+    assert not store_kv or torch.equal(out, want)
+    assert torch.equal(E.forward_noalloc(*c, store_kv=store_kv), out)

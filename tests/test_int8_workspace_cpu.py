@@ -44,3 +44,22 @@ def test_a_workspace_that_is_used_may_not(dispatch):
     lines = [f"wkvat {T} {K} {N} {p} {ofs} {need}" for p in (0, 2, 3, 4) for ofs in (0, -256)]
     assert [s for s, _ in dispatch.calls(lines)] == [INV] * 8
     assert dispatch.calls([f"wkvat {T} {K} {N} 5 0 {need}"])[0][0] == OK
+
+
+def test_the_forward_keeps_no_staged_rows_on_int8_weights(dispatch):
+    """Its gather writes int8 codes: codes and scales and kv are all it keeps, beside
+    the 64 KiB of flags."""
+    for T, hc, dim, c, hd in ((1, 4, 4096, 16, 128), (300, 2, 512, 8, 64), (1000, 4, 4096, 16, 128)):
+        K, N = c * hd, (hc + 1) * dim
+        pad = lambda b: -(-b // 256) * 256   # noqa: E731
+        need = 65536 + pad(2 * T * N) + pad(T * K) + pad(4 * T)
+        assert dispatch.calls([f"fwdsize {T} {hc} {dim} {c} {hd} 3"])[0][0] == -(-need // 1024)
+        # the other formats stage bf16 rows
+        assert dispatch.calls([f"fwdsize {T} {hc} {dim} {c} {hd} 2"])[0][0] == -(-(65536 + pad(2 * T * N) + pad(2 * T * K)) // 1024)
+
+
+def test_noalloc_takes_what_fits_the_scratch(dispatch):
+    """32 MiB at hc 4, dim 4096, K 2048: 43012 bytes a token."""
+    T = 32 * 2 ** 20 // (2 * 20480 + 2048 + 4) - 1
+    assert dispatch.calls([f"noalloc {T} 4 4096 16 128 3"])[0][0] == OK
+    assert dispatch.calls([f"noalloc {T + 2} 4 4096 16 128 3"])[0][0] == 4
