@@ -4,9 +4,10 @@ from __future__ import annotations
 
 import sys
 
-import numpy as np
 import pytest
 import torch
+
+from tests._threads import run_together
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +62,33 @@ def test_forward_noalloc_and_a_workspace_of_the_stated_size(T, dim, hc, C, hd, s
     assert torch.equal(out, E.forward(*c, store_kv=store_kv))
     assert not store_kv or torch.equal(out, want)
     assert torch.equal(E.forward_noalloc(*c, store_kv=store_kv), out)
+
+
+def test_two_threads_both_end_with_the_serial_results():
+    """Norms, both products and the quantizer of two host threads at once, each on its own
+    stream and of its own sizes: both threads come to their end, with the serial bits."""
+    E = _E()
+    work = []
+    for T, dim, N in ((3, 1024, 4096), (150, 2064, 1280)):
+        _say(f"threads {T} {dim} {N}")
+        g = torch.Generator(device=DEV).manual_seed(T)
+        x, r = (torch.randn((T, 2, dim), generator=g, device=DEV).to(torch.bfloat16) for _ in range(2))
+        gate = torch.rand((T, 2), generator=g, device=DEV)
+        w, ws = _int8_weight(g, N, dim)
+
+        def calls(x=x, r=r, gate=gate, w=w, ws=ws, n=2 * T, dim=dim):
+            res, out, xq, xs = E.post_pre_norm(x, r, gate=gate, out_format="both", q_format="int8")
+            rows = out.view(n, dim)
+            return res, out, xq, xs, E.wkv_int8(xq.view(n, dim), xs.view(n), w, ws), E.wkv(rows, w, ws), *E.int8_quantize(rows)
+
+        def thread(calls=calls, want=calls(), stream=torch.cuda.Stream()):
+            with torch.cuda.stream(stream):
+                got = [calls() for _ in range(60)]
+                stream.synchronize()
+                for i in got:
+                    for a, b in zip(i, want):
+                        assert torch.equal(a, b)
+
+        work.append(thread)
+    torch.cuda.synchronize()
+    run_together(work)
