@@ -288,8 +288,9 @@ int engram_wkv_int8(const int8_t* xq, const float* xs, int64_t T, int32_t K, con
  *                           engram_mx_quantize, taken on the fp32 y (one
  *                           rounding; a non-finite 32-element block gets byte
  *                           255 and codes 0x7F)
- *   The norm is taken of the unrounded sum s. Sums in fp32, fixed order (an
- *   |s| past about 1e18 overflows its square).
+ *   The norm is taken of the unrounded sum s. Sums in fp32, fixed order: where
+ *   sum(s^2) passes 2^128 (|s| of 2^64 / sqrt(dim) throughout, 2.9e17 at dim
+ *   4096) 1 / sqrt is 0 and so is the row's y.
  *
  *   x, residual   bf16, element (t, h, d) at t*stride_t + h*stride_h + d
  *                 (strides in elements, multiples of 8, >= 0: slices of wider
@@ -328,10 +329,11 @@ int engram_add_rms_norm(const void* x, int64_t x_stride_t, int64_t x_stride_h, c
  *   g is 1, one factor per row (ENGRAM_GATE_ROW, such as gate_out of
  *   engram_gate) or one per channel (ENGRAM_GATE_CHANNEL), through a sigmoid
  *   where gate_sigmoid is set. Everything is fp32 up to the outputs, each rounded
- *   once from there (the norm is of the unrounded s); sums in a fixed order. An
- *   |x| or |s| past about 1e18 overflows its square. NaN and infinities spread
- *   over their row as the formulas say; an int8 row with one of them in s *
- *   pre_weight gets scale NaN.
+ *   once from there (the norm is of the unrounded s); sums in a fixed order. Where
+ *   sum(x^2) or sum(s^2) passes 2^128 (a magnitude of 2^64 / sqrt(dim)
+ *   throughout, 2.9e17 at dim 4096) 1 / sqrt is 0 and so is the row's p or y (an
+ *   int8 row's scale). NaN and infinities spread over their row as the formulas
+ *   say; an int8 row with one of them in s * pre_weight gets scale NaN.
  *
  *   x, residual   bf16, element (t, h, d) at t*stride_t + h*stride_h + d (strides
  *                 in elements, multiples of 8, >= 0; stride_h 0: one row for

@@ -92,3 +92,37 @@ def test_two_threads_both_end_with_the_serial_results():
         work.append(thread)
     torch.cuda.synchronize()
     run_together(work)
+
+
+@pytest.mark.parametrize("dim", [64, 2080, 4096, 16384])
+def test_norms_of_rows_as_long_as_fp32_holds(dim):
+    """A row's sum of squares is an fp32: up to 2^128 the norm of a row of one magnitude
+    is 1 in bf16 (sums and root are off by at most dim / 128 + 11 half steps of 2^-24, far
+    below the half step of 2^-9 under 1), past it 0, which is not NaN and reaches no other row."""
+    E = _E()
+    _say(f"long rows {dim}")
+    limit = 2.0 ** 64 / dim ** 0.5
+    sign = torch.ones((dim,), device=DEV)
+    sign[::3] = -1
+    rows = torch.tensor([0.9 * limit, 1.2 * limit, 1.0, -0.98 * limit, 3e38], device=DEV)   # bf16: within 2^-8
+    x = (rows.view(-1, 1) * sign).to(torch.bfloat16)
+    unit = torch.tensor([1.0, 0.0, 1.0, -1.0, 0.0], device=DEV).view(-1, 1) * sign
+    two = torch.full_like(x, 2.0)
+    # the norm after the block: the branch
+    res, out, _, _ = E.post_pre_norm(x, two)
+    assert torch.equal(res.float(), 2 + unit)
+    # the norm before the next one, in every format
+    kw = dict(post_norm=False)
+    res, out, xq, xs = E.post_pre_norm(x, out_format="both", q_format="int8", **kw)
+    assert torch.equal(res, x) and torch.equal(out.float(), unit)
+    short = torch.tensor([True, False, True, True, False], device=DEV)
+    assert bool((xs[~short] == 0).all())
+    n = (dim / 128 + 16) * 2.0 ** -24
+    assert bool(((xs[short].double() * 127 - 1).abs() <= n).all()) and torch.equal(xq[short].float(), 127 * unit[short])
+    _, _, xq, xs = E.post_pre_norm(x, out_format="mxfp8", **kw)
+    v = xq.view(torch.float8_e4m3fn).float() * xs.view(torch.float8_e8m0fnu).float().repeat_interleave(32, -1)
+    # the MX rule: a largest of just under 1 has the exponent -1, the block scale 2^-9 and, of 512
+    # steps, the code's largest, 448: 0.875; at 1 or above the scale is 2^-8, the code 256
+    assert bool(((v == unit) | (v == 0.875 * unit)).all())
+    _, out, _, _ = E.add_rms_norm(x)
+    assert torch.equal(out.float(), unit)
