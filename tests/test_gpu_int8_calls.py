@@ -126,3 +126,28 @@ def test_norms_of_rows_as_long_as_fp32_holds(dim):
     assert bool(((v == unit) | (v == 0.875 * unit)).all())
     _, out, _, _ = E.add_rms_norm(x)
     assert torch.equal(out.float(), unit)
+
+
+def test_row_gate_sigmoid_error():
+    """The sigmoid of a row's gate, read from the int8 rows' fp32 scales: with x = 1 (2^100
+    below -40, to stay clear of subnormals) and eps = 2^112, which takes in s^2, the scale is
+    sigmoid * x * 2^-56 / 127, the quotient's rounding the only one behind the sigmoid.
+
+    Of a value: fl(z * log2 e) is off by half a step, 2^-21 below 16 and 2^-20 below 32, and
+    by |z| * 2^-25.6 for log2 e; times ln 2 (z 11: 0.35 + 0.15, z 16: 0.69 + 0.23 of 2^-20);
+    exp and reciprocal one step each (2^-23), the sum half (2^-24): 0.31 of 2^-20."""
+    E = _E()
+    g = torch.Generator(device=DEV).manual_seed(1)
+    z = torch.cat([(torch.rand((1 << 19,), generator=g, device=DEV) * 2 - 1) * top for top in (1, 11, 16, 80)]
+                  + [torch.linspace(-16, -15, 1 << 18, device=DEV), torch.linspace(-11, -10, 1 << 18, device=DEV),
+                     torch.arange(-80, 81, device=DEV) * 1.0])
+    up = torch.where(z < -40, 2.0 ** 100, 1.0)
+    x = up.view(-1, 1).expand(-1, 8).to(torch.bfloat16)
+    _, _, _, xs = E.post_pre_norm(x, gate=z, gate_act="sigmoid", post_norm=False, eps=2.0 ** 112, out_format="int8")
+    got = xs.double() * 127 * 2.0 ** 56 / up.double()
+    want = 1 / (1 + torch.exp(-z.double()))
+    err = (got - want).abs() / want
+    for lo, hi, tol in ((0, 11, 2.0 ** -20), (11, 16, 2.0 ** -19), (16, 80, 2.0 ** -17)):
+        m = (z.abs() >= lo) & (z.abs() <= hi)
+        _say(f"sigmoid, |z| {lo} - {hi}: {float(err[m].max() * 2.0 ** 20):.3f} of 2^-20")
+        assert float(err[m].max()) <= tol + 2.0 ** -24
