@@ -344,11 +344,15 @@ __device__ __forceinline__ void deep_tile(const GemmI8Args& p, char* smem, int b
 
 // Two 128x128 workgroups on a compute unit that run in step load at the same time,
 // multiply at the same time and store at the same time; over several rounds they may
-// stay so. The second one of the first round therefore starts `pause` * 256 clocks late,
-// about half a tile: N 5784, K 912, T 4643 47.4 -> 42 - 44 us; N 4264, K 448, T 5058 24.8 ->
-// 21 - 22; and without it the same launch may take half as long again (N 10240, K 512, T
-// 3000 27 or 49, with it 26 - 28; N 19828, K 640, T 3388 81 or 116, 70 - 72). A launch of
-// one round gains nothing.
+// stay so. The second one of the first round (workgroups cus .. 2 cus - 1, as they are
+// handed out one to a compute unit, then another; only time rests on that) therefore
+// starts `pause` * 256 clocks late: 5 for each slice of a tile, at most 25, about the 3 us
+// a tile takes outside its loop. That much whatever the K above 640 (us without / 12 / 25 /
+// 40 / 60): N 19828, K 640, T 3388 81 / 80 / 72 / 79 / 84, N 11932, K 928, T 4299 84 / 84 / 80 /
+// 80 / 86, N 15876, K 1120, T 2687 80 / 78 / 73 / 73 / 79; from K 1680 on none of them is 3%
+// from another (N 7380, K 1872, T 2861 60.5 / 60.1 / 60.4 / 60.3 / 60.0). Shorter K: N 4264,
+// K 448, T 5058 24.8 -> 21 - 22. Without it the same launch may take half as long again (N
+// 10240, K 512, T 3000 27 or 49, with it 26 - 28). A launch of one round gains nothing.
 template <int NT, bool KTAIL>
 __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(NT == 4 ? 1 : 2, NT == 4 ? 1 : 2)))
 void gemm_int8_kernel(const GemmI8Args p, int tiles_n, int tiles_t, uint32_t cus, int pause, GateEpi ep) {

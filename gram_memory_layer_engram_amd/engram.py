@@ -494,8 +494,8 @@ def add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None = None, weight: 
     residual_out comes with a residual.
 
     x and residual: bf16 [T, hc, dim] (or [T, dim]), last dimension contiguous,
-    other strides free (a slice of a wider tensor, or an expanded copy
-    dimension). weight: bf16 [dim], or [hc, dim] with one row per copy. The
+    other strides multiples of 8 (a slice of a wider tensor, or an expanded copy
+    dimension), 16-byte aligned. weight: bf16 [dim], or [hc, dim] with one row per copy. The
     outputs may be given (contiguous); residual_out may be residual itself and
     out may be x itself."""
     L = _lib or load_library()
@@ -628,10 +628,11 @@ def post_pre_norm(x: torch.Tensor, residual: torch.Tensor | None = None, post_we
     ``q_format``) or "none" (residual_out alone).
 
     x and residual: bf16 [T, hc, dim] (or [T, dim]), last dimension contiguous,
-    other strides free. gate: fp32 [T, hc] (or [T]), one factor a row, or bf16 of
-    x's shape; ``gate_act`` "sigmoid" takes it through one. Weights: bf16 [dim],
-    or [hc, dim]. post_eps is eps where not given. The outputs may be given
-    (contiguous); residual_out may be residual itself and out may be x itself."""
+    other strides multiples of 8 (0 among them), 16-byte aligned. gate: fp32
+    [T, hc] (or [T]) of any strides, one factor a row, or bf16 laid out as x is;
+    ``gate_act`` "sigmoid" takes it through one. Weights: bf16 [dim], or [hc, dim].
+    post_eps is eps where not given. The outputs may be given (contiguous);
+    residual_out may be residual itself and out may be x itself."""
     L = _lib or load_library()
     shape = x.shape
     if len(shape) == 3:

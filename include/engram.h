@@ -223,8 +223,9 @@ int engram_int8_quantize(const void* x, int64_t T, int32_t K, int8_t* xq, float*
  *   Kernels: a tiled GEMM; for T <= 64 a weight-streaming GEMV instead
  *   (MXFP8 with K/128 <= 32; bf16 with K % 32 == 0, K <= 2048, N % 16 == 0
  *   where it beats the GEMM; MXFP4 while a tile's scale bytes fit LDS: K up
- *   to 35840 whatever T and x are; INT8 also past that where the
- *   GEMM's tiles are few).
+ *   to 35840 whatever T and x are; INT8 for T <= 96 whatever K and N are, for
+ *   T <= 128 up to N 16384, and past that where 64 x 64 or 48 x 128 tiles of
+ *   kv are no more than the compute units).
  *   The two sum in different fp32 orders, so their kv can differ in the last
  *   bit; INT8 sums are exact, its kv is the same from both.
  */
