@@ -2,10 +2,9 @@
 // bf16(float(x . W^T) * xs[t] * ws[n]), x int8 with one fp32 scale a token, or (up
 // to 16 tokens) bf16, quantized by the rule of int8_rule.h on the way.
 //
-// With few tokens the product is a stream of the weight, a byte a weight
-// ("vllm.models.deepseek_v41.amd.mono.attention.gemv": weight loads in flight
-// before the activations, split over k). A workgroup owns RT tiles of 16 rows and
-// all T tokens (past 64 a group of 64 or 128 of them). The sums are whole numbers, exact in any order: k may be split and
+// With few tokens the product is a stream of the weight, a byte a weight. A
+// workgroup owns RT tiles of 16 rows and all T tokens (past 64 a group of 64 or 128
+// of them). The sums are whole numbers, exact in any order: k may be split and
 // started anywhere, and kv is that of the tiled GEMM bit for bit.
 //
 // W goes through LDS (gemv_int8_dma.h): a fragment read straight from memory

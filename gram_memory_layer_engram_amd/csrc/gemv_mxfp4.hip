@@ -2,10 +2,8 @@
 // bf16(x . deq(W)^T), x bf16 (fp32 sums) or MXFP8 (fp32 but for runs of 8 k).
 //
 // W is e2m1 codes [N, K/2] with one E8M0 byte per row and 32 k [N, K/32] (OCP
-// MX v1.0 MXFP4). With few tokens the product is a stream of the weight
-// ("vllm.models.deepseek_v41.amd.mono.attention.gemv": weight loads in flight
-// before the activations, split over k), here of 17/32 byte per weight: half
-// of MXFP8's, a quarter of bf16's.
+// MX v1.0 MXFP4). With few tokens the product is a stream of the
+// weight, here of 17/32 byte per weight: half of MXFP8's, a quarter of bf16's.
 //
 // A workgroup owns RT tiles of 16 W rows and all T tokens (NT tiles of 16);
 // each of its waves takes a contiguous run of k steps of 128, and the waves'

@@ -1,7 +1,6 @@
 // Quantization of bf16 rows to 8-bit integers, one fp32 scale a row (the rule:
 // int8_rule.h), from dense rows x [T, K] or from the gather itself: with int8
-// projection weights the staged rows never reach memory ("vllm.models.
-// deepseek_v4_1.common.engram", Engram.forward: wkv(embed(hash_ids).flatten(-2))).
+// projection weights the staged rows never reach memory.
 //
 // Bound: HBM, 2 bytes in and 1 out per element; for few rows a launch and one
 // trip to memory (two with a gather: ids, then rows). A row is owned by TPR

@@ -1,9 +1,8 @@
 // The norm after a block, its gate, the scaled residual and the norm before the
 // next block, in one pass over the streams.
 //
-// "vllm.models.deepseek_v4_1.common.engram", Engram.__init__ / forward: streams
-// [T, hc_mult, dim], rms_norm_eps, and a branch gated per token and copy. A block
-// between two norms adds to a stream, per row (t, h):
+// The layer's streams are [T, hc, dim], its branch is gated per token and copy. A
+// block between two norms adds to a stream, per row (t, h):
 //   p   = x / sqrt(sum(x^2) / dim + post_eps) * post_weight[h]
 //   s   = residual_scale * residual + branch_scale * (g * p)
 //   y   = s / sqrt(sum(s^2) / dim + eps) * pre_weight[h]

@@ -1,9 +1,8 @@
 // Residual addition and root-mean-square norm of the layer's streams, with
 // the norm's output in bf16, in MXFP8, or both.
 //
-// "vllm.models.deepseek_v4_1.common.engram", Engram.__init__ / forward: the
-// layer updates hidden [T, hc_mult, dim] and carries rms_norm_eps; what
-// follows it adds a branch to the streams and normalizes them. Per row (t, h):
+// The layer updates hidden [T, hc, dim]; what follows it adds a branch to the
+// streams and normalizes them. Per row (t, h):
 //   s   = x + residual                     (fp32; residual_out = bf16(s))
 //   inv = 1 / sqrt(sum(s^2) / dim + eps)
 //   y   = s * inv * weight[h]

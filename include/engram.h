@@ -278,9 +278,8 @@ int engram_wkv_int8(const int8_t* xq, const float* xs, int64_t T, int32_t K, con
 
 /*
  * engram_add_rms_norm -- residual addition and root-mean-square norm of the
- *   streams, with the output in bf16, in MXFP8, or both in one pass.
- *   [P-common] Engram.__init__ / forward: streams [T, hc_mult, dim] and
- *   rms_norm_eps. For every row (t, h):
+ *   streams [T, hc, dim], with the output in bf16, in MXFP8, or both in one
+ *   pass. For every row (t, h):
  *     s   = x[t,h,:] + residual[t,h,:]          (fp32; x alone without residual)
  *     y   = s / sqrt(sum(s^2)/dim + eps) * weight[h,:]
  *     residual_out[t,h,:] = bf16(s)
@@ -317,9 +316,8 @@ int engram_add_rms_norm(const void* x, int64_t x_stride_t, int64_t x_stride_h, c
 
 /*
  * engram_post_pre_norm -- the norm after a block, its gate, the scaled residual
- *   and the norm before the next block, in one pass.
- *   [P-common] Engram.__init__ / forward: streams [T, hc_mult, dim],
- *   rms_norm_eps, a gated branch added to each stream. For every row (t, h):
+ *   and the norm before the next block, in one pass over the streams [T, hc,
+ *   dim]. For every row (t, h):
  *     p   = x / sqrt(sum(x^2)/dim + post_eps) * post_weight[h,:]
  *           (post_norm 0: x * post_weight[h,:])
  *     s   = residual_scale * residual + branch_scale * (g * p)   (no residual: 0)
