@@ -427,6 +427,12 @@ static bool int8_deep(int64_t T, int64_t N, int K) {
   return 4 * tiles <= (T <= 128 ? 3 : 4) * cus && (K >= 4096 || (K >= 2048 && 2 * tiles > cus));
 }
 
+// The other GEMMs' model (gemm_tile.h) with times of this one's. It charges the split
+// as two launches with two 128x128 tiles on a compute unit; here it is one launch and
+// they run one on a compute unit, in the deep ring. The times are fitted to what is
+// launched, the charge keeps the split to where it surely pays: N 6588, K 4000, T 4955
+// 128x128 tiles 166 us, split 143; N 10924, K 2240, T 1764 59 and 55; the other way N
+// 11932, K 928, T 4299 80 and 84.
 static int int8_big_columns(int64_t T, int N, int K) {
   return big_columns(T, N, (K + 127) / 128 * 128, {9000, 1430, 3300, 870, 3200, 660});
 }

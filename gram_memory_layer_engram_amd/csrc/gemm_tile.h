@@ -1,5 +1,5 @@
 // What the tiled projection GEMMs share (gemm.hip: bf16 and MXFP8 weights,
-// gemm_fp4.hip: MXFP4 weights, gemm_int8.hip: int8 weights): block geometry, tile order, waits and the
+// gemm_fp4.hip: MXFP4 weights): block geometry, tile order, waits and the
 // epilogue. The design is described in gemm.hip.
 #pragma once
 
@@ -237,11 +237,6 @@ __device__ __forceinline__ void store_tile(f32x16 (&acc)[NT][NT], char* smem, ui
 // workgroups on a compute unit one's epilogue runs beside the other's loop. The
 // times (ns) are fitted to T 65-8192, N 96-35840, K 128-4096 for each kernel; kv
 // is the same bit for bit whatever the tile.
-// The int8 GEMM has the split in one launch, its 128x128 tiles there one on a
-// compute unit, and is charged as the others are, its times fitted to that. So it
-// splits where that pays for sure and leaves some of it: N 6588, K 4000, T 4955
-// 128x128 tiles 166 us, split 143; N 10924, K 2240, T 1764 59 and 55; N 11932, K 928,
-// T 4299 80 and 84.
 struct TileTimes {
   int big, big_k;     // a round of 256x256 tiles
   int full, full_k;   // a round of 128x128 tiles, two on a compute unit
