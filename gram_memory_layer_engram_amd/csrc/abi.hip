@@ -104,7 +104,7 @@ struct Span {
 };
 inline bool meet(const Span& a, const Span& b) {
   const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
-  return x && y && a.bytes > 0 && b.bytes > 0 && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+  return x && y && a.bytes && b.bytes && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
 }
 
 // Whether an output lies on an operand of a product (the tiles that come later
